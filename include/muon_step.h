@@ -273,6 +273,134 @@ int muon_step_noalloc(void* params, int param_dtype, int64_t n_param_elems, cons
                       int64_t n, float lr, float weight_decay, float beta, int nesterov,
                       int ns_steps, int gemm_mode, hipStream_t stream);
 
+/* ------------------------------------------- gradient norm, clipping, AdamW
+ *
+ * What a training step needs beside the Muon step: the norm of ALL gradients
+ * (matrices and the rest), the clipping that follows from it, and an optimizer
+ * for the parameters that Muon skips ("Non-2D parameters are skipped. Use a
+ * separate optimizer", FsdpMuon class docstring; "clip_grad" in the
+ * Megatron-Bridge #5933 commit message).  They keep no plan and allocate nothing: every call, the
+ * first one too, may be captured into a HIP graph.  Nothing returns to the
+ * host: the norm and the clipping coefficient stay in a record in device
+ * memory, which the consuming kernels read when they run.  Errors, streams and
+ * ownership as above. */
+
+/* One tensor of a list: `numel` consecutive elements (0..2^34; a list holds at
+ * most 2^36) of type MUON_DTYPE_F32 or MUON_DTYPE_BF16 in device memory,
+ * aligned to its elements only.  data may be NULL where numel is 0.  Lists are
+ * host memory read during the call. */
+typedef struct muon_tensor {
+    void* data;
+    int64_t numel;
+    int32_t dtype;
+    int32_t reserved;
+} muon_tensor_t;
+
+/* The clipping record, in DEVICE memory, 16-byte aligned, owned by the caller:
+ *   sumsq  sum of the squares of all elements, float64
+ *   norm   sqrt(sumsq), rounded to float32
+ *   coef   min(1, max_norm / (sqrt(sumsq) + 1e-6)), rounded to float32
+ * The sum is float64 from the first element on (squares of float32 are exact
+ * there), so it neither overflows nor underflows.  A NaN among the elements
+ * makes sumsq, norm and coef NaN; an infinity without a NaN gives sumsq = norm
+ * = inf and coef = 0 (NaN where max_norm is infinite too), so that clipping
+ * turns the infinite elements into NaN.  Results are deterministic; they depend
+ * on the list's lengths, order and addresses modulo 16 only. */
+typedef struct __attribute__((aligned(16))) muon_clip {
+    double sumsq;
+    float norm;
+    float coef;
+} muon_clip_t;
+
+/* Bytes of device workspace (256-byte aligned) of muon_grad_norm for this
+ * list.  It depends on the lengths alone.  Host-only. */
+int muon_clip_workspace_bytes(const muon_tensor_t* tensors, int64_t n, size_t* out_bytes);
+
+/* Global 2-norm of the listed tensors, and the clipping coefficient.
+ *   max_norm      >= 0; infinity never clips.
+ *   clip          receives the record (n == 0: sumsq = norm = 0).
+ *   tensor_norms  NULL, or device float32 [n]: the norm of every tensor.
+ *   workspace     device, >= muon_clip_workspace_bytes(); calls that share it
+ *                 (or a record) must be ordered on one stream.
+ * Tensors may overlap each other (each counts in full); the record, the norms
+ * and the workspace may not overlap anything. */
+int muon_grad_norm(const muon_tensor_t* tensors, int64_t n, float max_norm, muon_clip_t* clip,
+                   float* tensor_norms, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+
+/* norm and coef of a record from its sumsq: after the caller has summed sumsq
+ * over the ranks that hold parts of the gradient. */
+int muon_clip_finish(muon_clip_t* clip, float max_norm, hipStream_t stream);
+
+/* dst[i] = coef * src[i], in float32, rounded once to dst's type (nearest
+ * even), for every element of every tensor.  Lists have the same lengths;
+ * types may differ.  A dst may be its src (same address and type: in place,
+ * where nothing is read or written while coef is 1); apart from that no dst
+ * may overlap another dst or a src. */
+int muon_clip_grads(const muon_tensor_t* src, const muon_tensor_t* dst, int64_t n,
+                    const muon_clip_t* clip, hipStream_t stream);
+
+/* muon_step_grouped on the clipped gradient fl(coef * G), without a pass of its
+ * own: the kernel that reads G multiplies.  Results equal, bit for bit, those of
+ * muon_clip_grads into another float32 buffer followed by muon_step_grouped
+ * with it; grads itself is only read.  clip must not overlap the other buffers. */
+int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
+                      const float* grads, float* momentum, int64_t n_state_elems,
+                      const muon_matrix_desc_t* descs, int64_t n, const muon_group_t* groups,
+                      int32_t n_groups, const muon_clip_t* clip, int ns_steps, int gemm_mode,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One range of parameters of muon_adamw.
+ *   offset        first element in grads / exp_avg / exp_avg_sq; multiple of 4
+ *   numel         0..2^34 elements (2^36 in all ranges)
+ *   param_offset  first element in params (and model_copy); 16-byte aligned
+ *   group         row of the group table */
+typedef struct muon_range {
+    int64_t offset;
+    int64_t numel;
+    int64_t param_offset;
+    int32_t group;
+    int32_t reserved;
+} muon_range_t;
+
+/* One optimizer group of muon_adamw, in DEVICE memory and read by the kernels
+ * when they run, like muon_group_t.  step is the number t >= 1 of the step to be
+ * made, for the bias corrections; the caller raises it between steps.  Values
+ * are not checked. */
+typedef struct muon_adamw_group {
+    float lr;
+    float weight_decay;
+    float beta1;
+    float beta2;
+    float eps;
+    int32_t reserved;
+    int64_t step;
+} muon_adamw_group_t;
+
+/* One AdamW step on ranges of flat buffers:
+ *   g = fl(coef * G)  (coef of `clip`; g = G where clip is NULL)
+ *   m <- fl(fl(beta1*m) + fl((1-beta1)*g))
+ *   v <- fl(fl(beta2*v) + fl(fl((1-beta2)*g)*g))
+ *   W <- fl(fl(W*f) - fl(a * fl(m / fl(fl(sqrt(v)*r) + eps))))
+ *   f = fl(1 - fl(lr*wd)),  a = fl(lr / (1 - beta1^t)),  r = fl(1 / sqrt(1 - beta2^t))
+ * in float32, each operation rounded on its own; a and r are computed in
+ * float64 and rounded once.  bfloat16 weights are rounded once, to nearest
+ * even, on store.
+ *   params      device, n_param_elems of param_dtype, updated in place
+ *   model_copy  NULL, or (float32 params only) device bfloat16 laid out like
+ *               params, receives every updated weight rounded to nearest even
+ *   grads       device, n_state_elems of grad_dtype, read only
+ *   exp_avg, exp_avg_sq  device float32, n_state_elems, updated in place
+ *   groups, n_groups     DEVICE array of 1..65536 groups (8-byte aligned)
+ *   clip        NULL or a record
+ * Every buffer starts 16-byte aligned.  Buffers must not overlap one another,
+ * nor ranges each other.  Elements outside the ranges stay as they are. */
+int muon_adamw(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
+               const void* grads, int grad_dtype, float* exp_avg, float* exp_avg_sq,
+               int64_t n_state_elems, const muon_range_t* ranges, int64_t n,
+               const muon_adamw_group_t* groups, int32_t n_groups, const muon_clip_t* clip,
+               hipStream_t stream);
+
 /* Kernel timing, a profiling aid (not part of the step's semantics).
  * Between muon_profile_begin() and muon_profile_end(), every kernel the
  * library launches, from any thread, is bracketed by two HIP events recorded
@@ -282,7 +410,8 @@ int muon_step_noalloc(void* params, int param_dtype, int64_t n_param_elems, cons
  * distinct kernels, which may exceed max_entries).  Names are
  * "front", "sumsq", "norm", "cast", "apply" and "ns_<stage>_t<tile>_<type>"
  * for the Newton-Schulz products (stage a: X X^T, b: b A + c A A, x: a X + B X;
- * tile 64/128/256; type bf16/f32).  Events come from a pool the library owns;
+ * tile 64/128/256; type bf16/f32); "grad_norm", "tensor_norms", "norm_finish",
+ * "clip_finish", "clip" and "adamw" for the operators above.  Events come from a pool the library owns;
  * when timing is off the only cost is one flag test per launch. */
 typedef struct muon_kernel_time {
     char name[48];

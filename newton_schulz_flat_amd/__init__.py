@@ -16,12 +16,31 @@ Entry points (same names as the C ABI):
 ``muon_momentum``       momentum update and orthogonalization input only
 ``muon_orthogonalize``  Newton-Schulz orthogonalization (with shape scale) only
 ``muon_apply``          decoupled decay and update, scattered into slices
+``muon_step_clipped``   ``muon_step_grouped`` on the clipped gradient
+``muon_grad_norm``      global 2-norm of many tensors and the clipping coefficient
+``muon_clip_grads``     every tensor times the coefficient, in place or into others
+``muon_clip_finish``    norm and coefficient from a record's (all-reduced) sum of squares
+``muon_adamw``          AdamW on ranges of flat buffers, for the parameters Muon skips
 ``muon_workspace_bytes``      workspace for one wave
 ``muon_workspace_min_bytes``  smallest workspace (the matrices then run in waves)
 
 Descriptors are objects with ``offset, rows, cols`` and optionally
 ``param_offset`` (default ``offset``), ``shard_stride`` (0), ``n_shards`` (1)
-and ``group`` (0), or tuples in that field order.
+and ``group`` (0), or tuples in that field order.  Ranges (``muon_adamw``) are
+objects with ``offset, numel`` and optionally ``param_offset`` (default
+``offset``) and ``group`` (0), or tuples in that field order.
+
+A training step clips by the global norm without a word to the host::
+
+    clip = clip_state(device)                       # kept
+    tensors = tensor_list([*matrix_grads, *other_grads])    # kept
+    muon_grad_norm(tensors, 1.0, clip)
+    muon_step_clipped(params, grads, momentum, descs, groups, clip)
+    muon_adamw(other_params, other_grads, m, v, ranges, adamw_groups, clip=clip)
+    adamw_steps(adamw_groups).add_(1)
+
+Where ranks hold parts of the gradient, ``dist.all_reduce(clip_sumsq(clip))`` and
+``muon_clip_finish(clip, 1.0)`` come after the norm.
 """
 
 from __future__ import annotations
@@ -42,8 +61,9 @@ _MODES = {"bf16": MUON_GEMM_BF16_MFMA, "f32": MUON_GEMM_F32}
 
 #: C names of every exported entry point (mirrors include/muon_step.h).
 EXPORTS = ("muon_workspace_bytes", "muon_workspace_min_bytes", "muon_step", "muon_step_grouped",
-           "muon_step_noalloc", "muon_momentum", "muon_orthogonalize", "muon_apply",
-           "muon_profile_begin", "muon_profile_end", "muon_status_string", "muon_last_error")
+           "muon_step_noalloc", "muon_step_clipped", "muon_momentum", "muon_orthogonalize",
+           "muon_apply", "muon_clip_workspace_bytes", "muon_grad_norm", "muon_clip_finish",
+           "muon_clip_grads", "muon_adamw", "muon_profile_begin", "muon_profile_end", "muon_status_string", "muon_last_error")
 
 
 class MatrixDescC(ctypes.Structure):
@@ -52,6 +72,21 @@ class MatrixDescC(ctypes.Structure):
     _fields_ = [("offset", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("param_offset", ctypes.c_int64), ("shard_stride", ctypes.c_int64),
                 ("n_shards", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class TensorC(ctypes.Structure):
+    """``muon_tensor_t``."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RangeC(ctypes.Structure):
+    """``muon_range_t``."""
+
+    _fields_ = [("offset", ctypes.c_int64), ("numel", ctypes.c_int64),
+                ("param_offset", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class KernelTimeC(ctypes.Structure):
@@ -96,6 +131,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_momentum.argtypes = [p, p, p, i64, dp, i64, f32, i32, p]
     lib.muon_orthogonalize.argtypes = [p, p, i64, dp, i64, i32, i32, p, sz, p]
     lib.muon_apply.argtypes = [p, i32, i64, p, i64, dp, i64, f32, f32, p]
+    tp = ctypes.POINTER(TensorC)
+    lib.muon_step_clipped.argtypes = [p, i32, i64, p, p, p, i64, dp, i64, p, ctypes.c_int32, p,
+                                      i32, i32, p, sz, p]
+    lib.muon_clip_workspace_bytes.argtypes = [tp, i64, ctypes.POINTER(sz)]
+    lib.muon_grad_norm.argtypes = [tp, i64, f32, p, p, p, sz, p]
+    lib.muon_clip_finish.argtypes = [p, f32, p]
+    lib.muon_clip_grads.argtypes = [tp, tp, i64, p, p]
+    lib.muon_adamw.argtypes = [p, i32, i64, p, p, i32, p, p, i64, ctypes.POINTER(RangeC), i64, p,
+                               ctypes.c_int32, p, p]
     lib.muon_profile_begin.argtypes = []
     lib.muon_profile_end.argtypes = [ctypes.POINTER(KernelTimeC), i32, ctypes.POINTER(i32)]
     lib.muon_status_string.argtypes = [i32]
@@ -104,7 +148,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_last_error.restype = ctypes.c_char_p
     for name in ("muon_workspace_bytes", "muon_workspace_min_bytes", "muon_step",
                  "muon_step_grouped", "muon_step_noalloc", "muon_momentum", "muon_orthogonalize",
-                 "muon_apply", "muon_profile_begin", "muon_profile_end"):
+                 "muon_apply", "muon_step_clipped", "muon_clip_workspace_bytes",
+                 "muon_grad_norm", "muon_clip_finish", "muon_clip_grads", "muon_adamw",
+                 "muon_profile_begin", "muon_profile_end"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -270,6 +316,21 @@ def muon_step_grouped(params, grads, momentum, descs, groups, ns_steps: int = 5,
     uses row k of ``groups`` (a ``group_table`` on the GPU, read when the
     kernels run).  ``model_copy`` (bf16, shaped like float32 ``params``)
     receives the updated weights rounded to bfloat16."""
+    _step_grouped(params, grads, momentum, descs, groups, None, ns_steps, mode, model_copy,
+                  workspace)
+
+
+def muon_step_clipped(params, grads, momentum, descs, groups, clip, ns_steps: int = 5,
+                      mode: str = "bf16", model_copy=None, workspace=None):
+    """``muon_step_grouped`` on ``grads`` times the coefficient of ``clip`` (a
+    ``clip_state`` that ``muon_grad_norm`` filled); ``grads`` is only read."""
+    _require_clip(clip, grads.device)
+    _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, model_copy,
+                  workspace)
+
+
+def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, model_copy,
+                  workspace):
     import torch
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(grads, "grads", (torch.float32,))
@@ -287,11 +348,15 @@ def muon_step_grouped(params, grads, momentum, descs, groups, ns_steps: int = 5,
         workspace = workspace_for(descs, mode, grads.device)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    check(lib.muon_step_grouped(params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
-                                momentum.data_ptr(), grads.numel(), descs_array(descs),
-                                _count(descs), groups.data_ptr(), groups.shape[0], int(ns_steps),
-                                _mode(mode), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(grads)))
+    head = (params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
+            momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
+            groups.data_ptr(), groups.shape[0])
+    tail = (int(ns_steps), _mode(mode), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(grads))
+    if clip is None:
+        check(lib.muon_step_grouped(*head, *tail))
+    else:
+        check(lib.muon_step_clipped(*head, clip.data_ptr(), *tail))
 
 
 def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = True):
@@ -328,6 +393,244 @@ def muon_apply(params, updates, descs, lr: float, weight_decay: float):
     check(lib.muon_apply(params.data_ptr(), dt, params.numel(), updates.data_ptr(),
                          updates.numel(), descs_array(descs), _count(descs), lr, weight_decay,
                          _stream(updates)))
+
+
+def clip_state(device):
+    """A clipping record on ``device`` (``muon_clip_t`` as two float64): zero norm,
+    zero coefficient until ``muon_grad_norm`` fills it."""
+    import torch
+    return torch.zeros(2, dtype=torch.float64, device=device)
+
+
+def clip_sumsq(clip):
+    """The record's sum of squares: a float64 view of shape (1,), to be all-reduced."""
+    return clip[:1]
+
+
+def clip_norm(clip):
+    """The record's norm: a float32 view without dimensions."""
+    import torch
+    return clip.view(torch.float32)[2]
+
+
+def clip_coef(clip):
+    """The record's clipping coefficient: a float32 view without dimensions."""
+    import torch
+    return clip.view(torch.float32)[3]
+
+
+def _require_clip(clip, device):
+    import torch
+    _require(clip, "clip", (torch.float64,))
+    if clip.numel() != 2:
+        raise ValueError("clip must be a clip_state")
+    if clip.device != device:
+        raise ValueError(f"clip is on {clip.device}, the tensors are on {device}")
+
+
+class TensorList:
+    """Tensors as a ``muon_tensor_t`` array.  Keeps the tensors; their addresses
+    are taken once, so a tensor whose storage is replaced needs a new list."""
+
+    def __init__(self, tensors: Iterable):
+        import torch
+        self.tensors = list(tensors)
+        self.array = (TensorC * max(1, len(self.tensors)))()
+        self.device = None
+        for k, t in enumerate(self.tensors):
+            _require(t, f"tensors[{k}]", (torch.float32, torch.bfloat16))
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"tensors[{k}] is on {t.device}, the first one on {self.device}")
+            bf16 = t.dtype == torch.bfloat16
+            self.array[k] = TensorC(t.data_ptr(), t.numel(),
+                                    MUON_DTYPE_BF16 if bf16 else MUON_DTYPE_F32, 0)
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
+def tensor_list(tensors) -> TensorList:
+    """``tensors`` as a list that the norm and clipping calls take as it is: a
+    program that keeps its gradient buffers makes it once."""
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def _on(device):
+    """Launches go to the current device: a guard where that is another one."""
+    import contextlib
+
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def muon_clip_workspace_bytes(tensors) -> int:
+    """Workspace bytes of ``muon_grad_norm`` for these tensors."""
+    tl = tensor_list(tensors)
+    out = ctypes.c_size_t(0)
+    check(load_library().muon_clip_workspace_bytes(tl.array, len(tl), ctypes.byref(out)))
+    return out.value
+
+
+#: Default workspaces of muon_grad_norm, one per (device, stream).
+_clip_workspaces: dict = {}
+
+
+def _clip_workspace_for(tl: TensorList, device):
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("pass an explicit workspace to calls made under graph capture")
+    stream = torch.cuda.current_stream(device)
+    key = (device, stream.cuda_stream)
+    need = muon_clip_workspace_bytes(tl)
+    ws = _clip_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        _clip_workspaces.pop(key, None)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _clip_workspaces[key] = ws
+    return ws
+
+
+def muon_grad_norm(tensors, max_norm: float, clip, tensor_norms=None, workspace=None):
+    """Global 2-norm of ``tensors`` (f32 or bf16, any mix) and the coefficient
+    ``min(1, max_norm / (norm + 1e-6))``, written to ``clip`` (a ``clip_state``)
+    on its device's current stream; nothing returns to the host.
+
+    ``tensor_norms``: float32, one element per tensor, receives their norms.
+    ``workspace``: a uint8 GPU tensor of ``muon_clip_workspace_bytes`` (default: a
+    cached one per device and stream; give one under graph capture)."""
+    import torch
+    tl = tensor_list(tensors)
+    _require_clip(clip, tl.device if tl.device is not None else clip.device)
+    norms_ptr = None
+    if tensor_norms is not None:
+        _require(tensor_norms, "tensor_norms", (torch.float32,))
+        if tensor_norms.numel() != len(tl) or tensor_norms.device != clip.device:
+            raise ValueError("tensor_norms must have one element per tensor, on their device")
+        norms_ptr = tensor_norms.data_ptr()
+    if workspace is None:
+        workspace = _clip_workspace_for(tl, clip.device)
+    else:
+        _require(workspace, "workspace", (torch.uint8,))
+        if workspace.device != clip.device:
+            raise ValueError("workspace is on another device than the tensors")
+    with _on(clip.device):
+        check(load_library().muon_grad_norm(tl.array, len(tl), max_norm, clip.data_ptr(),
+                                            norms_ptr, workspace.data_ptr(), workspace.numel(),
+                                            _stream(clip)))
+
+
+def muon_clip_finish(clip, max_norm: float):
+    """Norm and coefficient of ``clip`` from its ``clip_sumsq``, as it stands after
+    the sums of several ranks (or calls) were added up."""
+    _require_clip(clip, clip.device)
+    with _on(clip.device):
+        check(load_library().muon_clip_finish(clip.data_ptr(), max_norm, _stream(clip)))
+
+
+def muon_clip_grads(tensors, clip, out=None):
+    """Every tensor times the coefficient of ``clip``, in place, or into the
+    tensors of ``out`` (same lengths; f32 or bf16, rounded once)."""
+    src = tensor_list(tensors)
+    dst = src if out is None else tensor_list(out)
+    if len(src) != len(dst):
+        raise ValueError(f"{len(src)} tensors, but {len(dst)} in out")
+    if len(src) == 0:
+        return
+    _require_clip(clip, src.device)
+    if dst.device != src.device:
+        raise ValueError("out is on another device than the tensors")
+    with _on(clip.device):
+        check(load_library().muon_clip_grads(src.array, dst.array, len(src), clip.data_ptr(),
+                                             _stream(clip)))
+
+
+def ranges_array(ranges) -> ctypes.Array:
+    """Ranges as a ``muon_range_t`` array (which ``muon_adamw`` takes as it is)."""
+    if isinstance(ranges, ctypes.Array) and ranges._type_ is RangeC:
+        return ranges
+    items = list(ranges)
+    arr = (RangeC * len(items))()
+    for k, r in enumerate(items):
+        if isinstance(r, (tuple, list)):
+            vals = list(r) + [None] * (4 - len(r))
+            off, numel, poff, group = vals[:4]
+        else:
+            off, numel = r.offset, r.numel
+            poff = getattr(r, "param_offset", None)
+            group = getattr(r, "group", None)
+        arr[k] = RangeC(int(off), int(numel), int(off if poff is None else poff), int(group or 0),
+                        0)
+    return arr
+
+
+def adamw_group_table(groups, device):
+    """A device table of optimizer groups for ``muon_adamw``: rows of ``(lr,
+    weight_decay, beta1, beta2, eps)`` or ``(..., step)``, stored as
+    ``muon_adamw_group_t`` in an int64 tensor of shape (len(groups), 4).  ``step``
+    is the number of the next step (default 1); see ``adamw_steps``."""
+    import numpy as np
+    import torch
+    rows = np.zeros((len(groups), 8), dtype=np.int32)
+    steps = rows.view(np.int64)
+    for k, row in enumerate(groups):
+        if len(row) not in (5, 6):
+            raise ValueError("a group is (lr, weight_decay, beta1, beta2, eps[, step])")
+        rows[k, :5] = np.array(row[:5], dtype=np.float32).view(np.int32)
+        steps[k, 3] = int(row[5]) if len(row) == 6 else 1
+    return torch.from_numpy(rows.view(np.int64)).to(device)
+
+
+def adamw_steps(groups):
+    """The step numbers of an ``adamw_group_table``: an int64 view; ``.add_(1)``
+    between steps (it may be captured into the graph with them)."""
+    return groups[:, 3]
+
+
+def muon_adamw(params, grads, exp_avg, exp_avg_sq, ranges, groups, clip=None, model_copy=None):
+    """One AdamW step in place on ``params`` (f32 or bf16), ``exp_avg`` and
+    ``exp_avg_sq`` (f32) over ``ranges`` of the flat buffers; ``grads`` (f32 or bf16)
+    is multiplied by the coefficient of ``clip`` (a ``clip_state``) as it is read.
+    ``groups``: an ``adamw_group_table``, read when the kernels run.
+    ``model_copy`` (bf16, shaped like float32 ``params``) receives the updated
+    weights rounded to bfloat16."""
+    import torch
+    both = (torch.float32, torch.bfloat16)
+    _require(params, "params", both)
+    _require(grads, "grads", both)
+    _require(exp_avg, "exp_avg", (torch.float32,))
+    _require(exp_avg_sq, "exp_avg_sq", (torch.float32,))
+    _require(groups, "groups", (torch.int64,))
+    if groups.dim() != 2 or groups.shape[1] != 4:
+        raise ValueError("groups must be an adamw_group_table of shape (n_groups, 4)")
+    if not grads.numel() == exp_avg.numel() == exp_avg_sq.numel():
+        raise ValueError("grads, exp_avg and exp_avg_sq must have as many elements as each other")
+    copy_ptr = clip_ptr = None
+    if model_copy is not None:
+        _require(model_copy, "model_copy", (torch.bfloat16,))
+        if model_copy.numel() != params.numel():
+            raise ValueError("model_copy must have as many elements as params")
+        copy_ptr = model_copy.data_ptr()
+    if clip is not None:
+        _require_clip(clip, grads.device)
+        clip_ptr = clip.data_ptr()
+    for t, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"),
+                    (groups, "groups"), (model_copy, "model_copy")):
+        if t is not None and t.device != grads.device:
+            raise ValueError(f"{name} is on {t.device}, grads on {grads.device}")
+    arr = ranges_array(ranges)
+    pdt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
+    gdt = MUON_DTYPE_BF16 if grads.dtype == torch.bfloat16 else MUON_DTYPE_F32
+    with _on(grads.device):
+        check(load_library().muon_adamw(params.data_ptr(), pdt, params.numel(), copy_ptr,
+                                        grads.data_ptr(), gdt, exp_avg.data_ptr(),
+                                        exp_avg_sq.data_ptr(), grads.numel(), arr, len(arr),
+                                        groups.data_ptr(), groups.shape[0], clip_ptr,
+                                        _stream(grads)))
 
 
 def muon_profile_begin() -> None:

@@ -30,9 +30,12 @@ SOURCES = [
     "k_norm_cast.hip",
     "k_ns_gemm.hip",
     "muon_noalloc.hip",
+    "muon_clip.cpp",
+    "k_clip.hip",
+    "k_adamw.hip",
 ]
 # Sources whose arithmetic must round every operation separately.
-NO_CONTRACT = {"k_elementwise.hip", "k_norm_cast.hip"}
+NO_CONTRACT = {"k_elementwise.hip", "k_norm_cast.hip", "k_clip.hip", "k_adamw.hip"}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -69,7 +69,7 @@ __device__ __forceinline__ void store2_stream(uint2* p, uint2 v) {
 // One matrix's optimizer scalars; decay = fl(1 - fl(lr * wd)), the same two
 // roundings as on the host.
 struct HyperVals {
-    float lr, decay, beta;
+    float lr, decay, beta, coef;
     int nesterov;
 };
 __device__ __forceinline__ HyperVals hyper_for(const Hyper& h, const MatInfo& mt) {
@@ -84,6 +84,7 @@ __device__ __forceinline__ HyperVals hyper_for(const Hyper& h, const MatInfo& mt
     }
     const float lrwd = v.lr * wd;
     v.decay = 1.0f - lrwd;
+    v.coef = h.clip != nullptr ? h.clip->coef : 1.0f;
     return v;
 }
 

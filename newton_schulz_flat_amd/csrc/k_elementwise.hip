@@ -37,7 +37,8 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
     return t;
 }
 
-// kMode 0: M <- beta M + G, U <- G + beta M (or M); partial sums of U^2.
+// kMode 0: M <- beta M + G, U <- G + beta M (or M); partial sums of U^2.  G is
+// the gradient times the clipping coefficient (1 without clipping).
 // kMode 1: partial sums of U^2 only (U given).
 // U element e of a matrix at offset off lives at u[e] (grads layout) or, with
 // u_compact, at u[e - off + u_off] (the workspace's compact U region).
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(kFrontThreads) void front_kernel(
     const int blk = chunk0 + int(blockIdx.x);
     const int mi = owner_of(prefix, n, blk);
     const HyperVals hv = hyper_for(h, mats[mi]);
-    const float beta = hv.beta;
+    const float beta = hv.beta, coef = hv.coef;
     const int nesterov = hv.nesterov;
     const int64_t off = mats[mi].off;
     const int64_t end = off + mats[mi].numel;
@@ -65,8 +66,9 @@ __global__ __launch_bounds__(kFrontThreads) void front_kernel(
         if (e + kEwVec <= end) {
             float4 uv;
             if (kMode == 0) {
-                const float4 gv = load4_stream(g + e);
+                float4 gv = load4_stream(g + e);
                 const float4 mv = load4_stream(m + e);
+                gv.x = coef * gv.x, gv.y = coef * gv.y, gv.z = coef * gv.z, gv.w = coef * gv.w;
                 float4 m1;
                 m1.x = beta * mv.x + gv.x;
                 m1.y = beta * mv.y + gv.y;
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(kFrontThreads) void front_kernel(
             for (int64_t k = e; k < end && k < e + kEwVec; ++k) {
                 float uk;
                 if (kMode == 0) {
-                    const float gk = g[k];
+                    const float gk = coef * g[k];
                     const float m1 = beta * m[k] + gk;
                     m[k] = m1;
                     uk = nesterov ? beta * m1 + gk : m1;

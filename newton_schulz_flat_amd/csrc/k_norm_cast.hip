@@ -7,7 +7,8 @@
 //
 // front_cast_kernel: one workgroup per 4096 elements of the padded
 // NS-orientation matrix (as many workgroups as cast_kernel has 64 x 64 tiles).
-// It reads the matching elements of G and M (or of U) along U's rows,
+// It reads the matching elements of G and M (or of U) along U's rows
+// (G times the clipping coefficient, which is 1 outside muon_step_clipped),
 // computes M <- fl(fl(beta M) + G) (stored) and U = fl(fl(beta M) + G) (or M)
 // in float32 exactly as the elementwise front kernel does, stores U rounded to
 // the Newton-Schulz type -- not yet divided by its norm: the first iteration
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(256) void front_cast_kernel(const MatInfo* __restri
     const bool tall = mt.tall != 0;
     const bool vec = (mt.C & 3) == 0;  // rows start 16-byte aligned
     const HyperVals hv = hyper_for(h, mt);
-    const float beta = hv.beta;
+    const float beta = hv.beta, coef = hv.coef;
     const int nesterov = hv.nesterov;
     // Each thread first loads all of its G and M (or U) groups and only then
     // stores: loads and stores share the vector memory counter, and with both
@@ -187,8 +188,9 @@ __global__ __launch_bounds__(256) void front_cast_kernel(const MatInfo* __restri
         float m1[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            m1[q] = beta * mv[q] + gv[q];
-            uv[q] = nesterov ? beta * m1[q] + gv[q] : m1[q];
+            const float gc = coef * gv[q];
+            m1[q] = beta * mv[q] + gc;
+            uv[q] = nesterov ? beta * m1[q] + gc : m1[q];
         }
         if (vec && gc + 3 < mt.C) {
             store4_stream(m + e, make_float4(m1[0], m1[1], m1[2], m1[3]));
@@ -241,8 +243,9 @@ __global__ __launch_bounds__(256) void front_cast_kernel(const MatInfo* __restri
         float m1[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            m1[q] = beta * mv[q] + gv[q];
-            uv[q] = nesterov ? beta * m1[q] + gv[q] : m1[q];
+            const float gc = coef * gv[q];
+            m1[q] = beta * mv[q] + gc;
+            uv[q] = nesterov ? beta * m1[q] + gc : m1[q];
         }
         const int64_t e = mt.off + a;
         if (a >= lo && a + 4 <= hi) {

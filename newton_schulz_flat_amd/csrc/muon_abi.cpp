@@ -73,6 +73,16 @@ int check_null(const void* p, const char* name, Status* st) {
     return MUON_OK;
 }
 
+int check_groups(const muon_group_t* groups, int32_t n_groups, int64_t n, Status* st) {
+    if (n_groups < 1 || n_groups > muon::kMaxGroups) {
+        st->code = MUON_ERR_BAD_ARG;
+        snprintf(st->msg, sizeof(st->msg), "n_groups = %d is outside [1, %d]", n_groups,
+                 muon::kMaxGroups);
+        return st->code;
+    }
+    return n > 0 ? check_null(groups, "groups", st) : int(MUON_OK);
+}
+
 // The workspace must hold the largest single-matrix wave (need_min).  When it
 // holds the whole set (need_full), everything runs in one wave (*capacity = 0);
 // otherwise the set runs in waves of at most `have` bytes each.
@@ -144,14 +154,15 @@ int check_step_args(Status& st, void* params, int param_dtype, int64_t n_param_e
         snprintf(st.msg, sizeof(st.msg), "model_copy is not 16-byte aligned");
         return st.code;
     }
-    const Range ranges[6] = {
+    const Range ranges[7] = {
         {params, param_bytes(param_dtype, n_param_elems), "params"},
         {grads, size_t(n_state_elems) * 4, "grads"},
         {momentum, size_t(n_state_elems) * 4, "momentum"},
         {h.groups, h.groups ? size_t(n_groups) * sizeof(muon_group_t) : 0, "groups"},
         {model_copy, model_copy ? size_t(n_param_elems) * 2 : 0, "model_copy"},
+        {h.clip, h.clip ? sizeof(muon_clip_t) : 0, "clip"},
         extra ? *extra : Range{nullptr, 0, "unused"}};
-    return check_no_alias(ranges, 6, &st);
+    return check_no_alias(ranges, 7, &st);
 }
 
 int check_step_scalars(Status& st, float lr, float weight_decay, float beta, int nesterov) {
@@ -276,14 +287,27 @@ int muon_step_grouped(void* params, int param_dtype, int64_t n_param_elems, void
                       int32_t n_groups, int ns_steps, int gemm_mode, void* workspace,
                       size_t workspace_bytes, hipStream_t stream) {
     Status st{MUON_OK, ""};
-    if (n_groups < 1 || n_groups > muon::kMaxGroups) {
-        st.code = MUON_ERR_BAD_ARG;
-        snprintf(st.msg, sizeof(st.msg), "n_groups = %d is outside [1, %d]", n_groups,
-                 muon::kMaxGroups);
+    TRY(check_groups(groups, n_groups, n, &st));
+    const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0};
+    return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
+                    n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
+                    workspace_bytes, stream);
+}
+
+int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
+                      const float* grads, float* momentum, int64_t n_state_elems,
+                      const muon_matrix_desc_t* descs, int64_t n, const muon_group_t* groups,
+                      int32_t n_groups, const muon_clip_t* clip, int ns_steps, int gemm_mode,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    Status st{MUON_OK, ""};
+    TRY(check_groups(groups, n_groups, n, &st));
+    if (n > 0) TRY(check_null(clip, "clip", &st));
+    if (reinterpret_cast<uintptr_t>(clip) % alignof(muon_clip_t) != 0) {
+        st.code = MUON_ERR_MISALIGNED;
+        snprintf(st.msg, sizeof(st.msg), "clip is not %zu-byte aligned", alignof(muon_clip_t));
         return finish(st);
     }
-    if (n > 0) TRY(check_null(groups, "groups", &st));
-    const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0};
+    const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0, clip};
     return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
                     n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
                     workspace_bytes, stream);

@@ -220,11 +220,13 @@ class LaunchTimer {
 
 // Optimizer hyperparameters of a launch: one set for every matrix
 // (groups == nullptr), or per matrix groups[MatInfo::group], read from device
-// memory by the kernels.
+// memory by the kernels.  The gradient is multiplied by clip->coef as it is
+// read (muon_step_clipped), or by 1 where clip is null.
 struct Hyper {
     const muon_group_t* groups;
     float lr, weight_decay, beta;
     int nesterov;
+    const muon_clip_t* clip = nullptr;
 };
 
 
