@@ -304,8 +304,9 @@ typedef struct muon_tensor {
  * there), so it neither overflows nor underflows.  A NaN among the elements
  * makes sumsq, norm and coef NaN; an infinity without a NaN gives sumsq = norm
  * = inf and coef = 0 (NaN where max_norm is infinite too), so that clipping
- * turns the infinite elements into NaN.  Results are deterministic; they depend
- * on the list's lengths, order and addresses modulo 16 only. */
+ * turns the infinite elements into NaN.  The same call gives the same bits; the
+ * last bits of sumsq depend on the order of summation, that is on the list's
+ * lengths, order and addresses and on whether tensor_norms are asked for. */
 typedef struct __attribute__((aligned(16))) muon_clip {
     double sumsq;
     float norm;

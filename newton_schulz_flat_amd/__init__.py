@@ -202,6 +202,8 @@ def _stream(t):
 
 def _require(t, name, dtypes):
     import torch
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -356,7 +358,7 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
     if clip is None:
         check(lib.muon_step_grouped(*head, *tail))
     else:
-        check(lib.muon_step_clipped(*head, clip.data_ptr(), *tail))
+        check(lib.muon_step_clipped(*head, clip.record.data_ptr(), *tail))
 
 
 def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = True):
@@ -395,35 +397,45 @@ def muon_apply(params, updates, descs, lr: float, weight_decay: float):
                          _stream(updates)))
 
 
-def clip_state(device):
-    """A clipping record on ``device`` (``muon_clip_t`` as two float64): zero norm,
-    zero coefficient until ``muon_grad_norm`` fills it."""
-    import torch
-    return torch.zeros(2, dtype=torch.float64, device=device)
+class ClipState:
+    """A clipping record (``muon_clip_t``) in device memory: ``record``, two float64,
+    and views of its fields: ``sumsq`` (float64, shape (1,), to be all-reduced),
+    ``norm`` and ``coef`` (float32, without dimensions)."""
+
+    def __init__(self, device):
+        import torch
+        self.record = torch.zeros(2, dtype=torch.float64, device=device)
+        self.sumsq = self.record[:1]
+        self.norm = self.record.view(torch.float32)[2]
+        self.coef = self.record.view(torch.float32)[3]
+        self.device = self.record.device
 
 
-def clip_sumsq(clip):
+def clip_state(device) -> ClipState:
+    """A clipping record on ``device``: zero until ``muon_grad_norm`` fills it."""
+    return ClipState(device)
+
+
+def clip_sumsq(clip: ClipState):
     """The record's sum of squares: a float64 view of shape (1,), to be all-reduced."""
-    return clip[:1]
+    return clip.sumsq
 
 
-def clip_norm(clip):
+def clip_norm(clip: ClipState):
     """The record's norm: a float32 view without dimensions."""
-    import torch
-    return clip.view(torch.float32)[2]
+    return clip.norm
 
 
-def clip_coef(clip):
+def clip_coef(clip: ClipState):
     """The record's clipping coefficient: a float32 view without dimensions."""
-    import torch
-    return clip.view(torch.float32)[3]
+    return clip.coef
 
 
 def _require_clip(clip, device):
-    import torch
-    _require(clip, "clip", (torch.float64,))
-    if clip.numel() != 2:
-        raise ValueError("clip must be a clip_state")
+    if not isinstance(clip, ClipState):
+        raise TypeError("clip must be a clip_state")
+    if not clip.record.is_cuda:
+        raise ValueError("clip must be on a GPU (no CPU path exists)")
     if clip.device != device:
         raise ValueError(f"clip is on {clip.device}, the tensors are on {device}")
 
@@ -437,6 +449,7 @@ class TensorList:
         self.tensors = list(tensors)
         self.array = (TensorC * max(1, len(self.tensors)))()
         self.device = None
+        self.workspace_bytes = None
         for k, t in enumerate(self.tensors):
             _require(t, f"tensors[{k}]", (torch.float32, torch.bfloat16))
             if self.device is None:
@@ -457,22 +470,35 @@ def tensor_list(tensors) -> TensorList:
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
 
 
-def _on(device):
-    """Launches go to the current device: a guard where that is another one."""
-    import contextlib
-
+def _launch(index: int, call, *args) -> None:
+    """``call(*args, stream)`` on the current stream of GPU ``index``.  Launches go to the
+    current device, which another one than ``index`` gives way for the call."""
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            check(call(*args, _current_stream(index)))
+    else:
+        check(call(*args, _current_stream(index)))
+
+
+def _current_stream(index: int) -> int:
+    """Handle of the current stream, without the stream object that
+    ``torch.cuda.current_stream`` makes around it (1 us a call)."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def muon_clip_workspace_bytes(tensors) -> int:
     """Workspace bytes of ``muon_grad_norm`` for these tensors."""
     tl = tensor_list(tensors)
-    out = ctypes.c_size_t(0)
-    check(load_library().muon_clip_workspace_bytes(tl.array, len(tl), ctypes.byref(out)))
-    return out.value
+    if tl.workspace_bytes is None:
+        out = ctypes.c_size_t(0)
+        check(load_library().muon_clip_workspace_bytes(tl.array, len(tl), ctypes.byref(out)))
+        tl.workspace_bytes = out.value
+    return tl.workspace_bytes
 
 
 #: Default workspaces of muon_grad_norm, one per (device, stream).
@@ -518,18 +544,15 @@ def muon_grad_norm(tensors, max_norm: float, clip, tensor_norms=None, workspace=
         _require(workspace, "workspace", (torch.uint8,))
         if workspace.device != clip.device:
             raise ValueError("workspace is on another device than the tensors")
-    with _on(clip.device):
-        check(load_library().muon_grad_norm(tl.array, len(tl), max_norm, clip.data_ptr(),
-                                            norms_ptr, workspace.data_ptr(), workspace.numel(),
-                                            _stream(clip)))
+    _launch(clip.device.index, load_library().muon_grad_norm, tl.array, len(tl), max_norm,
+            clip.record.data_ptr(), norms_ptr, workspace.data_ptr(), workspace.numel())
 
 
 def muon_clip_finish(clip, max_norm: float):
     """Norm and coefficient of ``clip`` from its ``clip_sumsq``, as it stands after
     the sums of several ranks (or calls) were added up."""
     _require_clip(clip, clip.device)
-    with _on(clip.device):
-        check(load_library().muon_clip_finish(clip.data_ptr(), max_norm, _stream(clip)))
+    _launch(clip.device.index, load_library().muon_clip_finish, clip.record.data_ptr(), max_norm)
 
 
 def muon_clip_grads(tensors, clip, out=None):
@@ -544,9 +567,8 @@ def muon_clip_grads(tensors, clip, out=None):
     _require_clip(clip, src.device)
     if dst.device != src.device:
         raise ValueError("out is on another device than the tensors")
-    with _on(clip.device):
-        check(load_library().muon_clip_grads(src.array, dst.array, len(src), clip.data_ptr(),
-                                             _stream(clip)))
+    _launch(clip.device.index, load_library().muon_clip_grads, src.array, dst.array, len(src),
+            clip.record.data_ptr())
 
 
 def ranges_array(ranges) -> ctypes.Array:
@@ -617,20 +639,18 @@ def muon_adamw(params, grads, exp_avg, exp_avg_sq, ranges, groups, clip=None, mo
         copy_ptr = model_copy.data_ptr()
     if clip is not None:
         _require_clip(clip, grads.device)
-        clip_ptr = clip.data_ptr()
+        clip_ptr = clip.record.data_ptr()
+    at = grads.get_device()
     for t, name in ((params, "params"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"),
                     (groups, "groups"), (model_copy, "model_copy")):
-        if t is not None and t.device != grads.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name} is on {t.device}, grads on {grads.device}")
     arr = ranges_array(ranges)
     pdt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     gdt = MUON_DTYPE_BF16 if grads.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    with _on(grads.device):
-        check(load_library().muon_adamw(params.data_ptr(), pdt, params.numel(), copy_ptr,
-                                        grads.data_ptr(), gdt, exp_avg.data_ptr(),
-                                        exp_avg_sq.data_ptr(), grads.numel(), arr, len(arr),
-                                        groups.data_ptr(), groups.shape[0], clip_ptr,
-                                        _stream(grads)))
+    _launch(at, load_library().muon_adamw, params.data_ptr(), pdt, params.numel(), copy_ptr,
+            grads.data_ptr(), gdt, exp_avg.data_ptr(), exp_avg_sq.data_ptr(), grads.numel(), arr,
+            len(arr), groups.data_ptr(), groups.shape[0], clip_ptr)
 
 
 def muon_profile_begin() -> None:

@@ -15,17 +15,18 @@
 
 namespace muon {
 
-// Elements of one unit of work.  A tensor of numel elements is cut into
-// max(1, ceil(numel / kClipUnit)) units (its last one short); units of a
-// launch's tensors are numbered through in list order.
-constexpr int64_t kClipUnit = 8192;
+// Elements of one unit of work of the norm and of the clipping kernel.  A tensor
+// of numel elements is cut into max(1, ceil(numel / unit)) units (its last one
+// short); units of a launch's tensors are numbered through in list order.
+constexpr int64_t kNormUnit = 8192;
+constexpr int64_t kScaleUnit = 1024;
 // Workgroups of one launch of the norm kernel, at most: each takes a
 // contiguous run of units, so that it leaves one partial sum for each tensor
 // it meets and the partials of a launch number at most workgroups + tensors.
-constexpr int kNormGroups = 2048;
+constexpr int kNormGroups = 1024;
 
-inline int64_t clip_units(int64_t numel) {
-    return std::max<int64_t>(1, (numel + kClipUnit - 1) / kClipUnit);
+inline int64_t units_of(int64_t numel, int64_t unit) {
+    return std::max<int64_t>(1, (numel + unit - 1) / unit);
 }
 
 // A tensor's length, type(s) and first unit in one word: bits 0-34 numel
@@ -36,7 +37,7 @@ inline uint64_t clip_meta(int64_t numel, int src_bf16, int dst_bf16, int64_t uni
     return uint64_t(numel) | uint64_t(src_bf16) << 35 | uint64_t(dst_bf16) << 36 |
            uint64_t(unit) << 37;
 }
-static_assert((kMaxSetNumel / kClipUnit + 256) < (int64_t(1) << 27), "unit number");
+static_assert((kMaxSetNumel / kScaleUnit + 256) < (int64_t(1) << 27), "unit number");
 
 constexpr int kNormTensors = 248;
 struct NormArgs {
@@ -62,12 +63,13 @@ struct ClipArgs {
 static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments");
 
 // Elements of one unit of the AdamW kernel.
-constexpr int64_t kAdamwUnit = 2048;
+constexpr int64_t kAdamwUnit = 256;
 constexpr int kAdamwRanges = 144;
+static_assert(kMaxSetNumel / kAdamwUnit + kAdamwRanges < (int64_t(1) << 29), "unit number");
 struct AdamwArgs {
     int64_t off[kAdamwRanges];   // first element in grads / exp_avg / exp_avg_sq
     int64_t poff[kAdamwRanges];  // first element in params / model_copy
-    uint64_t meta[kAdamwRanges];  // bits 0-35 numel (<= 2^34), bits 36-63 the first unit
+    uint64_t meta[kAdamwRanges];  // bits 0-34 numel (<= 2^34), bits 35-63 the first unit
     uint16_t group[kAdamwRanges];
     void* params;
     uint16_t* copy;
@@ -81,7 +83,9 @@ struct AdamwArgs {
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 
-// Slots of partial sums that a list of tensors takes over all its launches.
+// Slots of partial sums that a list of tensors takes over all its launches, at
+// most: as many launches as its length asks for, each with all the workgroups
+// that its units could fill.
 int64_t norm_slots(const muon_tensor_t* t, int64_t n);
 // Sums of squares of the listed tensors into `slots`, then the record (and
 // with tensor_norms every tensor's own norm).

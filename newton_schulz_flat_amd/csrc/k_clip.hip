@@ -21,13 +21,33 @@ namespace muon {
 
 namespace {
 
+// The norm: 1024 workgroups of 256 threads, 8 vectors of 16 bytes in flight per
+// thread.  7 G float32 elements 3.99 ms (7.0 TB/s), 218 M bfloat16 72 us.  Of 512 to
+// 16384 workgroups, 128 to 1024 threads and 2 to 8 vectors the ones near this lie
+// within 1%; half the vectors with double the workgroups 1.5% more, 2 vectors
+// 5% more, 8192 workgroups (more partials, less of each tensor) 3% more.  Plain
+// instead of nontemporal loads: 6.2 TB/s.
 constexpr int kThreads = 256;
+constexpr int kFlight = 8;
 constexpr int kWaves = kThreads / 64;
+// One workgroup of this size reads up to kSoloUnits units of kSoloUnit elements by
+// itself and saves the second launch.  Time of a call among others, alone in
+// brackets, one workgroup against two launches: 1000 elements 5.7 (16.7) against
+// 8.5 us (21), 64 Ki 5.8 (18.2) against 8.6 (21), 64 tensors of 1024 6.1 (18.4)
+// against 8.9 (22); at 128 Ki float32 they meet (8.0 and 8.5), at 256 Ki one
+// workgroup takes 13.4.  Units of 512 or 1024 elements: 9.5 and 6.4 us at 64 Ki.
+constexpr int kSoloThreads = 1024;
+constexpr int64_t kSoloUnit = 2048;
+constexpr int kSoloUnits = 48;
+// Clipping: 128 threads, 2 vectors of 4 elements in flight per thread.  2.1 G float32
+// elements into another buffer 2.75 ms (6.2 TB/s); 64 threads x 2 3.38 ms, 128 x 4
+// 3.00, 256 x 2 2.84.
+constexpr int kScaleThreads = 128;
 
 typedef uint32_t u32x4_stream __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ int64_t meta_numel(uint64_t m) { return int64_t(m & ((uint64_t(1) << 35) - 1)); }
-__device__ __forceinline__ int meta_src(uint64_t m) { return int(m >> 35) & 1; }
+__host__ __device__ __forceinline__ int meta_src(uint64_t m) { return int(m >> 35) & 1; }
 __device__ __forceinline__ int meta_dst(uint64_t m) { return int(m >> 36) & 1; }
 __device__ __forceinline__ int meta_unit(uint64_t m) { return int(m >> 37); }
 
@@ -45,8 +65,9 @@ __device__ __forceinline__ int tensor_of(const uint64_t* meta, int n, int u) {
     return lo;
 }
 
-// Sum over the workgroup, in a fixed order; thread 0 has it.  The barriers
-// make `lds` free again on return.
+// Sum over the workgroup, in a fixed order, for every thread.  The barriers make
+// `lds` free again on return.
+template <int kWaves>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
@@ -81,11 +102,12 @@ __device__ __forceinline__ void add_vector(u32x4_stream q, const uint16_t*, doub
     }
 }
 
-// This thread's share of the sum of squares of p[begin, end): elements before
-// the first and behind the last 16-byte boundary one by one, whole vectors
-// between them.
-template <typename T>
-__device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t begin, int64_t end) {
+// Share of thread `me` of kStep in the sum of squares of p[begin, end): elements
+// before the first and behind the last 16-byte boundary one by one, whole
+// vectors between them.
+template <int kStep, int kFlight, typename T>
+__device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t begin, int64_t end,
+                                              int me) {
     constexpr int V = 16 / sizeof(T);
     const T* first = p + begin;
     const int64_t count = end - begin;
@@ -94,17 +116,17 @@ __device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t b
     const int64_t nvec = (count - head) / V;
     double acc[4] = {0., 0., 0., 0.};
     const u32x4_stream* v = reinterpret_cast<const u32x4_stream*>(first + head);
-    int64_t i = threadIdx.x;
-    for (; i + 3 * kThreads < nvec; i += 4 * kThreads) {
-        u32x4_stream q[4];
+    int64_t i = me;
+    for (; i + (kFlight - 1) * kStep < nvec; i += kFlight * kStep) {
+        u32x4_stream q[kFlight];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = __builtin_nontemporal_load(v + i + k * kThreads);
+        for (int k = 0; k < kFlight; ++k) q[k] = __builtin_nontemporal_load(v + i + k * kStep);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add_vector(q[k], p, acc);
+        for (int k = 0; k < kFlight; ++k) add_vector(q[k], p, acc);
     }
-    for (; i < nvec; i += kThreads) add_vector(__builtin_nontemporal_load(v + i), p, acc);
-    if (int64_t(threadIdx.x) < head) acc[0] = square_add(acc[0], element(first + threadIdx.x));
-    const int64_t tail = head + nvec * V + threadIdx.x;
+    for (; i < nvec; i += kStep) add_vector(__builtin_nontemporal_load(v + i), p, acc);
+    if (me < head) acc[0] = square_add(acc[0], element(first + me));
+    const int64_t tail = head + nvec * V + me;
     if (tail < count) acc[1] = square_add(acc[1], element(first + tail));
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
@@ -125,16 +147,18 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const NormArgs a) {
         const int t_end = t + 1 < a.n ? meta_unit(a.meta[t + 1]) : a.units;
         const int stop = min(t_end, u_end);
         const int64_t numel = meta_numel(meta);
-        const int64_t begin = int64_t(u - t_begin) * kClipUnit;
-        const int64_t end = min(int64_t(stop - t_begin) * kClipUnit, numel);
+        const int64_t begin = int64_t(u - t_begin) * kNormUnit;
+        const int64_t end = min(int64_t(stop - t_begin) * kNormUnit, numel);
         double s = 0.;
         if (begin < end) {
             if (meta_src(meta))
-                s = sum_squares(static_cast<const uint16_t*>(a.data[t]), begin, end);
+                s = sum_squares<kThreads, kFlight>(static_cast<const uint16_t*>(a.data[t]), begin,
+                                                   end, threadIdx.x);
             else
-                s = sum_squares(static_cast<const float*>(a.data[t]), begin, end);
+                s = sum_squares<kThreads, kFlight>(static_cast<const float*>(a.data[t]), begin, end,
+                                                   threadIdx.x);
         }
-        s = block_sum(s, lds);
+        s = block_sum<kWaves>(s, lds);
         if (threadIdx.x == 0) {
             a.partial[w + t] = s;
             if (stop == u_end && stop == t_end && t + 1 < a.n) a.partial[w + t + 1] = 0.;
@@ -160,7 +184,31 @@ __global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double* __r
     __shared__ double lds[kWaves];
     double s = 0.;
     for (int i = threadIdx.x; i < count; i += kThreads) s += slots[i];
-    s = block_sum(s, lds);
+    s = block_sum<kWaves>(s, lds);
+    if (threadIdx.x == 0) finish(clip, s, max_norm);
+}
+
+// Short lists, in one launch: the waves of one workgroup take units of kSoloUnit
+// elements in turn, and the workgroup ends with the record.
+__global__ __launch_bounds__(kSoloThreads) void norm_solo_kernel(const NormArgs a, float max_norm,
+                                                                 muon_clip_t* clip) {
+    constexpr int kSoloWaves = kSoloThreads / 64;
+    __shared__ double lds[kSoloWaves];
+    double s = 0.;
+    for (int u = int(threadIdx.x) / 64; u < a.units; u += kSoloWaves) {
+        const int t = tensor_of(a.meta, a.n, u);
+        const uint64_t meta = a.meta[t];
+        const int64_t begin = int64_t(u - meta_unit(meta)) * kSoloUnit;
+        const int64_t end = min(begin + kSoloUnit, meta_numel(meta));
+        if (begin >= end) continue;
+        if (meta_src(meta))
+            s += sum_squares<64, 2>(static_cast<const uint16_t*>(a.data[t]), begin, end,
+                                    threadIdx.x & 63);
+        else
+            s += sum_squares<64, 4>(static_cast<const float*>(a.data[t]), begin, end,
+                                    threadIdx.x & 63);
+    }
+    s = block_sum<kSoloWaves>(s, lds);
     if (threadIdx.x == 0) finish(clip, s, max_norm);
 }
 
@@ -188,101 +236,110 @@ __global__ void clip_finish_kernel(muon_clip_t* clip, float max_norm) {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = bf16_rne(v); }
 
+// V consecutive elements, aligned to 4 elements (bfloat16 pairs: to 8).
 template <int V>
 __device__ __forceinline__ void load_v(const float* p, float v[V]) {
-#pragma unroll
-    for (int k = 0; k < V; k += 4) {
-        const float4 q = load4_stream(p + k);
-        v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
-    }
+    static_assert(V == 4, "16 bytes");
+    const float4 q = load4_stream(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
 }
 template <int V>
 __device__ __forceinline__ void load_v(const uint16_t* p, float v[V]) {
-    static_assert(V == 8, "16 bytes");
-    const u32x4_stream q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_stream*>(p));
+    if constexpr (V == 8) {
+        const u32x4_stream q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_stream*>(p));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(q[k]), v[2 * k + 1] = bf16_hi(q[k]);
+        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(q[k]), v[2 * k + 1] = bf16_hi(q[k]);
+    } else {
+        const uint2 q = load2_stream(reinterpret_cast<const uint2*>(p));
+        v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+    }
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    return uint32_t(bf16_rne(lo)) | uint32_t(bf16_rne(hi)) << 16;
 }
 template <int V>
 __device__ __forceinline__ void store_v(float* p, const float v[V]) {
-#pragma unroll
-    for (int k = 0; k < V; k += 4) store4_stream(p + k, make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+    static_assert(V == 4, "16 bytes");
+    store4_stream(p, make_float4(v[0], v[1], v[2], v[3]));
 }
 template <int V>
 __device__ __forceinline__ void store_v(uint16_t* p, const float v[V]) {
-    static_assert(V == 8, "16 bytes");
-    u32x4_stream q;
+    if constexpr (V == 8) {
+        u32x4_stream q;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        q[k] = uint32_t(bf16_rne(v[2 * k])) | uint32_t(bf16_rne(v[2 * k + 1])) << 16;
-    __builtin_nontemporal_store(q, reinterpret_cast<u32x4_stream*>(p));
-}
-
-// dst[i] = coef * src[i] for [begin, end).  Vectors of 16 bytes of the narrower
-// type where source and destination come to their 16-byte boundaries at the same
-// element, else one element after the other.  src may be dst.
-template <typename TS, typename TD>
-__device__ __forceinline__ void scale(const TS* src, TD* dst, int64_t begin, int64_t end,
-                                      float coef) {
-    constexpr int V = (sizeof(TS) == 2 || sizeof(TD) == 2) ? 8 : 4;
-    const int64_t count = end - begin;
-    src += begin, dst += begin;
-    const int sp = int((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / int(sizeof(TS));
-    const int dp = int((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / int(sizeof(TD));
-    // elements up to a boundary of both: the phase of the narrower type decides
-    const int head0 = sizeof(TS) == 2 ? sp : dp;
-    const bool together = sp % int(16 / sizeof(TS)) == head0 % int(16 / sizeof(TS)) &&
-                          dp % int(16 / sizeof(TD)) == head0 % int(16 / sizeof(TD));
-    const int64_t head = together ? min(int64_t(head0), count) : count;
-    const int64_t nvec = (count - head) / V;
-    for (int64_t i = threadIdx.x; i < nvec; i += kThreads) {
-        float v[V];
-        load_v<V>(src + head + i * V, v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = coef * v[k];
-        store_v<V>(dst + head + i * V, v);
+        for (int k = 0; k < 4; ++k) q[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
+        __builtin_nontemporal_store(q, reinterpret_cast<u32x4_stream*>(p));
+    } else {
+        store2_stream(reinterpret_cast<uint2*>(p),
+                      make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])));
     }
-    for (int64_t i = threadIdx.x; i < head; i += kThreads) put(dst + i, coef * element(src + i));
-    const int64_t tail = head + nvec * V + threadIdx.x;
-    if (tail < count) put(dst + tail, coef * element(src + tail));
 }
 
-__global__ __launch_bounds__(kThreads) void clip_kernel(const ClipArgs a) {
+// Unit k of dst = coef * src.  Where source and destination come to their vector
+// boundaries at the same element (`head` elements in), units are whole vectors
+// counted from there, unit 0 takes the head as well and the last one the tail;
+// elsewhere they are plain runs of elements.  src may be dst.
+//
+// A thread's vector is 4 elements (8 where both sides are bfloat16), so that
+// neighbouring lanes meet without a gap on the wider side too: 8 bfloat16 read
+// and two times 16 bytes of float32 stored by each lane took 1.6 times as long.
+template <typename TS, typename TD>
+__device__ __forceinline__ void scale_unit(const TS* src, TD* dst, int64_t numel, int64_t k,
+                                           float coef) {
+    constexpr int V = (sizeof(TS) == 2 && sizeof(TD) == 2) ? 8 : 4;
+    constexpr int kIters = int(kScaleUnit / (kScaleThreads * V));
+    static_assert(kScaleUnit == kIters * kScaleThreads * V, "whole passes of a workgroup");
+    const int head = int(-(reinterpret_cast<uintptr_t>(src) / sizeof(TS)) & (V - 1));
+    const bool together = head == int(-(reinterpret_cast<uintptr_t>(dst) / sizeof(TD)) & (V - 1));
+    const int64_t begin = k * kScaleUnit + (together ? head : 0);
+    if (together && begin + kScaleUnit <= numel) {
+        float v[kIters][V];
+#pragma unroll
+        for (int it = 0; it < kIters; ++it)
+            load_v<V>(src + begin + (it * kScaleThreads + int(threadIdx.x)) * V, v[it]);
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[it][j] = coef * v[it][j];
+            store_v<V>(dst + begin + (it * kScaleThreads + int(threadIdx.x)) * V, v[it]);
+        }
+    } else {
+        const int64_t end = min(begin + kScaleUnit, numel);
+        for (int64_t i = begin + threadIdx.x; i < end; i += kScaleThreads)
+            put(dst + i, coef * element(src + i));
+    }
+    if (k == 0 && together && int(threadIdx.x) < head && int64_t(threadIdx.x) < numel)
+        put(dst + threadIdx.x, coef * element(src + threadIdx.x));
+}
+
+__global__ __launch_bounds__(kScaleThreads) void clip_kernel(const ClipArgs a) {
     const float coef = a.clip->coef;
-    for (int u = blockIdx.x; u < a.units; u += int(gridDim.x)) {
+    for (int b = blockIdx.x; b < a.units; b += int(gridDim.x)) {
+        const int u = b;
         const int t = tensor_of(a.meta, a.n, u);
         const uint64_t meta = a.meta[t];
         const void* src = a.src[t];
         void* dst = a.dst[t];
         // times 1 in place changes nothing
         if (src == dst && coef == 1.f) continue;
-        const int64_t begin = int64_t(u - meta_unit(meta)) * kClipUnit;
-        const int64_t end = min(begin + kClipUnit, meta_numel(meta));
-        if (begin >= end) continue;
+        const int64_t numel = meta_numel(meta), k = u - meta_unit(meta);
         if (meta_src(meta)) {
             if (meta_dst(meta))
-                scale(static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), begin, end, coef);
+                scale_unit(static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), numel, k, coef);
             else
-                scale(static_cast<const uint16_t*>(src), static_cast<float*>(dst), begin, end, coef);
+                scale_unit(static_cast<const uint16_t*>(src), static_cast<float*>(dst), numel, k, coef);
         } else {
             if (meta_dst(meta))
-                scale(static_cast<const float*>(src), static_cast<uint16_t*>(dst), begin, end, coef);
+                scale_unit(static_cast<const float*>(src), static_cast<uint16_t*>(dst), numel, k, coef);
             else
-                scale(static_cast<const float*>(src), static_cast<float*>(dst), begin, end, coef);
+                scale_unit(static_cast<const float*>(src), static_cast<float*>(dst), numel, k, coef);
         }
     }
 }
 
-// The launches of a tensor list: f(first tensor, count, units).
-template <typename F>
-void for_each_batch(const muon_tensor_t* t, int64_t n, int most, F f) {
-    for (int64_t i = 0; i < n; i += most) {
-        const int64_t m = std::min<int64_t>(most, n - i);
-        int64_t units = 0;
-        for (int64_t k = i; k < i + m; ++k) units += clip_units(t[k].numel);
-        f(i, int(m), units);
-    }
-}
+// A grid counts at most 2^32 - 1 work-items; longer lists loop.
+constexpr int64_t kMaxGrid = int64_t(1) << 24;
+static_assert(kMaxGrid * kScaleThreads < (int64_t(1) << 32), "grid");
 
 int span_of(int64_t units) { return int((units + kNormGroups - 1) / kNormGroups); }
 int groups_of(int64_t units) {
@@ -290,45 +347,71 @@ int groups_of(int64_t units) {
     return int((units + span - 1) / span);
 }
 
+size_t type_bytes(int dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
+
+// Whether y begins where x ends, so that one entry can stand for both.
+bool adjacent(const muon_tensor_t& x, const muon_tensor_t& y) {
+    return x.dtype == y.dtype && x.numel + y.numel <= kMaxNumel &&
+           static_cast<const char*>(x.data) + size_t(x.numel) * type_bytes(x.dtype) == y.data;
+}
+
 }  // namespace
 
 int64_t norm_slots(const muon_tensor_t* t, int64_t n) {
-    int64_t slots = 0;
-    for_each_batch(t, n, kNormTensors,
-                   [&](int64_t, int m, int64_t units) { slots += groups_of(units) + m - 1; });
-    return slots;
+    int64_t units = 0;
+    for (int64_t i = 0; i < n; ++i) units += units_of(t[i].numel, kNormUnit);
+    return (n + kNormTensors - 1) / kNormTensors * std::min<int64_t>(units, kNormGroups) + n;
 }
 
 hipError_t launch_grad_norm(const muon_tensor_t* t, int64_t n, float max_norm, muon_clip_t* clip,
                             float* tensor_norms, double* slots, hipStream_t s) {
-    hipError_t err = hipSuccess;
     int64_t at = 0;
-    for_each_batch(t, n, kNormTensors, [&](int64_t i, int m, int64_t units) {
-        if (err != hipSuccess) return;
+    for (int64_t i = 0; i < n;) {
         NormArgs a;
-        int64_t u = 0;
-        for (int k = 0; k < m; ++k) {
-            a.data[k] = t[i + k].data;
-            a.meta[k] = clip_meta(t[i + k].numel, t[i + k].dtype == MUON_DTYPE_BF16, 0, u);
-            u += clip_units(t[i + k].numel);
+        a.base = int32_t(i);
+        int m = 0;
+        int64_t numel[kNormTensors];
+        int64_t units = 0, solo_units = 0;
+        while (i < n && m < kNormTensors) {
+            // a run of adjacent tensors is one, unless each one's norm is asked for
+            muon_tensor_t x = t[i++];
+            while (tensor_norms == nullptr && i < n && adjacent(x, t[i])) x.numel += t[i++].numel;
+            a.data[m] = x.data;
+            a.meta[m] = clip_meta(x.numel, x.dtype == MUON_DTYPE_BF16, 0, units);
+            numel[m] = x.numel;
+            units += units_of(x.numel, kNormUnit);
+            solo_units += units_of(x.numel, kSoloUnit);
+            ++m;
         }
         a.partial = slots + at;
-        a.n = m, a.units = int32_t(units), a.span = span_of(units), a.base = int32_t(i);
+        a.n = m;
+        if (a.base == 0 && i == n && tensor_norms == nullptr && solo_units <= kSoloUnits) {
+            a.units = int32_t(solo_units);
+            solo_units = 0;
+            for (int k = 0; k < m; ++k) {
+                a.meta[k] = clip_meta(numel[k], meta_src(a.meta[k]), 0, solo_units);
+                solo_units += units_of(numel[k], kSoloUnit);
+            }
+            LaunchTimer timer("norm_solo", s);
+            norm_solo_kernel<<<dim3(1), dim3(kSoloThreads), 0, s>>>(a, max_norm, clip);
+            return hipGetLastError();
+        }
+        a.units = int32_t(units), a.span = span_of(units);
         const int groups = groups_of(units);
         {
             LaunchTimer timer("grad_norm", s);
             grad_norm_kernel<<<dim3(unsigned(groups)), dim3(kThreads), 0, s>>>(a);
         }
-        if ((err = hipGetLastError()) != hipSuccess) return;
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
         if (tensor_norms != nullptr) {
             LaunchTimer timer("tensor_norms", s);
             tensor_norms_kernel<<<dim3(unsigned((m + kWaves - 1) / kWaves)), dim3(kThreads), 0, s>>>(
                 a, tensor_norms);
-            err = hipGetLastError();
+            if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         at += groups + m - 1;
-    });
-    if (err != hipSuccess) return err;
+    }
     LaunchTimer timer("norm_finish", s);
     norm_finish_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(slots, int(at), max_norm, clip);
     return hipGetLastError();
@@ -342,25 +425,34 @@ hipError_t launch_clip_finish(muon_clip_t* clip, float max_norm, hipStream_t s) 
 
 hipError_t launch_clip(const muon_tensor_t* src, const muon_tensor_t* dst, int64_t n,
                        const muon_clip_t* clip, hipStream_t s) {
-    hipError_t err = hipSuccess;
-    for_each_batch(src, n, kClipTensors, [&](int64_t i, int m, int64_t units) {
-        if (err != hipSuccess) return;
+    for (int64_t i = 0; i < n;) {
         ClipArgs a;
-        int64_t u = 0;
-        for (int k = 0; k < m; ++k) {
-            a.src[k] = src[i + k].data;
-            a.dst[k] = dst[i + k].data;
-            a.meta[k] = clip_meta(src[i + k].numel, src[i + k].dtype == MUON_DTYPE_BF16,
-                                  dst[i + k].dtype == MUON_DTYPE_BF16, u);
-            u += clip_units(src[i + k].numel);
+        int64_t units = 0;
+        int m = 0;
+        while (i < n && m < kClipTensors) {
+            // a run of tensors adjacent on both sides is one
+            muon_tensor_t x = src[i], y = dst[i];
+            ++i;
+            while (i < n && adjacent(x, src[i]) && adjacent(y, dst[i])) {
+                x.numel += src[i].numel;
+                y.numel = x.numel;
+                ++i;
+            }
+            a.src[m] = x.data;
+            a.dst[m] = y.data;
+            a.meta[m] = clip_meta(x.numel, x.dtype == MUON_DTYPE_BF16, y.dtype == MUON_DTYPE_BF16,
+                                  units);
+            units += units_of(x.numel, kScaleUnit);
+            ++m;
         }
         a.clip = clip, a.n = m, a.units = int32_t(units);
-        const int64_t grid = std::min<int64_t>(units, int64_t(1) << 23);
+        const int64_t grid = std::min<int64_t>(units, kMaxGrid);
         LaunchTimer timer("clip", s);
-        clip_kernel<<<dim3(unsigned(grid)), dim3(kThreads), 0, s>>>(a);
-        err = hipGetLastError();
-    });
-    return err;
+        clip_kernel<<<dim3(unsigned(grid)), dim3(kScaleThreads), 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace muon

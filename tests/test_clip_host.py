@@ -231,7 +231,7 @@ def test_binding_refuses_host_tensors():
     for call in (lambda: nsf.tensor_list([t]), lambda: nsf.muon_grad_norm([t], 1.0, clip),
                  lambda: nsf.muon_clip_grads([t], clip), lambda: nsf.muon_clip_finish(clip, 1.0),
                  lambda: nsf.muon_adamw(t, t, t, t, [(0, 8)], None)):
-        with pytest.raises(ValueError, match="GPU tensor"):
+        with pytest.raises(ValueError, match="GPU"):
             call()
 
 
@@ -248,11 +248,11 @@ def test_binding_tables():
     assert nsf.ranges_array(arr) is arr
     assert [(r.offset, r.numel, r.param_offset, r.group) for r in arr] == [(4, 8, 4, 0), (16, 3, 32, 1)]
     clip = nsf.clip_state("cpu")
-    clip[0] = 9.0
+    clip.sumsq[0] = 9.0
     nsf.clip_norm(clip).fill_(3.0)
     nsf.clip_coef(clip).fill_(0.5)
     assert nsf.clip_sumsq(clip).tolist() == [9.0]
-    raw = clip.numpy().view(np.float32)
+    raw = clip.record.numpy().view(np.float32)
     assert raw[2] == 3.0 and raw[3] == 0.5
 
 

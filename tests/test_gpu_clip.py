@@ -67,7 +67,7 @@ def make_list(torch, sizes, seed, std=1.0, shift=0, dtypes=("f32", "bf16")):
 
 
 def read(nsf, clip):
-    c = clip.cpu()
+    c = clip.record.cpu()
     f = c.numpy().view(np.float32)
     return float(c[0]), float(f[2]), float(f[3])
 
@@ -86,6 +86,8 @@ def check_record(nsf, clip, arrays, max_norm):
 
 
 SIZES = {
+    "solo_full": [2048] * 47 + [2048],      # the longest list that one workgroup takes,
+    "solo_over": [2048] * 47 + [2049],      # and one element more
     "single": [1],
     "empty": [0],
     "edges": [0, 1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 31, 33, 63, 65, 255, 257, 1023, 1025],
@@ -106,20 +108,61 @@ def test_norm(nsf, torch, name, dtypes):
     nsf.muon_grad_norm(ts, 0.75, clip, tensor_norms=norms, workspace=ws)
     torch.cuda.synchronize()
     arrays = [values(t) for t in ts]
-    s = check_record(nsf, clip, arrays, 0.75)
+    check_record(nsf, clip, arrays, 0.75)
     got = host(norms)
     for a, x in zip(arrays, got):
         want = math.sqrt(ao.sumsq([a]))
         assert abs(float(x) - want) <= (HALF + a.size * 2.0 ** -53 + 2.0 ** -50) * want
-    # the same again, without norms and in the default workspace: the same bits
-    again = nsf.clip_state("cuda")
+    # without norms and in the default workspace the sum may take another order (short
+    # lists go to one workgroup, adjacent tensors are one): two sums of the same N
+    # terms, each within N 2^-53 of the exact one, check_record's bound for both
+    again, third = nsf.clip_state("cuda"), nsf.clip_state("cuda")
     nsf.muon_grad_norm(nsf.tensor_list(ts), 0.75, again)
+    nsf.muon_grad_norm(ts, 0.75, third)
     torch.cuda.synchronize()
-    assert torch.equal(again, clip) and read(nsf, again)[0] == s
+    check_record(nsf, again, arrays, 0.75)
+    # the same call twice: the same bits
+    assert torch.equal(again.record, third.record)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("count,n", [(5, 8), (40, 2001), (300, 9001), (700, 513)])
+def test_packed_lists(nsf, torch, count, n, dtype):
+    """Tensors one behind the other, in their order and shuffled: norm (with and
+    without each one's own), clipping into another buffer and in place."""
+    say("packed", count, n, dtype)
+    flat = torch.randn(count * n + 3, device="cuda").to(tdtype(torch, dtype))
+    out = torch.full((count * n + 3,), math.nan, device="cuda")
+    before = host(flat).copy()
+    parts = [flat[1 + k * n:1 + (k + 1) * n] for k in range(count)]
+    outs = [out[1 + k * n:1 + (k + 1) * n] for k in range(count)]
+    order = np.random.default_rng(count).permutation(count)
+    clip, norms = nsf.clip_state("cuda"), torch.zeros(count, device="cuda")
+    inner = values(flat)[1:-2]
+    for idx in (range(count), order):
+        nsf.muon_grad_norm([parts[k] for k in idx], 1.0, clip)
+        check_record(nsf, clip, [inner], 1.0)
+        nsf.muon_grad_norm([parts[k] for k in idx], 1.0, clip, tensor_norms=norms)
+        check_record(nsf, clip, [inner], 1.0)
+        got = host(norms)
+        for j, k in enumerate(idx):
+            want = math.sqrt(ao.sumsq([inner[k * n:(k + 1) * n]]))
+            assert abs(float(got[j]) - want) <= (HALF + n * 2.0 ** -53 + 2.0 ** -50) * want
+        out.fill_(math.nan)
+        nsf.muon_clip_grads([parts[k] for k in idx], clip, out=[outs[k] for k in idx])
+        coef = read(nsf, clip)[2]
+        want = ao.clip_same_order(before[1:-2], coef, "f32")
+        assert np.array_equal(bits(host(out)[1:-2]), bits(want))
+        assert np.isnan(host(out)[[0, -2, -1]]).all()
+    nsf.muon_clip_grads([parts[k] for k in order], clip)
+    want = before.copy()
+    want[1:-2] = ao.clip_same_order(before[1:-2], coef, dtype)
+    assert np.array_equal(bits(host(flat)), bits(want))
 
 
 def test_norm_of_an_empty_list(nsf, torch):
-    clip = torch.full((2,), 7.0, dtype=torch.float64, device="cuda")
+    clip = nsf.clip_state("cuda")
+    clip.record.fill_(7.0)
     nsf.muon_grad_norm([], 1.0, clip)
     torch.cuda.synchronize()
     assert read(nsf, clip) == (0.0, 0.0, 1.0)
@@ -188,7 +231,7 @@ def test_parts_add_up(nsf, torch):
     torch.cuda.synchronize()
     check_record(nsf, a, [values(t) for t in ts], 2.0)
     # one rounding of the sum apart
-    assert abs(float(a[0]) - float(whole[0])) <= 4 * 2.0 ** -53 * 130000 * float(whole[0])
+    assert abs(read(nsf, a)[0] - read(nsf, whole)[0]) <= 4 * 2.0 ** -53 * 130000 * read(nsf, whole)[0]
 
 
 def test_overlapping_tensors_count_each(nsf, torch):
@@ -438,7 +481,8 @@ def training_step(nsf, s):
 
 
 def state_of(s):
-    return [host(s[k]).copy() for k in ("params", "mom", "w", "m", "v", "copy", "clip", "agroups")]
+    return [host(x).copy() for x in (*(s[k] for k in ("params", "mom", "w", "m", "v", "copy",
+                                                       "agroups")), s["clip"].record)]
 
 
 def new_gradients(torch, s, seed):
@@ -525,10 +569,10 @@ def test_binding_refusals_on_the_device(nsf, torch):
         nsf.tensor_list([t[::2]])
     with pytest.raises(TypeError):
         nsf.tensor_list([1.0])
-    with pytest.raises(ValueError, match="clip_state"):
-        nsf.muon_grad_norm([t], 1.0, torch.zeros(3, dtype=torch.float64, device="cuda"))
-    with pytest.raises(TypeError):
-        nsf.muon_grad_norm([t], 1.0, torch.zeros(2, device="cuda"))
+    with pytest.raises(TypeError, match="clip_state"):
+        nsf.muon_grad_norm([t], 1.0, torch.zeros(2, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError, match="GPU"):
+        nsf.muon_grad_norm([], 1.0, nsf.clip_state("cpu"))
     with pytest.raises(ValueError, match="one element per tensor"):
         nsf.muon_grad_norm([t], 1.0, clip, tensor_norms=torch.zeros(2, device="cuda"))
     with pytest.raises(nsf.MuonError) as e:
@@ -551,12 +595,13 @@ def test_kernel_timing_names(nsf, torch):
     clip = nsf.clip_state("cuda")
     nsf.muon_profile_begin()
     nsf.muon_grad_norm([t], 1.0, clip, tensor_norms=torch.zeros(1, device="cuda"))
+    nsf.muon_grad_norm([t], 1.0, clip)
     nsf.muon_clip_finish(clip, 1.0)
     nsf.muon_clip_grads([t], clip)
     z = [torch.zeros(100, device="cuda") for _ in range(3)]
     nsf.muon_adamw(z[0], t, z[1], z[2], [(0, 100)], nsf.adamw_group_table(GROUPS, "cuda"), clip=clip)
     got = nsf.muon_profile_end()
-    for name in ("grad_norm", "clip_finish", "clip", "adamw"):
+    for name in ("grad_norm", "tensor_norms", "norm_finish", "norm_solo", "clip_finish", "clip", "adamw"):
         assert got[name][1] == 1
 
 
