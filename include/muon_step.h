@@ -352,9 +352,11 @@ int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void
                       void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* One range of parameters of muon_adamw.
- *   offset        first element in grads / exp_avg / exp_avg_sq; multiple of 4
+ *   offset        first element in grads / exp_avg / exp_avg_sq; multiple of 4,
+ *                 below 2^36
  *   numel         0..2^34 elements (2^36 in all ranges)
- *   param_offset  first element in params (and model_copy); 16-byte aligned
+ *   param_offset  first element in params (and model_copy); 16-byte aligned,
+ *                 below 2^36
  *   group         row of the group table */
 typedef struct muon_range {
     int64_t offset;
@@ -411,8 +413,8 @@ int muon_adamw(void* params, int param_dtype, int64_t n_param_elems, void* model
  * distinct kernels, which may exceed max_entries).  Names are
  * "front", "sumsq", "norm", "cast", "apply" and "ns_<stage>_t<tile>_<type>"
  * for the Newton-Schulz products (stage a: X X^T, b: b A + c A A, x: a X + B X;
- * tile 64/128/256; type bf16/f32); "grad_norm", "tensor_norms", "norm_finish",
- * "clip_finish", "clip" and "adamw" for the operators above.  Events come from a pool the library owns;
+ * tile 64/128/256; type bf16/f32); "grad_norm", "norm_solo", "tensor_norms",
+ * "norm_finish", "clip_finish", "clip" and "adamw" for the operators above.  Events come from a pool the library owns;
  * when timing is off the only cost is one flag test per launch. */
 typedef struct muon_kernel_time {
     char name[48];

@@ -64,13 +64,16 @@ static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments");
 
 // Elements of one unit of the AdamW kernel.
 constexpr int64_t kAdamwUnit = 256;
-constexpr int kAdamwRanges = 144;
-static_assert(kMaxSetNumel / kAdamwUnit + kAdamwRanges < (int64_t(1) << 29), "unit number");
+static_assert(kMaxSetNumel / kAdamwUnit + 256 < (int64_t(1) << 29), "unit number");
+constexpr int kAdamwRanges = 240;
+// A range in two words.  Offsets are multiples of 4 below kMaxSetNumel; the
+// length follows from the units that the range takes and what its last one lacks.
+struct AdamwRange {
+    uint64_t at;  // bits 0-33 offset / 4, 34-49 group, 50-57 elements missing in the last unit
+    uint64_t to;  // bits 0-33 param_offset / 4, 34-63 first unit
+};
 struct AdamwArgs {
-    int64_t off[kAdamwRanges];   // first element in grads / exp_avg / exp_avg_sq
-    int64_t poff[kAdamwRanges];  // first element in params / model_copy
-    uint64_t meta[kAdamwRanges];  // bits 0-34 numel (<= 2^34), bits 35-63 the first unit
-    uint16_t group[kAdamwRanges];
+    AdamwRange range[kAdamwRanges];
     void* params;
     uint16_t* copy;
     const void* grads;

@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kVec = 4;
 constexpr int kIters = int(kAdamwUnit / (kThreads * kVec));
+static_assert(kAdamwUnit <= 256, "the missing elements fit 8 bits");
 static_assert(kAdamwUnit == kIters * kThreads * kVec, "whole passes of a workgroup");
 
 // b^t by repeated squaring.  t = 0 gives 1 (and with it an infinite step
@@ -85,10 +86,8 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = bf16_rne(v); }
 
-__device__ __forceinline__ int unit_begin(uint64_t meta) { return int(meta >> 35); }
-__device__ __forceinline__ int64_t meta_numel(uint64_t meta) {
-    return int64_t(meta & ((uint64_t(1) << 35) - 1));
-}
+constexpr uint64_t kOffsetBits = (uint64_t(1) << 34) - 1;
+__device__ __forceinline__ int unit_begin(const AdamwRange& r) { return int(r.to >> 34); }
 
 // Unit of workgroup b.  Workgroups go to the 8 XCDs in turn; each XCD gets runs
 // of kRun consecutive units (64 Ki elements), so that it walks through pages of
@@ -111,19 +110,24 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwArgs a) {
         int lo = 0, hi = a.n - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (unit_begin(a.meta[mid]) <= u)
+            if (unit_begin(a.range[mid]) <= u)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const uint64_t meta = a.meta[lo];
-        const int64_t numel = meta_numel(meta);
-        const int64_t base = int64_t(u - unit_begin(meta)) * kAdamwUnit;
-        const TG* g = static_cast<const TG*>(a.grads) + a.off[lo];
-        float* m = a.m + a.off[lo];
-        float* v = a.v + a.off[lo];
-        TW* w = static_cast<TW*>(a.params) + a.poff[lo];
-        uint16_t* copy = a.copy != nullptr ? a.copy + a.poff[lo] : nullptr;
+        const AdamwRange range = a.range[lo];
+        const int next = lo + 1 < a.n ? unit_begin(a.range[lo + 1]) : a.units;
+        const int64_t numel = int64_t(next - unit_begin(range)) * kAdamwUnit -
+                              int64_t((range.at >> 50) & 255);
+        const int64_t base = int64_t(u - unit_begin(range)) * kAdamwUnit;
+        const int64_t off = int64_t(range.at & kOffsetBits) * 4;
+        const int64_t poff = int64_t(range.to & kOffsetBits) * 4;
+        const int group = int(range.at >> 34) & 0xffff;
+        const TG* g = static_cast<const TG*>(a.grads) + off;
+        float* m = a.m + off;
+        float* v = a.v + off;
+        TW* w = static_cast<TW*>(a.params) + poff;
+        uint16_t* copy = a.copy != nullptr ? a.copy + poff : nullptr;
         if (base + kAdamwUnit <= numel) {
             // whole unit: every load goes out before the first wait; the step's scalars
             // (some hundred cycles of float64) are worked out while they are on their way
@@ -136,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwArgs a) {
                 v4[it] = load4(v + e);
                 w4[it] = load4(w + e);
             }
-            const Step s = step_of(a.groups[a.group[lo]], a.clip);
+            const Step s = step_of(a.groups[group], a.clip);
 #pragma unroll
             for (int it = 0; it < kIters; ++it) {
                 const int64_t e = base + (int64_t(it) * kThreads + threadIdx.x) * kVec;
@@ -150,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwArgs a) {
                 if (copy != nullptr) store4(copy + e, w4[it]);
             }
         } else {
-            const Step s = step_of(a.groups[a.group[lo]], a.clip);
+            const Step s = step_of(a.groups[group], a.clip);
             for (int64_t k = base + threadIdx.x; k < numel; k += kThreads) {
                 float m1 = m[k], v1 = v[k], w1 = load1(w + k);
                 update(s, load1(g + k), m1, v1, w1);
@@ -196,11 +200,11 @@ hipError_t launch_adamw(void* params, int param_dtype, void* model_copy, const v
                    q.numel + ranges[i].numel <= kMaxNumel;
                  ++i)
                 q.numel += ranges[i].numel;
-            a.off[m] = q.offset;
-            a.poff[m] = q.param_offset;
-            a.meta[m] = uint64_t(q.numel) | uint64_t(units) << 35;
-            a.group[m] = uint16_t(q.group);
-            units += (q.numel + kAdamwUnit - 1) / kAdamwUnit;
+            const int64_t mine = (q.numel + kAdamwUnit - 1) / kAdamwUnit;
+            a.range[m].at = uint64_t(q.offset / 4) | uint64_t(q.group) << 34 |
+                            uint64_t(mine * kAdamwUnit - q.numel) << 50;
+            a.range[m].to = uint64_t(q.param_offset / 4) | uint64_t(units) << 34;
+            units += mine;
             ++m;
         }
         if (m == 0) break;

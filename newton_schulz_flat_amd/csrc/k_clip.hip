@@ -36,6 +36,7 @@ constexpr int kWaves = kThreads / 64;
 // 8.5 us (21), 64 Ki 5.8 (18.2) against 8.6 (21), 64 tensors of 1024 6.1 (18.4)
 // against 8.9 (22); at 128 Ki float32 they meet (8.0 and 8.5), at 256 Ki one
 // workgroup takes 13.4.  Units of 512 or 1024 elements: 9.5 and 6.4 us at 64 Ki.
+constexpr int kFinishThreads = 1024;
 constexpr int kSoloThreads = 1024;
 constexpr int64_t kSoloUnit = 2048;
 constexpr int kSoloUnits = 48;
@@ -178,14 +179,42 @@ __device__ __forceinline__ void finish(muon_clip_t* clip, double sumsq, float ma
     clip->coef = c > 1. ? 1.f : float(c);
 }
 
-__global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double* __restrict__ slots,
-                                                               int count, float max_norm,
-                                                               muon_clip_t* clip) {
-    __shared__ double lds[kWaves];
+// The record from all partials.  One workgroup as wide as they come, so that
+// each thread waits for one load (two launches' worth of partials: for two).
+__device__ __forceinline__ void finish_all(const double* __restrict__ slots, int count,
+                                           float max_norm, muon_clip_t* clip, double* lds) {
     double s = 0.;
-    for (int i = threadIdx.x; i < count; i += kThreads) s += slots[i];
-    s = block_sum<kWaves>(s, lds);
+    for (int i = threadIdx.x; i < count; i += kFinishThreads) s += slots[i];
+    s = block_sum<kFinishThreads / 64>(s, lds);
     if (threadIdx.x == 0) finish(clip, s, max_norm);
+}
+
+__global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(
+    const double* __restrict__ slots, int count, float max_norm, muon_clip_t* clip) {
+    __shared__ double lds[kFinishThreads / 64];
+    finish_all(slots, count, max_norm, clip, lds);
+}
+
+// The norms of a launch's tensors, one wave for each, and, from the list's last
+// launch (clip not null), the record by workgroup 0.
+__global__ __launch_bounds__(kFinishThreads) void tensor_norms_kernel(
+    const NormArgs a, float* __restrict__ norms, const double* __restrict__ slots, int count,
+    float max_norm, muon_clip_t* clip) {
+    __shared__ double lds[kFinishThreads / 64];
+    if (blockIdx.x == 0) {
+        if (clip != nullptr) finish_all(slots, count, max_norm, clip, lds);
+        return;
+    }
+    const int t = (int(blockIdx.x) - 1) * (kFinishThreads / 64) + int(threadIdx.x >> 6);
+    if (t >= a.n) return;
+    const int first = meta_unit(a.meta[t]);
+    const int last = (t + 1 < a.n ? meta_unit(a.meta[t + 1]) : a.units) - 1;
+    const int lo = first / a.span + t, hi = last / a.span + t;
+    double s = 0.;
+    for (int i = lo + int(threadIdx.x & 63); i <= hi; i += 64) s += a.partial[i];
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+    if ((threadIdx.x & 63) == 0) norms[a.base + t] = float(sqrt(s));
 }
 
 // Short lists, in one launch: the waves of one workgroup take units of kSoloUnit
@@ -210,21 +239,6 @@ __global__ __launch_bounds__(kSoloThreads) void norm_solo_kernel(const NormArgs 
     }
     s = block_sum<kSoloWaves>(s, lds);
     if (threadIdx.x == 0) finish(clip, s, max_norm);
-}
-
-// One wave sums the slots of one tensor.
-__global__ __launch_bounds__(kThreads) void tensor_norms_kernel(const NormArgs a,
-                                                                float* __restrict__ norms) {
-    const int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
-    if (t >= a.n) return;
-    const int first = meta_unit(a.meta[t]);
-    const int last = (t + 1 < a.n ? meta_unit(a.meta[t + 1]) : a.units) - 1;
-    const int lo = first / a.span + t, hi = last / a.span + t;
-    double s = 0.;
-    for (int i = lo + int(threadIdx.x & 63); i <= hi; i += 64) s += a.partial[i];
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-    if ((threadIdx.x & 63) == 0) norms[a.base + t] = float(sqrt(s));
 }
 
 __global__ void clip_finish_kernel(muon_clip_t* clip, float max_norm) {
@@ -404,16 +418,18 @@ hipError_t launch_grad_norm(const muon_tensor_t* t, int64_t n, float max_norm, m
         }
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        if (tensor_norms != nullptr) {
-            LaunchTimer timer("tensor_norms", s);
-            tensor_norms_kernel<<<dim3(unsigned((m + kWaves - 1) / kWaves)), dim3(kThreads), 0, s>>>(
-                a, tensor_norms);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
         at += groups + m - 1;
+        if (tensor_norms != nullptr) {
+            constexpr int kTensors = kFinishThreads / 64;  // of one workgroup
+            LaunchTimer timer("tensor_norms", s);
+            tensor_norms_kernel<<<dim3(unsigned(1 + (m + kTensors - 1) / kTensors)),
+                                  dim3(kFinishThreads), 0, s>>>(a, tensor_norms, slots, int(at),
+                                                                max_norm, i == n ? clip : nullptr);
+            if ((e = hipGetLastError()) != hipSuccess || i == n) return e;
+        }
     }
     LaunchTimer timer("norm_finish", s);
-    norm_finish_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(slots, int(at), max_norm, clip);
+    norm_finish_kernel<<<dim3(1), dim3(kFinishThreads), 0, s>>>(slots, int(at), max_norm, clip);
     return hipGetLastError();
 }
 

@@ -199,6 +199,11 @@ int check_ranges(const muon_range_t* r, int64_t n, int64_t n_groups, int64_t n_s
                         "ranges[%lld]: param_offset %lld, numel %lld are outside params (%lld elements)",
                         (long long)i, (long long)q.param_offset, (long long)q.numel,
                         (long long)n_params);
+        if (q.offset >= kMaxSetNumel || q.param_offset >= kMaxSetNumel)
+            return fail(st, MUON_ERR_BAD_SHAPE,
+                        "ranges[%lld]: offset %lld or param_offset %lld is not below %lld",
+                        (long long)i, (long long)q.offset, (long long)q.param_offset,
+                        (long long)kMaxSetNumel);
         if (q.offset % 4 != 0)
             return fail(st, MUON_ERR_MISALIGNED, "ranges[%lld]: offset %lld is not a multiple of 4",
                         (long long)i, (long long)q.offset);

@@ -184,6 +184,8 @@ def test_adamw_refuses(lib, kw, code):
 @pytest.mark.parametrize("ranges,kw,code", [
     ([(0, -1)], {}, "BAD_SHAPE"),
     ([(0, (1 << 34) + 1)], {}, "BAD_SHAPE"),
+    ([(1 << 36, 8, 0)], dict(n_state=1 << 37), "BAD_SHAPE"),
+    ([(0, 8, 1 << 36)], dict(n_params=1 << 37), "BAD_SHAPE"),
     ([(2, 8, 0)], {}, "MISALIGNED"),
     ([(0, 8, 2)], {}, "MISALIGNED"),
     ([(4, 8, 4)], dict(pdt=BF16), "MISALIGNED"),
