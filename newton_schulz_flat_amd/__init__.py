@@ -507,17 +507,17 @@ _clip_workspaces: dict = {}
 
 def _clip_workspace_for(tl: TensorList, device):
     import torch
-    if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("pass an explicit workspace to calls made under graph capture")
-    stream = torch.cuda.current_stream(device)
-    key = (device, stream.cuda_stream)
-    need = muon_clip_workspace_bytes(tl)
-    ws = _clip_workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        _clip_workspaces.pop(key, None)
-        with torch.cuda.stream(stream):
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("pass an explicit workspace to calls made under graph capture")
+        stream = torch.cuda.current_stream()
+        key = (device, stream.cuda_stream)
+        need = muon_clip_workspace_bytes(tl)
+        ws = _clip_workspaces.get(key)
+        if ws is None or ws.numel() < need:
+            _clip_workspaces.pop(key, None)
             ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _clip_workspaces[key] = ws
+            _clip_workspaces[key] = ws
     return ws
 
 

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <vector>
 
@@ -308,9 +309,15 @@ int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void
         return finish(st);
     }
     const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0, clip};
-    return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
-                    n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
-                    workspace_bytes, stream);
+    try {
+        return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
+                        n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
+                        workspace_bytes, stream);
+    } catch (const std::exception& e) {  // of the host tables' memory
+        st.code = MUON_ERR_INTERNAL;
+        snprintf(st.msg, sizeof(st.msg), "exception: %s", e.what());
+        return finish(st);
+    }
 }
 
 int muon_momentum(const float* grads, float* momentum, float* u_out, int64_t n_state_elems,

@@ -384,6 +384,28 @@ def test_adamw(nsf, torch, name, wdt, gdt, clipped):
         assert np.isnan(so.bf16_bits_to_f32(c[~inside])).all()
 
 
+@pytest.mark.parametrize("wdt", ["f32", "bf16"])
+def test_adamw_adjacent_ranges(nsf, torch, wdt):
+    """Ranges one behind the other (some of one group, empty ones among them, one that
+    is adjacent in the state alone), in any order: the same as each alone."""
+    say("adamw adjacent", wdt)
+    n = 4000
+    w = (torch.randn(n, device="cuda") * 0.05).to(tdtype(torch, wdt))
+    g, m = (torch.randn(n, device="cuda") * 0.1 for _ in range(2))
+    v = torch.rand(n, device="cuda") * 0.01
+    ranges = [(0, 64, 0, 0), (64, 128, 64, 0), (192, 0, 192, 0), (192, 800, 192, 0),
+              (992, 8, 992, 1), (1000, 1000, 1000, 1), (2000, 40, 2400, 1), (2040, 13, 2440, 1),
+              (2056, 5, 2000, 2), (2064, 1200, 2600, 2)]
+    want = adamw_want(ranges, w, g, m, v, None)
+    table = nsf.adamw_group_table(GROUPS, "cuda")
+    for idx in (range(len(ranges)), reversed(range(len(ranges)))):
+        w1, m1, v1 = w.clone(), m.clone(), v.clone()
+        nsf.muon_adamw(w1, g, m1, v1, [ranges[k] for k in idx], table)
+        torch.cuda.synchronize()
+        for got, ref in zip((w1, m1, v1), want):
+            assert np.array_equal(bits(host(got)), bits(ref))
+
+
 def test_adamw_against_the_definition(nsf, torch):
     """30 steps from zero state against float64.  The moments' relative error grows by
     at most 6 half steps a step; each update's is within (6 + 6) t of its own size
@@ -528,6 +550,43 @@ def test_training_step_in_a_graph(nsf, torch):
             wn[pl], mn[sl], vn[sl] = ao.adamw_same_order(wn[pl], gn[sl], mn[sl], vn[sl], grow, coef)
         for k, ref in zip("wmv", (wn, mn, vn)):
             assert np.array_equal(bits(host(eager[k])), bits(ref)), (rep, k)
+
+
+@pytest.mark.parametrize("sizes", [[300, 5, 77], [200000, 3, 8192, 70001]])
+def test_norm_and_clip_in_graphs(nsf, torch, sizes):
+    """Norm and clipping captured as their first calls on their tensors: in place and into
+    other tensors, two graphs over one record and workspace, replayed in turn."""
+    say("norm and clip in graphs", sizes)
+    ts, _ = make_list(torch, sizes, 21)
+    clip = nsf.clip_state("cuda")
+    outs = [torch.zeros(n, device="cuda") for n in sizes]
+    tl = nsf.tensor_list(ts)
+    ws = torch.empty(nsf.muon_clip_workspace_bytes(tl), dtype=torch.uint8, device="cuda")
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        nsf.muon_grad_norm(tl, 2.0, clip, workspace=ws)
+        nsf.muon_clip_grads(tl, clip, out=outs)
+    with torch.cuda.graph(second):
+        nsf.muon_grad_norm(tl, 1.0, clip, workspace=ws)
+        nsf.muon_clip_grads(tl, clip)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for rep in range(4):
+        for t in ts:
+            t.copy_(torch.randn(t.numel(), generator=gen, device="cuda"))
+        before = [host(t).copy() for t in ts]
+        torch.cuda.synchronize()
+        first.replay()
+        torch.cuda.synchronize()
+        check_record(nsf, clip, [ao.widen(b) for b in before], 2.0)
+        coef = read(nsf, clip)[2]
+        for b, o in zip(before, outs):
+            assert np.array_equal(bits(host(o)), bits(ao.clip_same_order(b, coef, "f32"))), rep
+        second.replay()
+        torch.cuda.synchronize()
+        coef = read(nsf, clip)[2]
+        for b, t in zip(before, ts):
+            to = "bf16" if t.dtype == torch.bfloat16 else "f32"
+            assert np.array_equal(bits(host(t)), bits(ao.clip_same_order(b, coef, to))), rep
 
 
 def test_default_workspace_is_refused_under_capture(nsf, torch):
