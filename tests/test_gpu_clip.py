@@ -272,6 +272,31 @@ def test_clip(nsf, torch, name, dtypes, out):
         assert torch.isnan(buf[:lo]).all() and torch.isnan(buf[lo + t.numel():]).all(), k
 
 
+@pytest.mark.parametrize("sdt", ["f32", "bf16"])
+@pytest.mark.parametrize("ddt", ["f32", "bf16"])
+def test_clip_long_lists(nsf, torch, sdt, ddt):
+    """Lists past the size up to which the source stays cached, odd lengths and
+    offsets; one product in float32, rounded once, is torch's too."""
+    say("clip long", sdt, ddt)
+    sizes = [40_000_003, 8192 * 700, 13]
+    ts, _ = make_list(torch, sizes, 13, dtypes=(sdt,))
+    res, bufs = make_list(torch, sizes, 1, dtypes=(ddt,))
+    clip = nsf.clip_state("cuda")
+    nsf.muon_grad_norm(ts, 3.0, clip)
+    nsf.muon_clip_grads(ts, clip, out=res)
+    for t, r, buf in zip(ts, res, bufs):
+        want = (t.float() * clip.coef).to(r.dtype)
+        assert torch.equal(r, want)
+        lo = r.storage_offset()
+        assert torch.isnan(buf[:lo]).all() and torch.isnan(buf[lo + r.numel():]).all()
+    total = sum(t.double().square().sum() for t in ts)
+    s, norm, coef = read(nsf, clip)
+    n = sum(sizes)
+    assert abs(s - float(total)) <= 2 * n * 2.0 ** -53 * s
+    assert abs(norm - math.sqrt(s)) <= HALF * (1 + 1e-6) * norm
+    assert abs(coef - 3.0 / (math.sqrt(s) + 1e-6)) <= HALF * (1 + 1e-6) * coef
+
+
 @pytest.mark.parametrize("sp", range(8))
 def test_clip_alignments(nsf, torch, sp):
     """Every pair of element offsets and types, lengths around the vectors'."""
