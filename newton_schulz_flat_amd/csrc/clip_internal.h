@@ -51,7 +51,7 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 
-constexpr int kClipTensors = 168;
+constexpr int kClipTensors = 169;
 struct ClipArgs {
     const void* src[kClipTensors];
     void* dst[kClipTensors];
@@ -59,6 +59,7 @@ struct ClipArgs {
     const muon_clip_t* clip;
     int32_t n;
     int32_t units;
+    int32_t in_place;  // every dst is its src
 };
 static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments");
 

@@ -338,13 +338,13 @@ __device__ __forceinline__ void scale_unit(const TS* src, TD* dst, int64_t numel
 template <bool kStream>
 __global__ __launch_bounds__(kScaleThreads) void clip_kernel(const ClipArgs a) {
     const float coef = a.clip->coef;
+    // times 1 in place changes nothing
+    if (a.in_place && coef == 1.f) return;
     for (int b = blockIdx.x; b < a.units; b += int(gridDim.x)) {
         const int t = tensor_of(a.meta, a.n, b);
         const uint64_t meta = a.meta[t];
         const void* src = a.src[t];
         void* dst = a.dst[t];
-        // times 1 in place changes nothing
-        if (src == dst && coef == 1.f) continue;
         const int64_t numel = meta_numel(meta), k = b - meta_unit(meta);
         const float* sf = static_cast<const float*>(src);
         const uint16_t* sb = static_cast<const uint16_t*>(src);
@@ -474,6 +474,7 @@ hipError_t launch_clip(const muon_tensor_t* src, const muon_tensor_t* dst, int64
         ClipArgs a;
         int64_t units = 0;
         int m = 0;
+        int32_t in_place = 1;
         while (i < n && m < kClipTensors) {
             // a run of tensors adjacent on both sides is one
             muon_tensor_t x = src[i], y = dst[i];
@@ -483,6 +484,7 @@ hipError_t launch_clip(const muon_tensor_t* src, const muon_tensor_t* dst, int64
                 y.numel = x.numel;
                 ++i;
             }
+            if (x.numel > 0 && x.data != y.data) in_place = 0;
             a.src[m] = x.data;
             a.dst[m] = y.data;
             a.meta[m] = clip_meta(x.numel, x.dtype == MUON_DTYPE_BF16, y.dtype == MUON_DTYPE_BF16,
@@ -490,7 +492,7 @@ hipError_t launch_clip(const muon_tensor_t* src, const muon_tensor_t* dst, int64
             units += units_of(x.numel, kScaleUnit);
             ++m;
         }
-        a.clip = clip, a.n = m, a.units = int32_t(units);
+        a.clip = clip, a.n = m, a.units = int32_t(units), a.in_place = in_place;
         const int64_t grid = std::min<int64_t>(units, kMaxGrid);
         LaunchTimer timer("clip", s);
         const auto kernel = keep ? clip_kernel<false> : clip_kernel<true>;

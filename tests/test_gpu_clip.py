@@ -336,6 +336,22 @@ def test_clip_special_values(nsf, torch):
             assert np.array_equal(bits(got)[ok], bits(want)[ok])
 
 
+def test_clip_by_one(nsf, torch):
+    """A coefficient of 1: in place nothing changes (the bits of NaN among it), into
+    other tensors everything arrives, also where a list has both."""
+    say("clip by one")
+    clip = nsf.clip_state("cuda")
+    nsf.clip_coef(clip).fill_(1.0)
+    raw = torch.tensor([0x7f800001, 0x7fc12345, 0x3f800000, 0xff812345 - (1 << 32)] * 5000,
+                       dtype=torch.int32, device="cuda").view(torch.float32)
+    a, b = raw.clone(), torch.randn(9001, device="cuda").bfloat16()
+    nsf.muon_clip_grads([a, b], clip)
+    assert torch.equal(a.view(torch.int32), raw.view(torch.int32))
+    c, d = b.clone(), torch.zeros(9001, device="cuda")
+    nsf.muon_clip_grads([c, b], clip, out=[c, d])
+    assert torch.equal(c, b) and torch.equal(d, b.float())
+
+
 # ---------------------------------------------------------------------- AdamW
 
 GROUPS = [(1e-3, 0.1, 0.9, 0.999, 1e-8, 1), (2e-2, 0.0, 0.5, 0.95, 1e-6, 7),
