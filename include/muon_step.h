@@ -335,9 +335,9 @@ int muon_clip_finish(muon_clip_t* clip, float max_norm, hipStream_t stream);
 
 /* dst[i] = coef * src[i], in float32, rounded once to dst's type (nearest
  * even), for every element of every tensor.  Lists have the same lengths;
- * types may differ.  A dst may be its src (same address and type: in place,
- * where nothing is read or written while coef is 1); apart from that no dst
- * may overlap another dst or a src. */
+ * types may differ.  A dst may be its src (same address and type: in place; a
+ * list that is so throughout is neither read nor written while coef is 1);
+ * apart from that no dst may overlap another dst or a src. */
 int muon_clip_grads(const muon_tensor_t* src, const muon_tensor_t* dst, int64_t n,
                     const muon_clip_t* clip, hipStream_t stream);
 

@@ -22,7 +22,7 @@ namespace muon {
 namespace {
 
 // The norm: 1024 workgroups of 256 threads, 8 vectors of 16 bytes in flight per
-// thread.  7 G float32 elements 3.99 ms (7.0 TB/s), 218 M bfloat16 72 us.  Of 512 to
+// thread.  7 G float32 elements 3.98 ms (7.0 TB/s), 218 M bfloat16 65 us (6.7).  Of 512 to
 // 16384 workgroups, 128 to 1024 threads and 2 to 8 vectors the ones near this lie
 // within 1%; half the vectors with double the workgroups 1.5% more, 2 vectors
 // 5% more, 8192 workgroups (more partials, less of each tensor) 3% more.  Plain
@@ -68,7 +68,7 @@ __device__ __forceinline__ int tensor_of(const uint64_t* meta, int n, int u) {
 
 // Sum over the workgroup, in a fixed order, for every thread.  The barriers make
 // `lds` free again on return.
-template <int kWaves>
+template <int kCount>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
@@ -76,7 +76,7 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
     __syncthreads();
     double t = lds[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) t += lds[w];
+    for (int w = 1; w < kCount; ++w) t += lds[w];
     __syncthreads();
     return t;
 }
@@ -112,7 +112,7 @@ __device__ __forceinline__ u32x4_stream load_vector(const u32x4_stream* v) {
 // Share of thread `me` of kStep in the sum of squares of p[begin, end): elements
 // before the first and behind the last 16-byte boundary one by one, whole
 // vectors between them.
-template <int kStep, int kFlight, bool kStream, typename T>
+template <int kStep, int kLoads, bool kStream, typename T>
 __device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t begin, int64_t end,
                                               int me) {
     constexpr int V = 16 / sizeof(T);
@@ -124,12 +124,12 @@ __device__ __forceinline__ double sum_squares(const T* __restrict__ p, int64_t b
     double acc[4] = {0., 0., 0., 0.};
     const u32x4_stream* v = reinterpret_cast<const u32x4_stream*>(first + head);
     int64_t i = me;
-    for (; i + (kFlight - 1) * kStep < nvec; i += kFlight * kStep) {
-        u32x4_stream q[kFlight];
+    for (; i + (kLoads - 1) * kStep < nvec; i += kLoads * kStep) {
+        u32x4_stream q[kLoads];
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) q[k] = load_vector<kStream>(v + i + k * kStep);
+        for (int k = 0; k < kLoads; ++k) q[k] = load_vector<kStream>(v + i + k * kStep);
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) add_vector(q[k], p, acc);
+        for (int k = 0; k < kLoads; ++k) add_vector(q[k], p, acc);
     }
     for (; i < nvec; i += kStep) add_vector(load_vector<kStream>(v + i), p, acc);
     if (me < head) acc[0] = square_add(acc[0], element(first + me));
@@ -239,10 +239,10 @@ __global__ __launch_bounds__(kSoloThreads) void norm_solo_kernel(const NormArgs 
         if (begin >= end) continue;
         if (meta_src(meta))
             s += sum_squares<64, 2, false>(static_cast<const uint16_t*>(a.data[t]), begin, end,
-                                    threadIdx.x & 63);
+                                           threadIdx.x & 63);
         else
             s += sum_squares<64, 4, false>(static_cast<const float*>(a.data[t]), begin, end,
-                                    threadIdx.x & 63);
+                                           threadIdx.x & 63);
     }
     s = block_sum<kSoloWaves>(s, lds);
     if (threadIdx.x == 0) finish(clip, s, max_norm);

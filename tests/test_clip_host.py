@@ -274,23 +274,77 @@ def test_oracle_sumsq_and_coefficient():
     assert math.isnan(ao.coefficient(math.nan, 1.0))
 
 
-def test_oracle_adamw_closed_forms():
+def adamw_pins(step):
+    """Closed forms that a step function (w, g, m, v, group, coef) has to meet."""
     z = np.zeros(1, np.float64)
     one = np.ones(1, np.float64)
     # from zero state, the first update is lr * sign(g) up to eps, whatever the size of g
     for g in (1e-3, -7.0, 1e4):
-        w, m, v = ao.adamw(z, one * g, z, z, (0.5, 0.0, 0.875, 0.75, 0.0, 1))
+        w, m, v = step(z, one * g, z, z, (0.5, 0.0, 0.875, 0.75, 0.0, 1), 1.0)
         assert abs(w[0] + 0.5 * math.copysign(1, g)) < 1e-12
         assert m[0] == 0.125 * g and v[0] == 0.25 * g * g
     # no gradient, no state: decay alone
-    w, _, _ = ao.adamw(one, z, z, z, (0.5, 0.25, 0.875, 0.75, 1e-8, 3))
+    w, _, _ = step(one, z, z, z, (0.5, 0.25, 0.875, 0.75, 0.5, 3), 1.0)
     assert w[0] == 1 - 0.125
+    # decay acts on the old weight alone: w (1 - lr wd) - lr sign(g)
+    w, _, _ = step(one * 4, one, z, z, (0.5, 0.25, 0.875, 0.75, 0.0, 1), 1.0)
+    assert abs(w[0] - (4 * 0.875 - 0.5)) < 1e-12
+    # eps beside the root of the corrected moment: g / (|g| + eps)
+    w, _, _ = step(z, one, z, z, (0.5, 0.0, 0.875, 0.75, 3.0, 1), 1.0)
+    assert abs(w[0] + 0.5 / 4) < 1e-12
     # constant gradient: m and v are 1 - beta^t of g and g^2, so every step is lr * sign(g)
     w, m, v = z, z, z
     for t in range(1, 30):
-        w, m, v = ao.adamw(w, one * 2.0, m, v, (0.25, 0.0, 0.875, 0.75, 0.0, t), coef=0.5)
+        w, m, v = step(w, one * 2.0, m, v, (0.25, 0.0, 0.875, 0.75, 0.0, t), 0.5)
     assert abs(m[0] - (1 - 0.875 ** 29)) < 1e-12 and abs(v[0] - (1 - 0.75 ** 29)) < 1e-12
     assert abs(w[0] + 0.25 * 29) < 1e-12
+
+
+def test_oracle_adamw_closed_forms():
+    adamw_pins(ao.adamw)
+
+
+def planted(mistake):
+    def step(w, g, m, v, group, coef):
+        lr, wd, b1, b2, eps, t = group
+        raw = g
+        if mistake != "coefficient dropped":
+            g = g * coef
+        if mistake == "decay in the gradient":
+            g = g + wd * w
+        m = b1 * m + (1 - b1) * g
+        v = b2 * v + (1 - b2) * (raw if mistake == "coefficient once in v" else g) * g
+        h = m / (1 - b1 ** (t - 1 if mistake == "step off by one" and t > 1 else t))
+        if mistake == "m not corrected":
+            h = m
+        u = v if mistake == "v not corrected" else v / (1 - b2 ** t)
+        root = np.sqrt(u + eps) if mistake == "eps in the root" else np.sqrt(u) + eps
+        with np.errstate(all="ignore"):
+            upd = np.nan_to_num(h / root)
+        if mistake == "decay after the update":
+            w = (w - lr * upd) * (1 - lr * wd)
+        elif mistake == "decay without lr":
+            w = w - wd * w - lr * upd
+        elif mistake == "decay in the gradient":
+            w = w - lr * upd
+        elif mistake == "betas swapped":
+            return planted("")(w, raw, m, v, (lr, wd, b2, b1, eps, t), coef)
+        else:
+            w = w - lr * wd * w - lr * upd
+        return w, m, v
+    return step
+
+
+MISTAKES = ["coefficient dropped", "decay in the gradient", "coefficient once in v",
+            "step off by one", "m not corrected", "v not corrected", "eps in the root",
+            "decay after the update", "decay without lr", "betas swapped"]
+
+
+@pytest.mark.parametrize("mistake", MISTAKES)
+def test_oracle_adamw_pins_find_mistakes(mistake):
+    adamw_pins(planted(""))
+    with pytest.raises(AssertionError):
+        adamw_pins(planted(mistake))
 
 
 def test_oracle_same_order_is_near_the_definition():

@@ -10,6 +10,7 @@
   eagerly and in a captured graph replayed with other gradients.
 """
 
+import dataclasses
 import math
 
 import numpy as np
@@ -516,6 +517,32 @@ def test_step_clipped_equals_clip_then_step(nsf, torch, mode, ns_steps, max_norm
     assert np.array_equal(bits(host(mom)), bits(host(m2)))
     coef = read(nsf, clip)[2]
     assert (coef == 1.0) == (max_norm > 1)
+
+
+@pytest.mark.parametrize("coef", [0.3, math.nan])
+def test_step_clipped_groups_copy_and_waves(nsf, torch, coef):
+    """float32 weights with model copy, three groups, tall and wide and unaligned rows, in
+    one wave and in several."""
+    wl = wlm.small_mixed(43, count=8, max_side=330, param_dtype="f32")
+    say("step_clipped groups, copy, waves", coef)
+    descs = [dataclasses.replace(d, group=k % 3) for k, d in enumerate(wl.descs)]
+    params, grads, mom = wlm.make_tensors(wl, "cuda", momentum_std=1e-3)
+    table = nsf.group_table([(0.02, 0.01, 0.95, True), (0.005, 0.0, 0.9, False),
+                             (0.05, 0.1, 0.8, True)], "cuda")
+    clip = nsf.clip_state("cuda")
+    nsf.clip_coef(clip).fill_(coef)
+    p0, m0, g0 = params.clone(), mom.clone(), grads.clone()
+    c0 = torch.zeros(params.numel(), dtype=torch.bfloat16, device="cuda")
+    nsf.muon_clip_grads([g0], clip)
+    nsf.muon_step_grouped(p0, g0, m0, descs, table, model_copy=c0)
+    for size in (nsf.muon_workspace_bytes(descs), nsf.muon_workspace_min_bytes(descs)):
+        p1, m1, c1 = params.clone(), mom.clone(), torch.zeros_like(c0)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        nsf.muon_step_clipped(p1, grads, m1, descs, table, clip, model_copy=c1, workspace=ws)
+        torch.cuda.synchronize()
+        for a, b in ((p0, p1), (m0, m1), (c0, c1)):
+            x, y = ao.widen(host(a)), ao.widen(host(b))
+            assert np.array_equal(x, y, equal_nan=True)
 
 
 def small_training(nsf, torch, seed):
