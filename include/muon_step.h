@@ -57,7 +57,8 @@
  * who keeps ownership.  Descriptor arrays are host memory read during the
  * call.  The workspace is caller-owned device memory, 256-byte aligned; its
  * contents are undefined after a call.  Calls that share a workspace must be
- * ordered on one stream.  With muon_workspace_bytes() bytes every matrix is
+ * ordered on one stream and made one after the other: a call is several
+ * launches, and those of calls made by two threads at once may mix.  With muon_workspace_bytes() bytes every matrix is
  * orthogonalized in one wave; a smaller workspace of at least
  * muon_workspace_min_bytes() bytes runs the matrices in waves, each wave's
  * intermediates fitting the workspace (the pages' optimizer likewise works
@@ -322,7 +323,8 @@ int muon_clip_workspace_bytes(const muon_tensor_t* tensors, int64_t n, size_t* o
  *   clip          receives the record (n == 0: sumsq = norm = 0).
  *   tensor_norms  NULL, or device float32 [n]: the norm of every tensor.
  *   workspace     device, >= muon_clip_workspace_bytes(); calls that share it
- *                 (or a record) must be ordered on one stream.
+ *                 (or a record) must be ordered on one stream and made one
+ *                 after the other, not by two threads at once.
  * Tensors may overlap each other (each counts in full); the record, the norms
  * and the workspace may not overlap anything. */
 int muon_grad_norm(const muon_tensor_t* tensors, int64_t n, float max_norm, muon_clip_t* clip,

@@ -45,8 +45,10 @@ Where ranks hold parts of the gradient, ``dist.all_reduce(clip_sumsq(clip))`` an
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import threading
 from typing import Iterable, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -259,6 +261,30 @@ def workspace_for(descs, mode: str, device):
     return ws
 
 
+#: Locks of the default workspaces, one per (device, stream).  A call is several
+#: launches that hand results on through its workspace, and threads on one
+#: stream share the default one: each enqueues its whole call under the lock, so that
+#: stream order keeps calls apart as well as launches.
+_stream_locks: dict = {}
+
+
+def _stream_lock(device):
+    import torch
+    key = (device, torch.cuda.current_stream(device).cuda_stream)
+    return _stream_locks.setdefault(key, threading.RLock())
+
+
+@contextlib.contextmanager
+def _workspace(given, descs, mode, device):
+    """The workspace of a call that is enqueued inside this context: ``given``, or the default
+    one under its lock."""
+    if given is not None:
+        yield given
+    else:
+        with _stream_lock(device):
+            yield workspace_for(descs, mode, device)
+
+
 def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, beta: float,
               nesterov: bool = True, ns_steps: int = 5, mode: str = "bf16", workspace=None):
     """One Muon step in place on ``params`` (f32 or bf16) and ``momentum`` (f32).
@@ -271,15 +297,14 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(grads, "grads", (torch.float32,))
     _require(momentum, "momentum", (torch.float32,))
-    if workspace is None:
-        workspace = workspace_for(descs, mode, grads.device)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    check(lib.muon_step(params.data_ptr(), dt, params.numel(), grads.data_ptr(),
-                        momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
-                        lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps), _mode(mode),
-                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                        _stream(grads)))
+    with _workspace(workspace, descs, mode, grads.device) as ws:
+        check(lib.muon_step(params.data_ptr(), dt, params.numel(), grads.data_ptr(),
+                            momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
+                            lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
+                            _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
+                            _stream(grads)))
 
 
 def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: float,
@@ -346,19 +371,18 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
         if model_copy.numel() != params.numel():
             raise ValueError("model_copy must have as many elements as params")
         copy_ptr = model_copy.data_ptr()
-    if workspace is None:
-        workspace = workspace_for(descs, mode, grads.device)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     head = (params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
             momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
             groups.data_ptr(), groups.shape[0])
-    tail = (int(ns_steps), _mode(mode), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(grads))
-    if clip is None:
-        check(lib.muon_step_grouped(*head, *tail))
-    else:
-        check(lib.muon_step_clipped(*head, clip.record.data_ptr(), *tail))
+    with _workspace(workspace, descs, mode, grads.device) as ws:
+        tail = (int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
+                _stream(grads))
+        if clip is None:
+            check(lib.muon_step_grouped(*head, *tail))
+        else:
+            check(lib.muon_step_clipped(*head, clip.record.data_ptr(), *tail))
 
 
 def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = True):
@@ -377,12 +401,12 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     import torch
     _require(u, "u", (torch.float32,))
     _require(o_out, "o_out", (torch.float32,))
-    if workspace is None:
-        workspace = workspace_for(descs, mode, u.device)
     lib = load_library()
-    check(lib.muon_orthogonalize(u.data_ptr(), o_out.data_ptr(), u.numel(), descs_array(descs),
-                                 _count(descs), int(ns_steps), _mode(mode), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(u)))
+    with _workspace(workspace, descs, mode, u.device) as ws:
+        check(lib.muon_orthogonalize(u.data_ptr(), o_out.data_ptr(), u.numel(),
+                                     descs_array(descs), _count(descs), int(ns_steps),
+                                     _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     _stream(u)))
 
 
 def muon_apply(params, updates, descs, lr: float, weight_decay: float):
@@ -538,14 +562,17 @@ def muon_grad_norm(tensors, max_norm: float, clip, tensor_norms=None, workspace=
         if tensor_norms.numel() != len(tl) or tensor_norms.device != clip.device:
             raise ValueError("tensor_norms must have one element per tensor, on their device")
         norms_ptr = tensor_norms.data_ptr()
+    head = (clip.device.index, load_library().muon_grad_norm, tl.array, len(tl), max_norm,
+            clip.record.data_ptr(), norms_ptr)
     if workspace is None:
-        workspace = _clip_workspace_for(tl, clip.device)
+        with _stream_lock(clip.device):
+            workspace = _clip_workspace_for(tl, clip.device)
+            _launch(*head, workspace.data_ptr(), workspace.numel())
     else:
         _require(workspace, "workspace", (torch.uint8,))
         if workspace.device != clip.device:
             raise ValueError("workspace is on another device than the tensors")
-    _launch(clip.device.index, load_library().muon_grad_norm, tl.array, len(tl), max_norm,
-            clip.record.data_ptr(), norms_ptr, workspace.data_ptr(), workspace.numel())
+        _launch(*head, workspace.data_ptr(), workspace.numel())
 
 
 def muon_clip_finish(clip, max_norm: float):

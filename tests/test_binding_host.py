@@ -1,0 +1,193 @@
+"""Host tests of what the binding does around a call: which workspace it takes,
+which device it launches on and which tensors it refuses.  The library and the
+GPU are stand-ins here; nothing is computed."""
+
+import contextlib
+import threading
+import time
+import types
+
+import pytest
+
+import newton_schulz_flat_amd as nsf
+
+
+class Library:
+    """Stands in for the library: every call is noted with the device that was current."""
+
+    def __init__(self, gpu, pause=0.0):
+        self.gpu, self.pause, self.calls, self.events = gpu, pause, [], []
+
+    def __getattr__(self, name):
+        if not name.startswith("muon_"):
+            raise AttributeError(name)
+
+        def call(*args):
+            self.events.append((name, "begins", threading.get_ident()))
+            time.sleep(self.pause)
+            self.calls.append((name, self.gpu["device"], args))
+            self.events.append((name, "ends", threading.get_ident()))
+            return 0
+        return call
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """Two GPUs of which device 0 is current; stream handles are 100 + device."""
+    import torch
+    state = {"device": 0, "capturing": None}
+
+    @contextlib.contextmanager
+    def device(d):
+        before = state["device"]
+        state["device"] = d if isinstance(d, int) else torch.device(d).index
+        try:
+            yield
+        finally:
+            state["device"] = before
+
+    def stream(d=None):
+        index = state["device"] if d is None else d if isinstance(d, int) else torch.device(d).index
+        return types.SimpleNamespace(cuda_stream=100 + index, device_index=index)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["device"])
+    monkeypatch.setattr(torch.cuda, "current_stream", stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+                        lambda: state["capturing"] == state["device"])
+    monkeypatch.setattr(nsf, "_current_stream", lambda index: 100 + index)
+    monkeypatch.setattr(nsf, "_require", lambda t, name, dtypes: None)
+    monkeypatch.setattr(nsf, "_require_clip", lambda clip, device: None)
+    real_empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: real_empty(*a, **kw))
+    for name in ("_workspaces", "_clip_workspaces"):
+        monkeypatch.setattr(nsf, name, {})
+    return state
+
+
+class Tensor:
+    """What the binding asks of a tensor; device memory that is never touched."""
+
+    def __init__(self, numel, dtype, device=0, at=1 << 40, shape=None):
+        import torch
+        self.n, self.dtype, self.at = numel, dtype, at
+        self.device = torch.device("cuda", device)
+        self.shape = shape or (numel,)
+        self.is_cuda = True
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        import torch
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def get_device(self):
+        return self.device.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+
+def record(device=0):
+    import torch
+    return types.SimpleNamespace(record=Tensor(2, torch.float64, device),
+                                 device=torch.device("cuda", device))
+
+
+DESCS = [(0, 8, 16)]
+
+
+def step_buffers(**devices):
+    """Buffers of a step on the matrix of DESCS, on device 0 but for those named."""
+    import torch
+    at = lambda name: devices.get(name, devices.get("all", 0))
+    return dict(params=Tensor(128, torch.bfloat16, at("params")),
+                grads=Tensor(128, torch.float32, at("grads")),
+                momentum=Tensor(128, torch.float32, at("momentum")),
+                u_out=Tensor(128, torch.float32, at("u_out")),
+                groups=Tensor(4, torch.int32, at("groups"), shape=(1, 4)),
+                workspace=Tensor(1 << 20, torch.uint8, at("workspace")))
+
+
+def calls(b, workspace=True):
+    """Every entry point that launches a Muon step or a part of it."""
+    ws = dict(workspace=b["workspace"]) if workspace else {}
+    clip = record(b["grads"].device.index)
+    p, g, m = b["params"], b["grads"], b["momentum"]
+    every = {
+        "muon_step": lambda: nsf.muon_step(p, g, m, DESCS, 0.1, 0.1, 0.9, **ws),
+        "muon_step_grouped": lambda: nsf.muon_step_grouped(p, g, m, DESCS, b["groups"], **ws),
+        "muon_step_clipped": lambda: nsf.muon_step_clipped(p, g, m, DESCS, b["groups"], clip, **ws),
+        "muon_orthogonalize": lambda: nsf.muon_orthogonalize(g, b["u_out"], DESCS, **ws),
+    }
+    if workspace:
+        every.update({
+            "muon_step_noalloc": lambda: nsf.muon_step_noalloc(p, g, m, DESCS, 0.1, 0.1, 0.9),
+            "muon_momentum": lambda: nsf.muon_momentum(g, m, b["u_out"], DESCS, 0.9),
+            "muon_apply": lambda: nsf.muon_apply(p, g, DESCS, 0.1, 0.1),
+        })
+    return every
+
+
+# ------------------------------------------------- two threads on one stream
+
+def overlap(events):
+    """Whether a call began while another thread's was under way."""
+    open_calls = set()
+    for _, what, who in events:
+        if what == "begins":
+            if open_calls:
+                return True
+            open_calls.add(who)
+        else:
+            open_calls.discard(who)
+    return False
+
+
+def from_two_threads(call):
+    threads = [threading.Thread(target=call) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+
+
+def default_workspace_calls():
+    import torch
+    tensors = nsf.tensor_list([Tensor(1000, torch.float32)])
+    every = calls(step_buffers(), workspace=False)
+    every["muon_grad_norm"] = lambda: nsf.muon_grad_norm(tensors, 1.0, record())
+    return every
+
+
+@pytest.mark.parametrize("name", ["muon_grad_norm", "muon_step", "muon_step_grouped",
+                                  "muon_step_clipped", "muon_orthogonalize"])
+def test_calls_that_share_a_default_workspace_do_not_overlap(gpu, monkeypatch, name):
+    """A call is several launches that pass results on through the workspace: two threads
+    on one stream share the default one, and one call's launches must all be
+    enqueued before the other's first."""
+    lib = Library(gpu, pause=0.05)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    monkeypatch.setattr(nsf, "muon_workspace_bytes", lambda descs, mode="bf16": 4096)
+    monkeypatch.setattr(nsf, "muon_clip_workspace_bytes", lambda tensors: 4096)
+    call = default_workspace_calls()[name]
+    call()                         # the workspace exists from here on
+    lib.events.clear()
+    from_two_threads(call)
+    assert [n for n, _, _ in lib.calls] == [name] * 3
+    assert not overlap(lib.events)
+
+
+def test_calls_with_their_own_workspaces_may_overlap(gpu, monkeypatch):
+    """Nothing waits where the caller names the workspace."""
+    lib = Library(gpu, pause=0.2)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    from_two_threads(calls(step_buffers())["muon_step"])
+    assert overlap(lib.events)
