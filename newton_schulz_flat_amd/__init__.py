@@ -197,9 +197,25 @@ def _mode(mode: str) -> int:
         raise ValueError(f"mode must be one of {sorted(_MODES)}, got {mode!r}") from None
 
 
-def _stream(t):
+def _launch(index: int, call, *args) -> None:
+    """``call(*args, stream)`` on the current stream of GPU ``index``.  Launches go to the
+    current device, which another one than ``index`` gives way for the call."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            check(call(*args, _current_stream(index)))
+    else:
+        check(call(*args, _current_stream(index)))
+
+
+def _current_stream(index: int) -> int:
+    """Handle of the current stream, without the stream object that
+    ``torch.cuda.current_stream`` makes around it (1 us a call)."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _require(t, name, dtypes):
@@ -241,13 +257,24 @@ def muon_workspace_min_bytes(descs, mode: str = "bf16") -> int:
 _workspaces: dict = {}
 
 
+def _capturing(dev) -> bool:
+    """Whether the current stream of ``dev``, or that of the current device, is being captured."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return False
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def workspace_for(descs, mode: str, device):
     """A cached uint8 workspace of at least the one-wave size, for the current
     stream of ``device``.  Not usable under graph capture (the graph would keep
     a pointer that a later, larger set frees): pass an explicit workspace there."""
     import torch
     dev = torch.device(device)
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(dev):
         raise RuntimeError("pass an explicit workspace to calls made under graph capture")
     stream = torch.cuda.current_stream(dev)
     need = muon_workspace_bytes(descs, mode)
@@ -300,11 +327,10 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     with _workspace(workspace, descs, mode, grads.device) as ws:
-        check(lib.muon_step(params.data_ptr(), dt, params.numel(), grads.data_ptr(),
-                            momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
-                            lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
-                            _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
-                            _stream(grads)))
+        _launch(grads.get_device(), lib.muon_step, params.data_ptr(), dt, params.numel(),
+                grads.data_ptr(), momentum.data_ptr(), grads.numel(), descs_array(descs),
+                _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
+                _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: float,
@@ -318,10 +344,10 @@ def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: f
     _require(momentum, "momentum", (torch.float32,))
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    check(lib.muon_step_noalloc(params.data_ptr(), dt, params.numel(), grads.data_ptr(),
-                                momentum.data_ptr(), grads.numel(), descs_array(descs),
-                                _count(descs), lr, weight_decay, beta, int(bool(nesterov)),
-                                int(ns_steps), _mode(mode), _stream(grads)))
+    _launch(grads.get_device(), lib.muon_step_noalloc, params.data_ptr(), dt, params.numel(),
+            grads.data_ptr(), momentum.data_ptr(), grads.numel(), descs_array(descs),
+            _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
+            _mode(mode))
 
 
 def group_table(groups, device):
@@ -377,12 +403,11 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
             momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
             groups.data_ptr(), groups.shape[0])
     with _workspace(workspace, descs, mode, grads.device) as ws:
-        tail = (int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
-                _stream(grads))
+        tail = (int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
         if clip is None:
-            check(lib.muon_step_grouped(*head, *tail))
+            _launch(grads.get_device(), lib.muon_step_grouped, *head, *tail)
         else:
-            check(lib.muon_step_clipped(*head, clip.record.data_ptr(), *tail))
+            _launch(grads.get_device(), lib.muon_step_clipped, *head, clip.record.data_ptr(), *tail)
 
 
 def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = True):
@@ -391,9 +416,9 @@ def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = T
     for t, nm in ((grads, "grads"), (momentum, "momentum"), (u_out, "u_out")):
         _require(t, nm, (torch.float32,))
     lib = load_library()
-    check(lib.muon_momentum(grads.data_ptr(), momentum.data_ptr(), u_out.data_ptr(),
-                            grads.numel(), descs_array(descs), _count(descs), beta,
-                            int(bool(nesterov)), _stream(grads)))
+    _launch(grads.get_device(), lib.muon_momentum, grads.data_ptr(), momentum.data_ptr(),
+            u_out.data_ptr(), grads.numel(), descs_array(descs), _count(descs), beta,
+            int(bool(nesterov)))
 
 
 def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", workspace=None):
@@ -403,10 +428,9 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     _require(o_out, "o_out", (torch.float32,))
     lib = load_library()
     with _workspace(workspace, descs, mode, u.device) as ws:
-        check(lib.muon_orthogonalize(u.data_ptr(), o_out.data_ptr(), u.numel(),
-                                     descs_array(descs), _count(descs), int(ns_steps),
-                                     _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _stream(u)))
+        _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(), u.numel(),
+                descs_array(descs), _count(descs), int(ns_steps), _mode(mode), ws.data_ptr(),
+                ws.numel() * ws.element_size())
 
 
 def muon_apply(params, updates, descs, lr: float, weight_decay: float):
@@ -416,9 +440,9 @@ def muon_apply(params, updates, descs, lr: float, weight_decay: float):
     _require(updates, "updates", (torch.float32,))
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    check(lib.muon_apply(params.data_ptr(), dt, params.numel(), updates.data_ptr(),
-                         updates.numel(), descs_array(descs), _count(descs), lr, weight_decay,
-                         _stream(updates)))
+    _launch(updates.get_device(), lib.muon_apply, params.data_ptr(), dt, params.numel(),
+            updates.data_ptr(), updates.numel(), descs_array(descs), _count(descs), lr,
+            weight_decay)
 
 
 class ClipState:
@@ -492,27 +516,6 @@ def tensor_list(tensors) -> TensorList:
     """``tensors`` as a list that the norm and clipping calls take as it is: a
     program that keeps its gradient buffers makes it once."""
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
-
-
-def _launch(index: int, call, *args) -> None:
-    """``call(*args, stream)`` on the current stream of GPU ``index``.  Launches go to the
-    current device, which another one than ``index`` gives way for the call."""
-    import torch
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            check(call(*args, _current_stream(index)))
-    else:
-        check(call(*args, _current_stream(index)))
-
-
-def _current_stream(index: int) -> int:
-    """Handle of the current stream, without the stream object that
-    ``torch.cuda.current_stream`` makes around it (1 us a call)."""
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(index)
-    except AttributeError:
-        return torch.cuda.current_stream(index).cuda_stream
 
 
 def muon_clip_workspace_bytes(tensors) -> int:

@@ -191,3 +191,36 @@ def test_calls_with_their_own_workspaces_may_overlap(gpu, monkeypatch):
     monkeypatch.setattr(nsf, "load_library", lambda: lib)
     from_two_threads(calls(step_buffers())["muon_step"])
     assert overlap(lib.events)
+
+
+# ------------------------------------------------------------ another device
+
+EVERY = ["muon_step", "muon_step_grouped", "muon_step_clipped", "muon_orthogonalize",
+         "muon_step_noalloc", "muon_momentum", "muon_apply"]
+
+
+@pytest.mark.parametrize("index", [0, 1])
+@pytest.mark.parametrize("name", EVERY)
+def test_steps_launch_on_the_device_of_their_tensors(gpu, monkeypatch, name, index):
+    """Kernels go to the current device, plans belong to it: it has to be the tensors' while
+    the library runs, and what it was before afterwards."""
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    calls(step_buffers(all=index))[name]()
+    (called, current, args), = lib.calls
+    stream = getattr(args[-1], "value", args[-1])
+    assert (called, current, stream) == (name, index, 100 + index)
+    assert gpu["device"] == 0
+
+
+@pytest.mark.parametrize("name", ["muon_step", "muon_step_clipped", "muon_orthogonalize"])
+def test_default_workspace_refused_under_capture_on_another_device(gpu, monkeypatch, name):
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    monkeypatch.setattr(nsf, "muon_workspace_bytes", lambda descs, mode="bf16": 4096)
+    gpu["capturing"] = 1
+    with pytest.raises(RuntimeError, match="explicit workspace"):
+        calls(step_buffers(all=1), workspace=False)[name]()
+    assert not lib.calls
+    calls(step_buffers(all=1))[name]()      # one of its own is fine
+    assert len(lib.calls) == 1
