@@ -232,6 +232,13 @@ def _require(t, name, dtypes):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _together(first, first_name: str, **others) -> None:
+    """Refuses tensors on another device than ``first``."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, {first_name} on {first.device}")
+
+
 def muon_workspace_bytes(descs, mode: str = "bf16") -> int:
     """Workspace bytes with which the descriptors run in one wave."""
     lib = load_library()
@@ -306,6 +313,10 @@ def _workspace(given, descs, mode, device):
     """The workspace of a call that is enqueued inside this context: ``given``, or the default
     one under its lock."""
     if given is not None:
+        if given.device != device:
+            raise ValueError(f"workspace is on {given.device}, the tensors on {device}")
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         yield given
     else:
         with _stream_lock(device):
@@ -324,6 +335,7 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(grads, "grads", (torch.float32,))
     _require(momentum, "momentum", (torch.float32,))
+    _together(grads, "grads", params=params, momentum=momentum)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     with _workspace(workspace, descs, mode, grads.device) as ws:
@@ -342,6 +354,7 @@ def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: f
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(grads, "grads", (torch.float32,))
     _require(momentum, "momentum", (torch.float32,))
+    _together(grads, "grads", params=params, momentum=momentum)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     _launch(grads.get_device(), lib.muon_step_noalloc, params.data_ptr(), dt, params.numel(),
@@ -397,6 +410,8 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
         if model_copy.numel() != params.numel():
             raise ValueError("model_copy must have as many elements as params")
         copy_ptr = model_copy.data_ptr()
+    _together(grads, "grads", params=params, momentum=momentum, groups=groups,
+              model_copy=model_copy)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     head = (params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
@@ -415,6 +430,7 @@ def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = T
     import torch
     for t, nm in ((grads, "grads"), (momentum, "momentum"), (u_out, "u_out")):
         _require(t, nm, (torch.float32,))
+    _together(grads, "grads", momentum=momentum, u_out=u_out)
     lib = load_library()
     _launch(grads.get_device(), lib.muon_momentum, grads.data_ptr(), momentum.data_ptr(),
             u_out.data_ptr(), grads.numel(), descs_array(descs), _count(descs), beta,
@@ -426,6 +442,7 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     import torch
     _require(u, "u", (torch.float32,))
     _require(o_out, "o_out", (torch.float32,))
+    _together(u, "u", o_out=o_out)
     lib = load_library()
     with _workspace(workspace, descs, mode, u.device) as ws:
         _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(), u.numel(),
@@ -438,6 +455,7 @@ def muon_apply(params, updates, descs, lr: float, weight_decay: float):
     import torch
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(updates, "updates", (torch.float32,))
+    _together(updates, "updates", params=params)
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     _launch(updates.get_device(), lib.muon_apply, params.data_ptr(), dt, params.numel(),

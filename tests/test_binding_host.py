@@ -113,6 +113,7 @@ def step_buffers(**devices):
                 momentum=Tensor(128, torch.float32, at("momentum")),
                 u_out=Tensor(128, torch.float32, at("u_out")),
                 groups=Tensor(4, torch.int32, at("groups"), shape=(1, 4)),
+                model_copy=Tensor(128, torch.bfloat16, at("model_copy")),
                 workspace=Tensor(1 << 20, torch.uint8, at("workspace")))
 
 
@@ -123,8 +124,10 @@ def calls(b, workspace=True):
     p, g, m = b["params"], b["grads"], b["momentum"]
     every = {
         "muon_step": lambda: nsf.muon_step(p, g, m, DESCS, 0.1, 0.1, 0.9, **ws),
-        "muon_step_grouped": lambda: nsf.muon_step_grouped(p, g, m, DESCS, b["groups"], **ws),
-        "muon_step_clipped": lambda: nsf.muon_step_clipped(p, g, m, DESCS, b["groups"], clip, **ws),
+        "muon_step_grouped": lambda: nsf.muon_step_grouped(p, g, m, DESCS, b["groups"],
+                                                           model_copy=b["model_copy"], **ws),
+        "muon_step_clipped": lambda: nsf.muon_step_clipped(p, g, m, DESCS, b["groups"], clip,
+                                                           model_copy=b["model_copy"], **ws),
         "muon_orthogonalize": lambda: nsf.muon_orthogonalize(g, b["u_out"], DESCS, **ws),
     }
     if workspace:
@@ -223,4 +226,43 @@ def test_default_workspace_refused_under_capture_on_another_device(gpu, monkeypa
         calls(step_buffers(all=1), workspace=False)[name]()
     assert not lib.calls
     calls(step_buffers(all=1))[name]()      # one of its own is fine
+    assert len(lib.calls) == 1
+
+
+# name -> the buffers that its calls take beside grads
+TAKES = {"muon_step": ["params", "momentum", "workspace"],
+         "muon_step_grouped": ["params", "momentum", "groups", "model_copy", "workspace"],
+         "muon_step_clipped": ["params", "momentum", "groups", "model_copy", "workspace"],
+         "muon_orthogonalize": ["u_out", "workspace"],
+         "muon_step_noalloc": ["params", "momentum"],
+         "muon_momentum": ["momentum", "u_out"],
+         "muon_apply": ["params"]}
+
+
+@pytest.mark.parametrize("name,odd", [(n, k) for n in EVERY for k in TAKES[n]])
+def test_steps_refuse_tensors_of_two_devices(gpu, monkeypatch, name, odd):
+    """A kernel that reads another device's memory faults."""
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    with pytest.raises(ValueError, match="is on cuda:1"):
+        calls(step_buffers(**{odd: 1}))[name]()
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("name", ["muon_step", "muon_step_grouped", "muon_step_clipped",
+                                  "muon_orthogonalize"])
+def test_steps_refuse_a_workspace_in_host_memory(gpu, monkeypatch, name):
+    import torch
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    b = step_buffers()
+    b["workspace"] = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        calls(b)[name]()
+    b["workspace"] = Tensor(1 << 20, torch.uint8)
+    b["workspace"].is_contiguous = lambda: False
+    with pytest.raises(ValueError, match="contiguous"):
+        calls(b)[name]()
+    b["workspace"] = Tensor(1 << 18, torch.float32)     # of any type
+    calls(b)[name]()
     assert len(lib.calls) == 1
