@@ -239,6 +239,12 @@ def _together(first, first_name: str, **others) -> None:
             raise ValueError(f"{name} is on {t.device}, {first_name} on {first.device}")
 
 
+def _shorter(a, b, *more) -> int:
+    """Elements that all state buffers have: the bound against which the library checks
+    the matrices."""
+    return min(t.numel() for t in (a, b, *more))
+
+
 def muon_workspace_bytes(descs, mode: str = "bf16") -> int:
     """Workspace bytes with which the descriptors run in one wave."""
     lib = load_library()
@@ -340,7 +346,7 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     with _workspace(workspace, descs, mode, grads.device) as ws:
         _launch(grads.get_device(), lib.muon_step, params.data_ptr(), dt, params.numel(),
-                grads.data_ptr(), momentum.data_ptr(), grads.numel(), descs_array(descs),
+                grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs),
                 _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
                 _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
@@ -358,7 +364,7 @@ def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: f
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     _launch(grads.get_device(), lib.muon_step_noalloc, params.data_ptr(), dt, params.numel(),
-            grads.data_ptr(), momentum.data_ptr(), grads.numel(), descs_array(descs),
+            grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs),
             _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
             _mode(mode))
 
@@ -415,7 +421,7 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
     lib = load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     head = (params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
-            momentum.data_ptr(), grads.numel(), descs_array(descs), _count(descs),
+            momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs), _count(descs),
             groups.data_ptr(), groups.shape[0])
     with _workspace(workspace, descs, mode, grads.device) as ws:
         tail = (int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -433,8 +439,8 @@ def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = T
     _together(grads, "grads", momentum=momentum, u_out=u_out)
     lib = load_library()
     _launch(grads.get_device(), lib.muon_momentum, grads.data_ptr(), momentum.data_ptr(),
-            u_out.data_ptr(), grads.numel(), descs_array(descs), _count(descs), beta,
-            int(bool(nesterov)))
+            u_out.data_ptr(), _shorter(grads, momentum, u_out), descs_array(descs), _count(descs),
+            beta, int(bool(nesterov)))
 
 
 def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", workspace=None):
@@ -445,8 +451,8 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     _together(u, "u", o_out=o_out)
     lib = load_library()
     with _workspace(workspace, descs, mode, u.device) as ws:
-        _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(), u.numel(),
-                descs_array(descs), _count(descs), int(ns_steps), _mode(mode), ws.data_ptr(),
+        _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(),
+                _shorter(u, o_out), descs_array(descs), _count(descs), int(ns_steps), _mode(mode), ws.data_ptr(),
                 ws.numel() * ws.element_size())
 
 

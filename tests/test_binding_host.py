@@ -266,3 +266,29 @@ def test_steps_refuse_a_workspace_in_host_memory(gpu, monkeypatch, name):
     b["workspace"] = Tensor(1 << 18, torch.float32)     # of any type
     calls(b)[name]()
     assert len(lib.calls) == 1
+
+
+# ------------------------------------------------------------ short buffers
+
+@pytest.mark.parametrize("name,short", [(n, k) for n in EVERY for k in ("momentum", "u_out")
+                                        if k in TAKES[n]])
+def test_steps_refuse_a_state_buffer_that_ends_early(gpu, monkeypatch, name, short):
+    """The library's own check sees the shorter of the state buffers: a matrix that
+    leaves it is out of bounds.  A longer one, or one that ends behind the last matrix, is fine."""
+    import os
+    if not os.path.exists(nsf.LIB_PATH):
+        from newton_schulz_flat_amd import build
+        build.build()
+    b = step_buffers()
+    for k, t in enumerate(b.values()):
+        t.at = (k + 1) << 40
+    b[short].n = 127
+    with pytest.raises(nsf.MuonError, match="OUT_OF_BOUNDS"):
+        calls(b)[name]()
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    b["params"].n = b["model_copy"].n = 999
+    for own, other in ((200, 128), (128, 200)):
+        b[short].n, b["grads"].n = own, other
+        calls(b)[name]()
+        assert 128 in lib.calls[-1][2]
