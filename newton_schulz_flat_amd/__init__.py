@@ -346,8 +346,8 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     with _workspace(workspace, descs, mode, grads.device) as ws:
         _launch(grads.get_device(), lib.muon_step, params.data_ptr(), dt, params.numel(),
-                grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs),
-                _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
+                grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum),
+                descs_array(descs), _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
                 _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
@@ -452,8 +452,8 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     lib = load_library()
     with _workspace(workspace, descs, mode, u.device) as ws:
         _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(),
-                _shorter(u, o_out), descs_array(descs), _count(descs), int(ns_steps), _mode(mode), ws.data_ptr(),
-                ws.numel() * ws.element_size())
+                _shorter(u, o_out), descs_array(descs), _count(descs), int(ns_steps),
+                _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def muon_apply(params, updates, descs, lr: float, weight_decay: float):

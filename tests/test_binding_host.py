@@ -108,7 +108,7 @@ def step_buffers(**devices):
     """Buffers of a step on the matrix of DESCS, on device 0 but for those named."""
     import torch
     at = lambda name: devices.get(name, devices.get("all", 0))
-    return dict(params=Tensor(128, torch.bfloat16, at("params")),
+    return dict(params=Tensor(128, torch.float32, at("params")),
                 grads=Tensor(128, torch.float32, at("grads")),
                 momentum=Tensor(128, torch.float32, at("momentum")),
                 u_out=Tensor(128, torch.float32, at("u_out")),
