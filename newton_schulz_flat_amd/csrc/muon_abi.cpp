@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <exception>
 #include <new>
 #include <vector>
 
@@ -177,6 +176,12 @@ int report(const Status& st) { return finish(st); }
 
 int report_hip(Status& st, hipError_t e, const char* what) { return finish((hip_fail(&st, e, what), st)); }
 
+int report_exception(const char* what) {
+    Status st{MUON_ERR_INTERNAL, ""};
+    snprintf(st.msg, sizeof(st.msg), "exception: %s", what);
+    return finish(st);
+}
+
 }  // namespace muon
 
 namespace {
@@ -251,7 +256,7 @@ hipError_t enqueue_step(const PlanView* views, int n_waves, void* params, int pa
 extern "C" {
 
 int muon_workspace_bytes(const muon_matrix_desc_t* descs, int64_t n, int gemm_mode,
-                         size_t* out_bytes) {
+                         size_t* out_bytes) try {
     Status st{MUON_OK, ""};
     TRY(check_null(out_bytes, "out_bytes", &st));
     TRY(check_mode(gemm_mode, &st));
@@ -260,9 +265,10 @@ int muon_workspace_bytes(const muon_matrix_desc_t* descs, int64_t n, int gemm_mo
     *out_bytes = muon::workspace_bytes_for(descs, n, gemm_mode);
     return MUON_OK;
 }
+MUON_CATCH
 
 int muon_workspace_min_bytes(const muon_matrix_desc_t* descs, int64_t n, int gemm_mode,
-                             size_t* out_bytes) {
+                             size_t* out_bytes) try {
     Status st{MUON_OK, ""};
     TRY(check_null(out_bytes, "out_bytes", &st));
     TRY(check_mode(gemm_mode, &st));
@@ -270,23 +276,25 @@ int muon_workspace_min_bytes(const muon_matrix_desc_t* descs, int64_t n, int gem
     *out_bytes = muon::min_workspace_bytes_for(descs, n, gemm_mode);
     return MUON_OK;
 }
+MUON_CATCH
 
 int muon_step(void* params, int param_dtype, int64_t n_param_elems, const float* grads,
               float* momentum, int64_t n_state_elems, const muon_matrix_desc_t* descs, int64_t n,
               float lr, float weight_decay, float beta, int nesterov, int ns_steps, int gemm_mode,
-              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+              void* workspace, size_t workspace_bytes, hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(muon::check_step_scalars(st, lr, weight_decay, beta, nesterov));
     const muon::Hyper h{nullptr, lr, weight_decay, beta, nesterov};
     return run_step(st, params, param_dtype, n_param_elems, nullptr, grads, momentum, n_state_elems,
                     descs, n, h, 1, ns_steps, gemm_mode, workspace, workspace_bytes, stream);
 }
+MUON_CATCH
 
 int muon_step_grouped(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
                       const float* grads, float* momentum, int64_t n_state_elems,
                       const muon_matrix_desc_t* descs, int64_t n, const muon_group_t* groups,
                       int32_t n_groups, int ns_steps, int gemm_mode, void* workspace,
-                      size_t workspace_bytes, hipStream_t stream) {
+                      size_t workspace_bytes, hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(check_groups(groups, n_groups, n, &st));
     const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0};
@@ -294,12 +302,13 @@ int muon_step_grouped(void* params, int param_dtype, int64_t n_param_elems, void
                     n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
                     workspace_bytes, stream);
 }
+MUON_CATCH
 
 int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
                       const float* grads, float* momentum, int64_t n_state_elems,
                       const muon_matrix_desc_t* descs, int64_t n, const muon_group_t* groups,
                       int32_t n_groups, const muon_clip_t* clip, int ns_steps, int gemm_mode,
-                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                      void* workspace, size_t workspace_bytes, hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(check_groups(groups, n_groups, n, &st));
     if (n > 0) TRY(check_null(clip, "clip", &st));
@@ -309,20 +318,15 @@ int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void
         return finish(st);
     }
     const muon::Hyper h{groups, 0.f, 0.f, 0.f, 0, clip};
-    try {
-        return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
-                        n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
-                        workspace_bytes, stream);
-    } catch (const std::exception& e) {  // of the host tables' memory
-        st.code = MUON_ERR_INTERNAL;
-        snprintf(st.msg, sizeof(st.msg), "exception: %s", e.what());
-        return finish(st);
-    }
+    return run_step(st, params, param_dtype, n_param_elems, model_copy, grads, momentum,
+                    n_state_elems, descs, n, h, n_groups, ns_steps, gemm_mode, workspace,
+                    workspace_bytes, stream);
 }
+MUON_CATCH
 
 int muon_momentum(const float* grads, float* momentum, float* u_out, int64_t n_state_elems,
                   const muon_matrix_desc_t* descs, int64_t n, float beta, int nesterov,
-                  hipStream_t stream) {
+                  hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(muon::check_desc_shapes(descs, n, &st));
     TRY(check_flag(nesterov, "nesterov", &st));
@@ -344,10 +348,11 @@ int muon_momentum(const float* grads, float* momentum, float* u_out, int64_t n_s
             "front");
     return MUON_OK;
 }
+MUON_CATCH
 
 int muon_orthogonalize(const float* u, float* o_out, int64_t n_elems,
                        const muon_matrix_desc_t* descs, int64_t n, int ns_steps, int gemm_mode,
-                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(muon::check_desc_shapes(descs, n, &st));
     TRY(check_mode(gemm_mode, &st));
@@ -386,10 +391,11 @@ int muon_orthogonalize(const float* u, float* o_out, int64_t n_elems,
     }
     return MUON_OK;
 }
+MUON_CATCH
 
 int muon_apply(void* params, int param_dtype, int64_t n_param_elems, const float* updates,
                int64_t n_update_elems, const muon_matrix_desc_t* descs, int64_t n, float lr,
-               float weight_decay, hipStream_t stream) {
+               float weight_decay, hipStream_t stream) try {
     Status st{MUON_OK, ""};
     TRY(muon::check_desc_shapes(descs, n, &st));
     TRY(muon::check_scalar(lr, "lr", &st));
@@ -412,6 +418,7 @@ int muon_apply(void* params, int param_dtype, int64_t n_param_elems, const float
             "apply");
     return MUON_OK;
 }
+MUON_CATCH
 
 const char* muon_status_string(int status) {
     switch (status) {

@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <exception>
 #include <vector>
 
 #include "clip_internal.h"
@@ -24,20 +23,13 @@ __attribute__((format(printf, 3, 4))) int fail(Status* st, int code, const char*
     return code;
 }
 
-// Runs an entry point's body; an exception (of the host tables' memory)
-// becomes a status.
+// Runs an entry point's body and reports its status.
 template <typename F>
-int guarded(F body) {
+int guarded(F body) try {
     Status st{MUON_OK, ""};
-    try {
-        return body(st) == MUON_OK ? MUON_OK : report(st);
-    } catch (const std::exception& e) {
-        fail(&st, MUON_ERR_INTERNAL, "exception: %s", e.what());
-    } catch (...) {
-        fail(&st, MUON_ERR_INTERNAL, "unknown exception");
-    }
-    return report(st);
+    return body(st) == MUON_OK ? int(MUON_OK) : report(st);
 }
+MUON_CATCH
 
 #define TRY(expr)                              \
     do {                                       \

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <exception>
 #include <memory>
 
 #include <hip/hip_runtime_api.h>
@@ -163,6 +164,13 @@ int check_step_scalars(Status& st, float lr, float weight_decay, float beta, int
 // returns its code.  report_hip fills st from a HIP error first.
 int report(const Status& st);
 int report_hip(Status& st, hipError_t e, const char* what);
+// Stores an exception (of the host tables' memory, as a rule) as the thread's
+// last error, MUON_ERR_INTERNAL.  Every entry point that can allocate is a function
+// try block that ends in MUON_CATCH: nothing is thrown across the ABI.
+int report_exception(const char* what);
+#define MUON_CATCH                                                             \
+    catch (const std::exception& e) { return muon::report_exception(e.what()); } \
+    catch (...) { return muon::report_exception("of an unknown type"); }
 
 // --------------------------------------------------------------------- plan
 
@@ -211,6 +219,7 @@ class LaunchTimer {
     LaunchTimer& operator=(const LaunchTimer&) = delete;
 
   private:
+    void stop();
     const char* name_;
     hipStream_t stream_;
     void* start_ = nullptr;  // hipEvent_t when active

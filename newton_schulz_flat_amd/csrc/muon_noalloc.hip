@@ -53,7 +53,7 @@ extern "C" int muon_step_noalloc(void* params, int param_dtype, int64_t n_param_
                                  const float* grads, float* momentum, int64_t n_state_elems,
                                  const muon_matrix_desc_t* descs, int64_t n, float lr,
                                  float weight_decay, float beta, int nesterov, int ns_steps,
-                                 int gemm_mode, hipStream_t stream) {
+                                 int gemm_mode, hipStream_t stream) try {
     using namespace muon;
     Status st{MUON_OK, ""};
     if (check_step_scalars(st, lr, weight_decay, beta, nesterov) != MUON_OK) return report(st);
@@ -136,3 +136,4 @@ extern "C" int muon_step_noalloc(void* params, int param_dtype, int64_t n_param_
     if (e != hipSuccess) return report_hip(st, e, "step");
     return MUON_OK;
 }
+MUON_CATCH

@@ -52,6 +52,13 @@ LaunchTimer::LaunchTimer(const char* name, hipStream_t s) : name_(name), stream_
 
 LaunchTimer::~LaunchTimer() {
     if (start_ == nullptr) return;
+    try {
+        stop();
+    } catch (...) {  // no memory for the record: this launch goes untimed
+    }
+}
+
+void LaunchTimer::stop() {
     std::lock_guard<std::mutex> lock(g_mu);
     hipEvent_t stop = take_event();
     hipEvent_t start = static_cast<hipEvent_t>(start_);
@@ -67,7 +74,7 @@ LaunchTimer::~LaunchTimer() {
 
 extern "C" {
 
-int muon_profile_begin(void) {
+int muon_profile_begin(void) try {
     std::lock_guard<std::mutex> lock(muon::g_mu);
     for (auto& r : muon::g_records) {
         muon::g_pool.push_back(r.start);
@@ -77,8 +84,9 @@ int muon_profile_begin(void) {
     muon::g_on.store(true);
     return MUON_OK;
 }
+MUON_CATCH
 
-int muon_profile_end(muon_kernel_time_t* out, int max_entries, int* n_entries) {
+int muon_profile_end(muon_kernel_time_t* out, int max_entries, int* n_entries) try {
     muon::g_on.store(false);
     std::lock_guard<std::mutex> lock(muon::g_mu);
     std::map<std::string, std::pair<double, int64_t>> agg;
@@ -112,5 +120,6 @@ int muon_profile_end(muon_kernel_time_t* out, int max_entries, int* n_entries) {
     if (n_entries != nullptr) *n_entries = k;
     return rc;
 }
+MUON_CATCH
 
 }  // extern "C"
