@@ -33,7 +33,7 @@ objects with ``offset, numel`` and optionally ``param_offset`` (default
 A training step clips by the global norm without a word to the host::
 
     clip = clip_state(device)                       # kept
-    tensors = tensor_list([*matrix_grads, *other_grads])    # kept
+    tensors = tensor_list([*matrix_grads, *other_grads])    # kept while they stay where they are
     muon_grad_norm(tensors, 1.0, clip)
     muon_step_clipped(params, grads, momentum, descs, groups, clip)
     muon_adamw(other_params, other_grads, m, v, ranges, adamw_groups, clip=clip)
@@ -513,8 +513,9 @@ def _require_clip(clip, device):
 
 
 class TensorList:
-    """Tensors as a ``muon_tensor_t`` array.  Keeps the tensors; their addresses
-    are taken once, so a tensor whose storage is replaced needs a new list."""
+    """Tensors as a ``muon_tensor_t`` array.  Keeps the tensors and the memory that they had;
+    their addresses are taken once, so a tensor whose storage is replaced, moved or
+    freed needs a new list: calls refuse one that holds it."""
 
     def __init__(self, tensors: Iterable):
         import torch
@@ -531,6 +532,18 @@ class TensorList:
             bf16 = t.dtype == torch.bfloat16
             self.array[k] = TensorC(t.data_ptr(), t.numel(),
                                     MUON_DTYPE_BF16 if bf16 else MUON_DTYPE_F32, 0)
+        # With the storages held, no other tensor's memory can come to lie at an address of
+        # the list, so an unchanged address is the same memory.
+        self._data_ptr = torch.Tensor.data_ptr
+        self._addresses = list(map(self._data_ptr, self.tensors))
+        self._storages = [t.untyped_storage() for t in self.tensors]
+
+    def check(self) -> None:
+        """Refuses the list if one of its tensors has moved.  Less than 0.1 us a tensor."""
+        now = list(map(self._data_ptr, self.tensors))
+        if now != self._addresses:
+            k = next(i for i, (a, b) in enumerate(zip(now, self._addresses)) if a != b)
+            raise ValueError(f"tensors[{k}] has moved since the list was made: make a new one")
 
     def __len__(self) -> int:
         return len(self.tensors)
@@ -538,8 +551,18 @@ class TensorList:
 
 def tensor_list(tensors) -> TensorList:
     """``tensors`` as a list that the norm and clipping calls take as it is: a
-    program that keeps its gradient buffers makes it once."""
+    program that keeps its gradient buffers makes it once (about 1 us a tensor).
+    Where gradients get new memory every step (``zero_grad(set_to_none=True)``), make a
+    new one, or pass the tensors themselves, every step."""
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def _tensors_now(tensors) -> TensorList:
+    """``tensors`` as a list whose addresses hold at this moment."""
+    if isinstance(tensors, TensorList):
+        tensors.check()
+        return tensors
+    return TensorList(tensors)
 
 
 def muon_clip_workspace_bytes(tensors) -> int:
@@ -581,7 +604,7 @@ def muon_grad_norm(tensors, max_norm: float, clip, tensor_norms=None, workspace=
     ``workspace``: a uint8 GPU tensor of ``muon_clip_workspace_bytes`` (default: a
     cached one per device and stream; give one under graph capture)."""
     import torch
-    tl = tensor_list(tensors)
+    tl = _tensors_now(tensors)
     _require_clip(clip, tl.device if tl.device is not None else clip.device)
     norms_ptr = None
     if tensor_norms is not None:
@@ -612,8 +635,8 @@ def muon_clip_finish(clip, max_norm: float):
 def muon_clip_grads(tensors, clip, out=None):
     """Every tensor times the coefficient of ``clip``, in place, or into the
     tensors of ``out`` (same lengths; f32 or bf16, rounded once)."""
-    src = tensor_list(tensors)
-    dst = src if out is None else tensor_list(out)
+    src = _tensors_now(tensors)
+    dst = src if out is None else _tensors_now(out)
     if len(src) != len(dst):
         raise ValueError(f"{len(src)} tensors, but {len(dst)} in out")
     if len(src) == 0:

@@ -164,7 +164,7 @@ def from_two_threads(call):
 
 def default_workspace_calls():
     import torch
-    tensors = nsf.tensor_list([Tensor(1000, torch.float32)])
+    tensors = nsf.tensor_list([torch.ones(1000)])
     every = calls(step_buffers(), workspace=False)
     every["muon_grad_norm"] = lambda: nsf.muon_grad_norm(tensors, 1.0, record())
     return every
@@ -292,3 +292,65 @@ def test_steps_refuse_a_state_buffer_that_ends_early(gpu, monkeypatch, name, sho
         b[short].n, b["grads"].n = own, other
         calls(b)[name]()
         assert 128 in lib.calls[-1][2]
+
+
+# ------------------------------------------------------------ kept lists
+
+def moved_by(name, t):
+    import torch
+    if name == "data":
+        t.data = torch.ones(t.numel())
+    elif name == "set_":
+        t.set_(torch.ones(t.numel()))
+    elif name == "resize_":
+        t.resize_(10 * t.numel())
+    elif name == "storage freed":
+        t.untyped_storage().resize_(0)
+    elif name == "another part":
+        t.data = t.data[8:]
+
+
+@pytest.mark.parametrize("how", ["data", "set_", "resize_", "storage freed", "another part"])
+def test_a_kept_list_refuses_tensors_that_moved(gpu, monkeypatch, how):
+    """A list holds addresses; the tensors' memory may have been freed since."""
+    import torch
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    monkeypatch.setattr(nsf, "muon_clip_workspace_bytes", lambda tensors: 4096)
+    still, t = torch.ones(64), torch.ones(1000)
+    kept, out = nsf.tensor_list([still, t]), nsf.tensor_list([torch.ones(64), torch.ones(1000)])
+    clip = record()
+    clip.device = kept.device
+
+    def every():
+        return [lambda: nsf.muon_grad_norm(kept, 1.0, clip), lambda: nsf.muon_clip_grads(kept, clip),
+                lambda: nsf.muon_clip_grads(kept, clip, out=out),
+                lambda: nsf.muon_clip_grads(out, clip, out=kept)]
+    monkeypatch.setattr(nsf, "_current_stream", lambda index: 100)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: types.SimpleNamespace(cuda_stream=100))
+    still.mul_(2)                  # new values are fine
+    for call in every():
+        call()
+    assert len(lib.calls) == 4
+    moved_by(how, t)
+    for call in every():
+        with pytest.raises(ValueError, match=r"tensors\[1\] has moved"):
+            call()
+    assert len(lib.calls) == 4
+    nsf.muon_clip_grads([still], clip)          # a list made by the call is of this moment
+    assert len(lib.calls) == 5
+
+
+def test_a_kept_list_keeps_the_memory_it_points_to(gpu):
+    """So that no other tensor can come to lie at an address of the list, unnoticed."""
+    import torch
+    t = torch.full((100000,), 7.0)
+    kept = nsf.tensor_list([t])
+    t.data = torch.ones(100000)
+    others = [torch.zeros(100000) for _ in range(20)]
+    assert kept.array[0].data not in [o.data_ptr() for o in others]
+    import ctypes
+    assert ctypes.c_float.from_address(kept.array[0].data).value == 7.0
