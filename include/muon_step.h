@@ -280,11 +280,13 @@ int muon_step_noalloc(void* params, int param_dtype, int64_t n_param_elems, cons
  * (matrices and the rest), the clipping that follows from it, and an optimizer
  * for the parameters that Muon skips ("Non-2D parameters are skipped. Use a
  * separate optimizer", FsdpMuon class docstring; "clip_grad" in the
- * Megatron-Bridge #5933 commit message).  They keep no plan and allocate nothing: every call, the
- * first one too, may be captured into a HIP graph.  Nothing returns to the
- * host: the norm and the clipping coefficient stay in a record in device
- * memory, which the consuming kernels read when they run.  Errors, streams and
- * ownership as above. */
+ * Megatron-Bridge #5933 commit message).  All but muon_step_clipped keep no
+ * plan and allocate nothing: every call of theirs, the first one too, may be
+ * captured into a HIP graph.  muon_step_clipped has the plans of
+ * muon_step_grouped, so its first call with a descriptor set is made outside
+ * graph capture.  Nothing returns to the host: the norm and the clipping
+ * coefficient stay in a record in device memory, which the consuming kernels
+ * read when they run.  Errors, streams and ownership as above. */
 
 /* One tensor of a list: `numel` consecutive elements (0..2^34; a list holds at
  * most 2^36) of type MUON_DTYPE_F32 or MUON_DTYPE_BF16 in device memory,
@@ -346,7 +348,11 @@ int muon_clip_grads(const muon_tensor_t* src, const muon_tensor_t* dst, int64_t 
 /* muon_step_grouped on the clipped gradient fl(coef * G), without a pass of its
  * own: the kernel that reads G multiplies.  Results equal, bit for bit, those of
  * muon_clip_grads into another float32 buffer followed by muon_step_grouped
- * with it; grads itself is only read.  clip must not overlap the other buffers. */
+ * with it; grads itself is only read.  clip must not overlap the other buffers.
+ * The first call with a descriptor set (unless muon_step_grouped or muon_step
+ * ran with it, in the same mode and workspace size) builds its plan, allocates and
+ * synchronizes: make it outside graph capture, where it is refused with
+ * MUON_ERR_BAD_ARG before anything is enqueued. */
 int muon_step_clipped(void* params, int param_dtype, int64_t n_param_elems, void* model_copy,
                       const float* grads, float* momentum, int64_t n_state_elems,
                       const muon_matrix_desc_t* descs, int64_t n, const muon_group_t* groups,

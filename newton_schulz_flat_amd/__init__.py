@@ -395,7 +395,8 @@ def muon_step_grouped(params, grads, momentum, descs, groups, ns_steps: int = 5,
 def muon_step_clipped(params, grads, momentum, descs, groups, clip, ns_steps: int = 5,
                       mode: str = "bf16", model_copy=None, workspace=None):
     """``muon_step_grouped`` on ``grads`` times the coefficient of ``clip`` (a
-    ``clip_state`` that ``muon_grad_norm`` filled); ``grads`` is only read."""
+    ``clip_state`` that ``muon_grad_norm`` filled); ``grads`` is only read.  The
+    first call with a descriptor set is made outside graph capture: it builds the plan."""
     _require_clip(clip, grads.device)
     _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, model_copy,
                   workspace)

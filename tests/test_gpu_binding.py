@@ -1,4 +1,5 @@
-"""GPU tests of calls made from two threads at once on one stream."""
+"""GPU tests of calls made from two threads at once on one stream, and of first calls under
+graph capture."""
 
 import threading
 
@@ -90,3 +91,39 @@ def test_clipped_steps_from_two_threads_on_one_stream(nsf, torch):
     for a, b in zip(want, got):
         for x, y in zip(a[1:], b[1:]):
             assert np.array_equal(bits(host(x)), bits(host(y)))
+
+
+def test_first_clipped_step_is_made_outside_capture(nsf, torch):
+    """Under capture a first call with a descriptor set is refused and leaves the capture
+    whole; after one call outside it is captured, and every replay is an eager call."""
+    say("first clipped step under capture")
+    wl = wlm.small_mixed(77, count=3, max_side=200, param_dtype="f32")
+    params, grads, mom = wlm.make_tensors(wl, "cuda", momentum_std=1e-3)
+    table = nsf.group_table([(0.02, 0.01, 0.95, True)], "cuda")
+    clip = nsf.clip_state("cuda")
+    cws = torch.empty(nsf.muon_clip_workspace_bytes([grads]), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nsf.muon_workspace_bytes(wl.descs), dtype=torch.uint8, device="cuda")
+
+    def step(p, m):
+        nsf.muon_grad_norm([grads], 0.5, clip, workspace=cws)
+        nsf.muon_step_clipped(p, grads, m, wl.descs, table, clip, workspace=ws)
+    p1, m1, p2, m2 = params.clone(), mom.clone(), params.clone(), mom.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(nsf.MuonError, match="outside graph capture"):
+            step(p1, m1)
+        grads.mul_(2.0)
+    assert torch.equal(p1, params) and torch.equal(m1, mom)
+    step(params.clone(), mom.clone())       # the plan
+    torch.cuda.synchronize()
+    whole = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(whole):
+        step(p1, m1)
+    for rep in range(3):
+        graph.replay()                      # the capture that went on after the refusal
+        whole.replay()
+        torch.cuda.synchronize()
+        step(p2, m2)
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(host(p1)), bits(host(p2))), rep
+        assert np.array_equal(bits(host(m1)), bits(host(m2))), rep
