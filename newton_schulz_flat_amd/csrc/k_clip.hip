@@ -31,11 +31,16 @@ constexpr int kThreads = 256;
 constexpr int kFlight = 8;
 constexpr int kWaves = kThreads / 64;
 // One workgroup of this size reads up to kSoloUnits units of kSoloUnit elements by
-// itself and saves the second launch.  Time of a call among others, alone in
-// brackets, one workgroup against two launches: 1000 elements 5.7 (16.7) against
-// 8.5 us (21), 64 Ki 5.8 (18.2) against 8.6 (21), 64 tensors of 1024 6.1 (18.4)
-// against 8.9 (22); at 128 Ki float32 they meet (8.0 and 8.5), at 256 Ki one
-// workgroup takes 13.4.  Units of 512 or 1024 elements: 9.5 and 6.4 us at 64 Ki.
+// itself and saves the second launch.  A tensor takes a unit at least, a run of
+// adjacent tensors counts as one.  Time of a call among others, alone in brackets, one
+// workgroup against two launches, float32: 1000 elements 5.4 (16.1) against 8.1 us
+// (20.1); one run of 64 Ki 5.4 (17.6) against 8.0 (18.6), of 96 Ki, the longest taken,
+// 6.6 (18.7) against 8.0 (19.3), of 128 Ki 8.0 (20.1) against 8.0 (18.6).  Tensors
+// that lie apart are dearer: 40 of 100 elements 6.3 (18.5) against 8.2 (19.4), 48 of 1024
+// 8.1 (20.4) against 8.2 (19.1), 48 of 2048 9.4 (21.6) against 8.2 (19.3), 64 of 1024
+// 10.2 (22.4) against 8.3 (19.4).  So the limit, one number of units for both, suits runs
+// well and is at or past the crossing for its 48 separate tensors.
+// Units of 512 or 1024 elements: 9.5 and 6.4 us at 64 Ki.
 constexpr int kFinishThreads = 1024;
 constexpr int kSoloThreads = 1024;
 constexpr int64_t kSoloUnit = 2048;
