@@ -188,9 +188,9 @@ __global__ __launch_bounds__(256) void front_cast_kernel(const MatInfo* __restri
         float m1[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float gc = coef * gv[q];
-            m1[q] = beta * mv[q] + gc;
-            uv[q] = nesterov ? beta * m1[q] + gc : m1[q];
+            const float clipped = coef * gv[q];
+            m1[q] = beta * mv[q] + clipped;
+            uv[q] = nesterov ? beta * m1[q] + clipped : m1[q];
         }
         if (vec && gc + 3 < mt.C) {
             store4_stream(m + e, make_float4(m1[0], m1[1], m1[2], m1[3]));
@@ -243,9 +243,9 @@ __global__ __launch_bounds__(256) void front_cast_kernel(const MatInfo* __restri
         float m1[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float gc = coef * gv[q];
-            m1[q] = beta * mv[q] + gc;
-            uv[q] = nesterov ? beta * m1[q] + gc : m1[q];
+            const float clipped = coef * gv[q];
+            m1[q] = beta * mv[q] + clipped;
+            uv[q] = nesterov ? beta * m1[q] + clipped : m1[q];
         }
         const int64_t e = mt.off + a;
         if (a >= lo && a + 4 <= hi) {
