@@ -65,7 +65,8 @@ _MODES = {"bf16": MUON_GEMM_BF16_MFMA, "f32": MUON_GEMM_F32}
 EXPORTS = ("muon_workspace_bytes", "muon_workspace_min_bytes", "muon_step", "muon_step_grouped",
            "muon_step_noalloc", "muon_step_clipped", "muon_momentum", "muon_orthogonalize",
            "muon_apply", "muon_clip_workspace_bytes", "muon_grad_norm", "muon_clip_finish",
-           "muon_clip_grads", "muon_adamw", "muon_profile_begin", "muon_profile_end", "muon_status_string", "muon_last_error")
+           "muon_clip_grads", "muon_adamw", "muon_profile_begin", "muon_profile_end",
+           "muon_status_string", "muon_last_error")
 
 
 class MatrixDescC(ctypes.Structure):
@@ -186,8 +187,9 @@ def descs_array(descs: Iterable) -> ctypes.Array:
     return arr
 
 
-def _count(descs) -> int:
-    return len(descs) if isinstance(descs, Sequence) else len(list(descs))
+def _listed(descs) -> Sequence:
+    """Descriptors as something that can be read more than once, with a length."""
+    return descs if isinstance(descs, Sequence) else list(descs)
 
 
 def _mode(mode: str) -> int:
@@ -248,18 +250,20 @@ def _shorter(a, b, *more) -> int:
 def muon_workspace_bytes(descs, mode: str = "bf16") -> int:
     """Workspace bytes with which the descriptors run in one wave."""
     lib = load_library()
+    descs = _listed(descs)
     arr = descs_array(descs)
     out = ctypes.c_size_t(0)
-    check(lib.muon_workspace_bytes(arr, _count(descs), _mode(mode), ctypes.byref(out)))
+    check(lib.muon_workspace_bytes(arr, len(descs), _mode(mode), ctypes.byref(out)))
     return out.value
 
 
 def muon_workspace_min_bytes(descs, mode: str = "bf16") -> int:
     """Smallest workspace that runs the descriptors (in waves, one matrix or more each)."""
     lib = load_library()
+    descs = _listed(descs)
     arr = descs_array(descs)
     out = ctypes.c_size_t(0)
-    check(lib.muon_workspace_min_bytes(arr, _count(descs), _mode(mode), ctypes.byref(out)))
+    check(lib.muon_workspace_min_bytes(arr, len(descs), _mode(mode), ctypes.byref(out)))
     return out.value
 
 
@@ -342,13 +346,13 @@ def muon_step(params, grads, momentum, descs, lr: float, weight_decay: float, be
     _require(grads, "grads", (torch.float32,))
     _require(momentum, "momentum", (torch.float32,))
     _together(grads, "grads", params=params, momentum=momentum)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     with _workspace(workspace, descs, mode, grads.device) as ws:
         _launch(grads.get_device(), lib.muon_step, params.data_ptr(), dt, params.numel(),
                 grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum),
-                descs_array(descs), _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
-                _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
+                descs_array(descs), len(descs), lr, weight_decay, beta, int(bool(nesterov)),
+                int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: float,
@@ -361,11 +365,11 @@ def muon_step_noalloc(params, grads, momentum, descs, lr: float, weight_decay: f
     _require(grads, "grads", (torch.float32,))
     _require(momentum, "momentum", (torch.float32,))
     _together(grads, "grads", params=params, momentum=momentum)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     _launch(grads.get_device(), lib.muon_step_noalloc, params.data_ptr(), dt, params.numel(),
             grads.data_ptr(), momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs),
-            _count(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
+            len(descs), lr, weight_decay, beta, int(bool(nesterov)), int(ns_steps),
             _mode(mode))
 
 
@@ -419,10 +423,10 @@ def _step_grouped(params, grads, momentum, descs, groups, clip, ns_steps, mode, 
         copy_ptr = model_copy.data_ptr()
     _together(grads, "grads", params=params, momentum=momentum, groups=groups,
               model_copy=model_copy)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     head = (params.data_ptr(), dt, params.numel(), copy_ptr, grads.data_ptr(),
-            momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs), _count(descs),
+            momentum.data_ptr(), _shorter(grads, momentum), descs_array(descs), len(descs),
             groups.data_ptr(), groups.shape[0])
     with _workspace(workspace, descs, mode, grads.device) as ws:
         tail = (int(ns_steps), _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -438,9 +442,9 @@ def muon_momentum(grads, momentum, u_out, descs, beta: float, nesterov: bool = T
     for t, nm in ((grads, "grads"), (momentum, "momentum"), (u_out, "u_out")):
         _require(t, nm, (torch.float32,))
     _together(grads, "grads", momentum=momentum, u_out=u_out)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     _launch(grads.get_device(), lib.muon_momentum, grads.data_ptr(), momentum.data_ptr(),
-            u_out.data_ptr(), _shorter(grads, momentum, u_out), descs_array(descs), _count(descs),
+            u_out.data_ptr(), _shorter(grads, momentum, u_out), descs_array(descs), len(descs),
             beta, int(bool(nesterov)))
 
 
@@ -450,10 +454,10 @@ def muon_orthogonalize(u, o_out, descs, ns_steps: int = 5, mode: str = "bf16", w
     _require(u, "u", (torch.float32,))
     _require(o_out, "o_out", (torch.float32,))
     _together(u, "u", o_out=o_out)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     with _workspace(workspace, descs, mode, u.device) as ws:
         _launch(u.get_device(), lib.muon_orthogonalize, u.data_ptr(), o_out.data_ptr(),
-                _shorter(u, o_out), descs_array(descs), _count(descs), int(ns_steps),
+                _shorter(u, o_out), descs_array(descs), len(descs), int(ns_steps),
                 _mode(mode), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
@@ -463,10 +467,10 @@ def muon_apply(params, updates, descs, lr: float, weight_decay: float):
     _require(params, "params", (torch.float32, torch.bfloat16))
     _require(updates, "updates", (torch.float32,))
     _together(updates, "updates", params=params)
-    lib = load_library()
+    descs, lib = _listed(descs), load_library()
     dt = MUON_DTYPE_BF16 if params.dtype == torch.bfloat16 else MUON_DTYPE_F32
     _launch(updates.get_device(), lib.muon_apply, params.data_ptr(), dt, params.numel(),
-            updates.data_ptr(), updates.numel(), descs_array(descs), _count(descs), lr,
+            updates.data_ptr(), updates.numel(), descs_array(descs), len(descs), lr,
             weight_decay)
 
 

@@ -3,6 +3,7 @@ which device it launches on and which tensors it refuses.  The library and the
 GPU are stand-ins here; nothing is computed."""
 
 import contextlib
+import ctypes
 import threading
 import time
 import types
@@ -352,5 +353,27 @@ def test_a_kept_list_keeps_the_memory_it_points_to(gpu):
     t.data = torch.ones(100000)
     others = [torch.zeros(100000) for _ in range(20)]
     assert kept.array[0].data not in [o.data_ptr() for o in others]
-    import ctypes
     assert ctypes.c_float.from_address(kept.array[0].data).value == 7.0
+
+
+# ------------------------------------------------------------ descriptors
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("name", EVERY)
+def test_descriptors_from_an_iterator(gpu, monkeypatch, name, workspace):
+    """An iterator can be read once; the call has to see every descriptor all the same."""
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    sized = []
+    monkeypatch.setattr(nsf, "muon_workspace_bytes",
+                        lambda descs, mode="bf16": sized.append(len(list(descs))) or 4096)
+    every = calls(step_buffers(), workspace=workspace)
+    if name not in every:
+        return
+    monkeypatch.setitem(globals(), "DESCS", iter([(0, 8, 4), (32, 4, 8), (64, 2, 2)]))
+    every[name]()
+    (_, _, args), = lib.calls
+    at = next(k for k, a in enumerate(args) if isinstance(a, ctypes.Array))
+    assert args[at + 1] == len(args[at]) == 3
+    assert [d.offset for d in args[at]] == [0, 32, 64]
+    assert sized in ([], [3])
