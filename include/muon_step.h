@@ -144,7 +144,7 @@ typedef enum muon_status {
     MUON_ERR_BAD_ARG = -7,             /* bad n, dtype, mode, ns_steps, group or non-finite scalar */
     MUON_ERR_WORKSPACE_TOO_SMALL = -8, /* workspace smaller than muon_workspace_bytes() */
     MUON_ERR_HIP = -9,                 /* a HIP runtime call failed (message has details) */
-    MUON_ERR_INTERNAL = -10            /* should not happen; message has details */
+    MUON_ERR_INTERNAL = -10            /* an exception, such as no host memory; message has details */
 } muon_status_t;
 
 /* Element type of the params buffer.  grads, momentum and updates are float32. */

@@ -308,6 +308,10 @@ __device__ __forceinline__ void store_v(uint16_t* p, const float v[V]) {
 // counted from there, unit 0 takes the head as well and the last one the tail;
 // elsewhere they are plain runs of elements.  src may be dst.
 //
+// Vectors against single elements, 218 M of them in TB/s: float32 to float32 6.3 against
+// 4.7, bfloat16 to float32 6.3 and 3.2, float32 to bfloat16 6.6 and 3.9, bfloat16 to
+// bfloat16 6.0 and 2.6.
+//
 // A thread's vector is 4 elements (8 where both sides are bfloat16), so that
 // neighbouring lanes meet without a gap on the wider side too: 8 bfloat16 read
 // and two times 16 bytes of float32 stored by each lane took 1.6 times as long.
