@@ -21,6 +21,10 @@ Entry points (same names as the C ABI):
 ``muon_clip_grads``     every tensor times the coefficient, in place or into others
 ``muon_clip_finish``    norm and coefficient from a record's (all-reduced) sum of squares
 ``muon_adamw``          AdamW on ranges of flat buffers, for the parameters Muon skips
+``muon_fp8_cast``       a matrix and its transpose into 8 bits, a scale for each block of 128
+``muon_fp8_matmul``     product of two such matrices, also added into float32 gradients
+``muon_orthogonalize_stack``  Newton-Schulz of stacked matrices with strides, in float32
+                        accuracy, with coefficients for each step
 ``muon_workspace_bytes``      workspace for one wave
 ``muon_workspace_min_bytes``  smallest workspace (the matrices then run in waves)
 
@@ -65,8 +69,9 @@ _MODES = {"bf16": MUON_GEMM_BF16_MFMA, "f32": MUON_GEMM_F32}
 EXPORTS = ("muon_workspace_bytes", "muon_workspace_min_bytes", "muon_step", "muon_step_grouped",
            "muon_step_noalloc", "muon_step_clipped", "muon_momentum", "muon_orthogonalize",
            "muon_apply", "muon_clip_workspace_bytes", "muon_grad_norm", "muon_clip_finish",
-           "muon_clip_grads", "muon_adamw", "muon_profile_begin", "muon_profile_end",
-           "muon_status_string", "muon_last_error")
+           "muon_clip_grads", "muon_adamw", "muon_fp8_cast", "muon_fp8_workspace_bytes",
+           "muon_fp8_matmul", "muon_stack_workspace_bytes", "muon_orthogonalize_stack",
+           "muon_profile_begin", "muon_profile_end", "muon_status_string", "muon_last_error")
 
 
 class MatrixDescC(ctypes.Structure):
@@ -90,6 +95,25 @@ class RangeC(ctypes.Structure):
     _fields_ = [("offset", ctypes.c_int64), ("numel", ctypes.c_int64),
                 ("param_offset", ctypes.c_int64), ("group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Fp8C(ctypes.Structure):
+    """``muon_fp8_t``."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("scale_row", ctypes.c_int64), ("scale_col", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("block_rows", ctypes.c_int32)]
+
+
+class StackC(ctypes.Structure):
+    """``muon_stack_t``."""
+
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("in_stride", ctypes.c_int64),
+                ("in_row", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("out_row", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class KernelTimeC(ctypes.Structure):
@@ -143,6 +167,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_clip_grads.argtypes = [tp, tp, i64, p, p]
     lib.muon_adamw.argtypes = [p, i32, i64, p, p, i32, p, p, i64, ctypes.POINTER(RangeC), i64, p,
                                ctypes.c_int32, p, p]
+    fp, sp = ctypes.POINTER(Fp8C), ctypes.POINTER(StackC)
+    lib.muon_fp8_cast.argtypes = [p, i32, i64, i64, i64, fp, fp, p]
+    lib.muon_fp8_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+    lib.muon_fp8_matmul.argtypes = [fp, fp, p, i32, i64, i32, p, sz, p]
+    lib.muon_stack_workspace_bytes.argtypes = [sp, ctypes.POINTER(sz)]
+    lib.muon_orthogonalize_stack.argtypes = [sp, ctypes.POINTER(f32), i32, f32, p, sz, p]
     lib.muon_profile_begin.argtypes = []
     lib.muon_profile_end.argtypes = [ctypes.POINTER(KernelTimeC), i32, ctypes.POINTER(i32)]
     lib.muon_status_string.argtypes = [i32]
@@ -153,6 +183,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "muon_step_grouped", "muon_step_noalloc", "muon_momentum", "muon_orthogonalize",
                  "muon_apply", "muon_step_clipped", "muon_clip_workspace_bytes",
                  "muon_grad_norm", "muon_clip_finish", "muon_clip_grads", "muon_adamw",
+                 "muon_fp8_cast", "muon_fp8_workspace_bytes", "muon_fp8_matmul",
+                 "muon_stack_workspace_bytes", "muon_orthogonalize_stack",
                  "muon_profile_begin", "muon_profile_end"):
         getattr(lib, name).restype = i32
     _lib = lib
@@ -733,6 +765,224 @@ def muon_adamw(params, grads, exp_avg, exp_avg_sq, ranges, groups, clip=None, mo
     _launch(at, load_library().muon_adamw, params.data_ptr(), pdt, params.numel(), copy_ptr,
             grads.data_ptr(), gdt, exp_avg.data_ptr(), exp_avg_sq.data_ptr(), grads.numel(), arr,
             len(arr), groups.data_ptr(), groups.shape[0], clip_ptr)
+
+
+def _fp8_formats():
+    """Formats of the 8-bit types, worked out once."""
+    global _FP8
+    if _FP8 is None:
+        import torch
+        _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+    return _FP8
+
+
+_FP8 = None
+
+
+def fp8_scales(rows: int, cols: int, block: str, device):
+    """Scales of a rows x cols matrix in 8 bits, uninitialised: float32 of shape
+    (rows, ceil(cols / 128)) for 1 x 128 blocks (``block`` "row") or (ceil(rows / 128),
+    ceil(cols / 128)) for 128 x 128 blocks ("square").  The scales of one block column
+    lie together, as products read them fastest."""
+    import torch
+    if block not in ("row", "square"):
+        raise ValueError(f"block must be 'row' or 'square', got {block!r}")
+    high = rows if block == "row" else -(-rows // 128)
+    return torch.empty(-(-cols // 128), high, dtype=torch.float32, device=device).t()
+
+
+def _matrix(t, name, dtypes):
+    """Refuses what is not a GPU matrix with neighbouring elements in a row."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, it has {t.dim()}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be neighbours")
+
+
+def _fp8(codes, scales, name, scales_name) -> Fp8C:
+    """Codes and scales as ``muon_fp8_t``.  Rows of blocks are told by the scales' shape; a
+    matrix of one row is the same either way."""
+    import torch
+    formats = _fp8_formats()
+    _matrix(codes, name, formats)
+    rows, cols = codes.shape
+    if (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or not scales.is_cuda
+            or scales.dim() != 2):
+        raise TypeError(f"{scales_name} must be a float32 GPU matrix")
+    if scales.device != codes.device:
+        raise ValueError(f"{scales_name} is on {scales.device}, {name} on {codes.device}")
+    across = -(-cols // 128)
+    if tuple(scales.shape) == (rows, across):
+        high = 1
+    elif tuple(scales.shape) == (-(-rows // 128), across):
+        high = 128
+    else:
+        raise ValueError(f"{scales_name} has shape {tuple(scales.shape)}, {name} {tuple(codes.shape)}: "
+                         "expected one scale for each 1 x 128 or 128 x 128 block")
+    return Fp8C(codes.data_ptr(), scales.data_ptr(), rows, cols, codes.stride(0), scales.stride(0),
+                scales.stride(1), formats[codes.dtype], high)
+
+
+def muon_fp8_cast(x, codes=None, scales=None, codes_t=None, scales_t=None):
+    """``x`` (a matrix, f32 or bf16, with any row stride) into 8 bits: into ``codes``
+    (float8_e4m3fn or float8_e5m2, shaped like x) with ``scales``, its transpose into
+    ``codes_t`` with ``scales_t``, or both.  The scales' shape says the blocks: see
+    ``fp8_scales``."""
+    import torch
+    _matrix(x, "x", (torch.float32, torch.bfloat16))
+    if codes is None and codes_t is None:
+        raise ValueError("codes or codes_t must be given")
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("codes and scales belong together, and so do codes_t and scales_t")
+    _together(x, "x", codes=codes, codes_t=codes_t)
+    out = None if codes is None else _fp8(codes, scales, "codes", "scales")
+    out_t = None if codes_t is None else _fp8(codes_t, scales_t, "codes_t", "scales_t")
+    if out is not None and out_t is not None and out.block_rows != out_t.block_rows:
+        # one row or one column: its 1 x 128 and 128 x 128 blocks are the same
+        if x.shape[0] <= 1:
+            out.block_rows = out_t.block_rows
+        elif x.shape[1] <= 1:
+            out_t.block_rows = out.block_rows
+    dt = MUON_DTYPE_BF16 if x.dtype == torch.bfloat16 else MUON_DTYPE_F32
+    _launch(x.get_device(), load_library().muon_fp8_cast, x.data_ptr(), dt, x.shape[0], x.shape[1],
+            x.stride(0), None if out is None else ctypes.byref(out),
+            None if out_t is None else ctypes.byref(out_t))
+
+
+def muon_fp8_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Workspace bytes of ``muon_fp8_matmul`` for m x n products over k (0 for most)."""
+    out = ctypes.c_size_t(0)
+    check(load_library().muon_fp8_workspace_bytes(m, n, k, ctypes.byref(out)))
+    return out.value
+
+
+#: Default workspaces of the calls that keep no plan, one per (device, stream).
+_call_workspaces: dict = {}
+
+
+def _call_workspace(need: int, device):
+    """A cached workspace of at least ``need`` bytes for the current stream of ``device``;
+    called under that stream's lock."""
+    import torch
+    if _capturing(device):
+        raise RuntimeError("pass an explicit workspace to calls made under graph capture")
+    stream = torch.cuda.current_stream(device)
+    key = (device, stream.cuda_stream)
+    ws = _call_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        _call_workspaces.pop(key, None)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _call_workspaces[key] = ws
+    return ws
+
+
+def _launch_with_workspace(workspace, need: int, device, call, *args) -> None:
+    """``call(*args, workspace, bytes, stream)`` with the given workspace, or, where one is
+    needed, the stream's default one under its lock."""
+    import torch
+    if workspace is not None:
+        _require(workspace, "workspace", (torch.uint8,))
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
+        _launch(device.index, call, *args, workspace.data_ptr(), workspace.numel())
+    elif need == 0:
+        _launch(device.index, call, *args, None, 0)
+    else:
+        with _stream_lock(device):
+            ws = _call_workspace(need, device)
+            _launch(device.index, call, *args, ws.data_ptr(), ws.numel())
+
+
+def muon_fp8_matmul(a, a_scales, b, b_scales, out, accumulate: bool = False, workspace=None):
+    """``out = a b^T``, or ``out += a b^T``: a (m, k) and b (n, k) in 8 bits with their
+    scales, out (m, n) f32 or bf16 (f32 with ``accumulate``), all with any row stride.
+
+    ``workspace``: a uint8 GPU tensor of ``muon_fp8_workspace_bytes`` (default: a cached
+    one per device and stream, where one is needed; give one under graph capture)."""
+    import torch
+    left, right = _fp8(a, a_scales, "a", "a_scales"), _fp8(b, b_scales, "b", "b_scales")
+    _matrix(out, "out", (torch.float32, torch.bfloat16))
+    _together(a, "a", b=b, out=out)
+    m, n, k = left.rows, right.rows, left.cols
+    if tuple(out.shape) != (m, n):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
+    dt = MUON_DTYPE_BF16 if out.dtype == torch.bfloat16 else MUON_DTYPE_F32
+    need = 0 if workspace is not None else muon_fp8_workspace_bytes(m, n, k)
+    _launch_with_workspace(workspace, need, a.device, load_library().muon_fp8_matmul,
+                           ctypes.byref(left), ctypes.byref(right), out.data_ptr(), dt, out.stride(0),
+                           int(bool(accumulate)))
+
+
+#: Coefficients of ``muon_orthogonalize_stack`` where none are given: those of ``muon_step``.
+QUINTIC = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _stack(x, out) -> StackC:
+    import torch
+    both = (torch.float32, torch.bfloat16)
+    for t, name in ((x, "x"), (out, "out")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
+        if t.dtype not in both:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {both}")
+        if t.dim() not in (2, 3):
+            raise ValueError(f"{name} must be a matrix or a stack of them, it has {t.dim()} dimensions")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the elements of a row of {name} must be neighbours")
+
+    def dt(t):
+        return MUON_DTYPE_BF16 if t.dtype == torch.bfloat16 else MUON_DTYPE_F32
+
+    if out is None:
+        out = x
+    count = x.shape[0] if x.dim() == 3 else 1
+    return StackC(x.data_ptr(), out.data_ptr(), count, x.shape[-2], x.shape[-1],
+                  x.stride(0) if x.dim() == 3 else 0, x.stride(-2),
+                  out.stride(0) if out.dim() == 3 else 0, out.stride(-2), dt(x), dt(out))
+
+
+def muon_stack_workspace_bytes(x) -> int:
+    """Workspace bytes with which ``muon_orthogonalize_stack`` takes all of ``x`` at once;
+    those of ``x[:1]`` are the least."""
+    stack = _stack(x, None)
+    need = ctypes.c_size_t(0)
+    check(load_library().muon_stack_workspace_bytes(ctypes.byref(stack), ctypes.byref(need)))
+    return need.value
+
+
+def muon_orthogonalize_stack(x, out, coefficients=None, scale=None, workspace=None):
+    """``out = scale * NS(x)`` for a matrix or every matrix of a stack (count, rows, cols), f32
+    or bf16, with any strides between rows and matrices, in float32 accuracy.
+
+    ``coefficients``: (a, b, c) of every step (default ``QUINTIC``).  ``scale``: default
+    sqrt(max(1, rows / cols)).  ``workspace``: a uint8 GPU tensor of
+    ``muon_stack_workspace_bytes``, or less (default: a cached one per device and
+    stream; give one under graph capture)."""
+    stack = _stack(x, out)
+    _together(x, "x", out=out)
+    if x.shape != out.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, x {tuple(x.shape)}")
+    steps = [tuple(c) for c in (QUINTIC if coefficients is None else coefficients)]
+    if any(len(c) != 3 for c in steps):
+        raise ValueError("coefficients are (a, b, c) for every step")
+    flat = (ctypes.c_float * max(1, 3 * len(steps)))(*[float(v) for c in steps for v in c])
+    if scale is None:
+        scale = max(1.0, stack.rows / max(1, stack.cols)) ** 0.5
+    need = 0 if workspace is not None else muon_stack_workspace_bytes(x)
+    _launch_with_workspace(workspace, need, x.device, load_library().muon_orthogonalize_stack,
+                           ctypes.byref(stack), flat, len(steps), scale)
 
 
 def muon_profile_begin() -> None:

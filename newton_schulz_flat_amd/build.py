@@ -33,9 +33,15 @@ SOURCES = [
     "muon_clip.cpp",
     "k_clip.hip",
     "k_adamw.hip",
+    "muon_fp8.cpp",
+    "k_fp8_cast.hip",
+    "k_fp8_gemm.hip",
+    "muon_stack.cpp",
+    "k_stack.hip",
 ]
 # Sources whose arithmetic must round every operation separately.
-NO_CONTRACT = {"k_elementwise.hip", "k_norm_cast.hip", "k_clip.hip", "k_adamw.hip"}
+NO_CONTRACT = {"k_elementwise.hip", "k_norm_cast.hip", "k_clip.hip", "k_adamw.hip",
+               "k_fp8_cast.hip"}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,259 @@
+// Casts into 8-bit floats with a scale for each 1 x 128 or 128 x 128 block, of a
+// matrix and of its transpose in one pass.
+//
+//   s = fl(max(largest magnitude of the block, 2^-100) / L),  code = rne8(fl(x fl(1 / s)))
+//
+// with L the format's largest number.  |x| fl(1 / s) exceeds L by less than 4
+// float32 roundings, far below the middle between L and the next step, so no code
+// leaves the format's range and nothing has to be clamped.  Magnitudes are
+// compared as bit patterns, in which a NaN is above infinity: a block that
+// holds one gets the scale NaN.
+//
+// A workgroup takes a 128 x 128 tile, a thread an 8 x 8 block of it, held in
+// registers: 16 neighbouring lanes read one row's 128 elements.  Row blocks
+// reduce over these 16 lanes (DPP), column blocks over the 16 threads of a column
+// group (lanes, then LDS).  The transposed codes go through LDS so that each
+// row of the transpose leaves as 128 contiguous bytes.  It is an HBM stream.
+#include "fp8_internal.h"
+#include "k_common.h"
+
+#pragma clang fp contract(off)
+
+namespace muon {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct CastSide {
+    uint8_t* codes;  // null: not asked for
+    float* scales;
+    int64_t row_stride, scale_row, scale_col;
+};
+
+struct CastArgs {
+    const void* x;
+    int64_t row_stride;
+    int32_t rows, cols, col_tiles;
+    CastSide out, out_t;
+};
+
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight consecutive elements, of which the first `left` exist; the rest are 0.
+__device__ __forceinline__ void load8(const float* p, int left, float v[8]) {
+    if (left >= 8) {
+        const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p);
+        const f32x4_any b = *reinterpret_cast<const f32x4_any*>(p + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.f;
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int left, float v[8]) {
+    if (left >= 8) {
+        const u32x4_any a = *reinterpret_cast<const u32x4_any*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(a[j] << 16);
+            v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < left ? bf16_to_f32(p[j]) : 0.f;
+    }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Maximum over the 16 lanes of a DPP row, in all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x128, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x124, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x122, 0xF, 0xF, true)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x121, 0xF, 0xF, true)));
+    return x;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ float scale_of(uint32_t largest) {
+    const uint32_t floor_bits = 27u << 23;  // 2^-100
+    return __uint_as_float(max(largest, floor_bits)) / (E5M2 ? 57344.f : 448.f);
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    int w = 0;
+    if constexpr (E5M2) {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    }
+    return uint32_t(w);
+}
+
+// The first `left` of eight codes.
+__device__ __forceinline__ void store8(uint8_t* p, int left, uint2 w) {
+    if (left >= 8) {
+        u32x2_any t = {w.x, w.y};
+        *reinterpret_cast<u32x2_any*>(p) = t;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    }
+}
+
+template <typename T, bool SQUARE, bool E5M2>
+__global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
+    __shared__ uint32_t col_max[4][kFp8Block];
+    __shared__ uint2 turned[kFp8Block * 16];
+    const int tr = blockIdx.x / a.col_tiles, tc = blockIdx.x % a.col_tiles;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;  // 8-column and 8-row group
+    const int r0 = tr * kFp8Block + rg * 8, c0 = tc * kFp8Block + cg * 8;
+    const int rows_left = a.rows - r0, cols_left = a.cols - c0;
+
+    float v[8][8];
+    const T* x = static_cast<const T*>(a.x) + int64_t(r0) * a.row_stride + c0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        if (p < rows_left)
+            load8(x + p * a.row_stride, cols_left, v[p]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[p][j] = 0.f;
+    }
+
+    float s_all = 0.f, r_all = 0.f;
+    if constexpr (SQUARE) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[p][j]));
+        top = row_max(top);
+        if (cg == 0) col_max[0][rg] = top;
+        __syncthreads();
+        top = row_max(col_max[0][cg]);
+        s_all = scale_of<E5M2>(top);
+        r_all = 1.f / s_all;
+        if (threadIdx.x == 0) {
+            if (a.out.codes != nullptr)
+                a.out.scales[tr * a.out.scale_row + tc * a.out.scale_col] = s_all;
+            if (a.out_t.codes != nullptr)
+                a.out_t.scales[tc * a.out_t.scale_row + tr * a.out_t.scale_col] = s_all;
+        }
+    }
+
+    if (a.out.codes != nullptr) {
+        uint8_t* q = a.out.codes + int64_t(r0) * a.out.row_stride + c0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float s = s_all, r = r_all;
+            if constexpr (!SQUARE) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[p][j]));
+                s = scale_of<E5M2>(row_max(top));
+                r = 1.f / s;
+            }
+            const uint2 w = {encode4<E5M2>(v[p][0] * r, v[p][1] * r, v[p][2] * r, v[p][3] * r),
+                             encode4<E5M2>(v[p][4] * r, v[p][5] * r, v[p][6] * r, v[p][7] * r)};
+            if (p < rows_left) {
+                store8(q + p * a.out.row_stride, cols_left, w);
+                if (!SQUARE && cg == 0)
+                    a.out.scales[(r0 + p) * a.out.scale_row + tc * a.out.scale_col] = s;
+            }
+        }
+    }
+
+    if (a.out_t.codes == nullptr) return;
+    float rc[8];
+    if constexpr (SQUARE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rc[j] = r_all;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) top = max(top, magnitude(v[p][j]));
+            top = max(top, uint32_t(__shfl_xor(int(top), 16)));
+            top = max(top, uint32_t(__shfl_xor(int(top), 32)));
+            if ((threadIdx.x & 63) < 16) col_max[threadIdx.x >> 6][cg * 8 + j] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = cg * 8 + j;
+            const float s = scale_of<E5M2>(
+                max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c])));
+            rc[j] = 1.f / s;
+            if (rg == 0 && j < cols_left)
+                a.out_t.scales[(c0 + j) * a.out_t.scale_row + tr * a.out_t.scale_col] = s;
+        }
+    }
+    // 8-byte chunk (column c, rows of group g) lies at c * 16 + (g ^ (c / 8)): lanes that write
+    // together meet 16 different chunks
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float r = rc[j];
+        turned[(cg * 8 + j) * 16 + (rg ^ cg)] = {
+            encode4<E5M2>(v[0][j] * r, v[1][j] * r, v[2][j] * r, v[3][j] * r),
+            encode4<E5M2>(v[4][j] * r, v[5][j] * r, v[6][j] * r, v[7][j] * r)};
+    }
+    __syncthreads();
+    const int left = a.rows - tr * kFp8Block - cg * 8;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int c = p * 16 + rg;
+        const int col = tc * kFp8Block + c;
+        if (col < a.cols)
+            store8(a.out_t.codes + int64_t(col) * a.out_t.row_stride + tr * kFp8Block + cg * 8, left,
+                   turned[c * 16 + (cg ^ (c >> 3))]);
+    }
+}
+
+CastSide side_of(const muon_fp8_t* m) {
+    if (m == nullptr) return {nullptr, nullptr, 0, 0, 0};
+    return {static_cast<uint8_t*>(m->codes), m->scales, m->row_stride, m->scale_row, m->scale_col};
+}
+
+template <typename T>
+void enqueue(const CastArgs& a, int64_t tiles, bool square, bool e5m2, hipStream_t s) {
+    const dim3 grid = dim3(unsigned(tiles)), block = dim3(kThreads);
+    if (square)
+        e5m2 ? fp8_cast_kernel<T, true, true><<<grid, block, 0, s>>>(a)
+             : fp8_cast_kernel<T, true, false><<<grid, block, 0, s>>>(a);
+    else
+        e5m2 ? fp8_cast_kernel<T, false, true><<<grid, block, 0, s>>>(a)
+             : fp8_cast_kernel<T, false, false><<<grid, block, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_cast(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                           const muon_fp8_t* out, const muon_fp8_t* out_t, hipStream_t s) {
+    const muon_fp8_t& any = out != nullptr ? *out : *out_t;
+    CastArgs a;
+    a.x = x, a.row_stride = row_stride;
+    a.rows = int32_t(rows), a.cols = int32_t(cols);
+    a.col_tiles = int32_t(fp8_blocks(cols));
+    a.out = side_of(out), a.out_t = side_of(out_t);
+    // at most 2^21: rows * cols <= 2^34 and both sides <= 2^24
+    const int64_t tiles = fp8_blocks(rows) * a.col_tiles;
+    LaunchTimer timer("fp8_cast", s);
+    if (dtype == MUON_DTYPE_BF16)
+        enqueue<uint16_t>(a, tiles, any.block_rows != 1, any.format == MUON_FP8_E5M2, s);
+    else
+        enqueue<float>(a, tiles, any.block_rows != 1, any.format == MUON_FP8_E5M2, s);
+    return hipGetLastError();
+}
+
+}  // namespace muon

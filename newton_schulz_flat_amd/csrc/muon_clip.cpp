@@ -4,47 +4,14 @@
 // across the ABI.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <vector>
 
+#include "abi_checks.h"
 #include "clip_internal.h"
 
 namespace muon {
 
 namespace {
-
-__attribute__((format(printf, 3, 4))) int fail(Status* st, int code, const char* fmt, ...) {
-    st->code = code;
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(st->msg, sizeof(st->msg), fmt, ap);
-    va_end(ap);
-    return code;
-}
-
-// Runs an entry point's body and reports its status.
-template <typename F>
-int guarded(F body) try {
-    Status st{MUON_OK, ""};
-    return body(st) == MUON_OK ? int(MUON_OK) : report(st);
-}
-MUON_CATCH
-
-#define TRY(expr)                              \
-    do {                                       \
-        if ((expr) != MUON_OK) return st.code; \
-    } while (0)
-
-bool known_dtype(int dtype) { return dtype == MUON_DTYPE_F32 || dtype == MUON_DTYPE_BF16; }
-size_t dtype_bytes(int dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
-
-int check_pointer(const void* p, const char* name, size_t align, Status* st) {
-    if (p == nullptr) return fail(st, MUON_ERR_NULL_POINTER, "%s is NULL", name);
-    if (reinterpret_cast<uintptr_t>(p) % align != 0)
-        return fail(st, MUON_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, align);
-    return MUON_OK;
-}
 
 int check_count(int64_t n, const void* list, const char* name, Status* st) {
     if (n < 0) return fail(st, MUON_ERR_BAD_ARG, "%s count n = %lld < 0", name, (long long)n);
@@ -150,11 +117,6 @@ int check_max_norm(float v, Status* st) {
     if (!(v >= 0.f))  // NaN too
         return fail(st, MUON_ERR_BAD_ARG, "max_norm = %g is not a number >= 0", v);
     return MUON_OK;
-}
-
-int hip_status(hipError_t e, const char* what, Status* st) {
-    if (e == hipSuccess) return MUON_OK;
-    return fail(st, MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 size_t workspace_need(const muon_tensor_t* t, int64_t n) {

@@ -1,0 +1,144 @@
+// extern "C" entry points of the orthogonalization of stacks (declared, with their
+// contracts, in include/muon_step.h), and the exponents of its float16 pairs.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "abi_checks.h"
+#include "stack_internal.h"
+
+namespace muon {
+
+StackShape stack_shape(int64_t rows, int64_t cols) {
+    StackShape s;
+    s.tall = rows > cols;
+    s.r = std::min(rows, cols), s.c = std::max(rows, cols);
+    s.rp = (s.r + kStackPad - 1) / kStackPad * kStackPad;
+    s.cp = (s.c + kStackPad - 1) / kStackPad * kStackPad;
+    return s;
+}
+
+// Two iterates, A and B, 4 bytes an element, the partial sums of squares and the exponents.
+size_t stack_matrix_bytes(const StackShape& s) {
+    return size_t(2 * s.rp * s.cp + 2 * s.rp * s.rp) * 4 + kStackPartials * sizeof(double) +
+           kStackScales * sizeof(StackScale);
+}
+
+namespace {
+
+int check_stack(const muon_stack_t* s, Status* st) {
+    if (s == nullptr) return fail(st, MUON_ERR_NULL_POINTER, "stack is NULL");
+    if (s->count < 0 || s->count > kStackMaxCount)
+        return fail(st, MUON_ERR_BAD_ARG, "count %lld is outside [0, %lld]", (long long)s->count,
+                    (long long)kStackMaxCount);
+    if (s->rows < 1 || s->cols < 1 || s->rows > kMaxSide || s->cols > kMaxSide ||
+        s->rows * s->cols > kStackMaxNumel)
+        return fail(st, MUON_ERR_BAD_SHAPE, "%lld x %lld has a side outside [1, %lld] or more than %lld "
+                    "elements", (long long)s->rows, (long long)s->cols, (long long)kMaxSide,
+                    (long long)kStackMaxNumel);
+    if (!known_dtype(s->in_dtype) || !known_dtype(s->out_dtype))
+        return fail(st, MUON_ERR_BAD_ARG, "in_dtype %d or out_dtype %d is not MUON_DTYPE_F32 or _BF16",
+                    s->in_dtype, s->out_dtype);
+    return MUON_OK;
+}
+
+// Strides of in (or out); matrices of out lie apart.
+int check_strides(const muon_stack_t& s, int64_t stride, int64_t row, bool apart, const char* name,
+                  Status* st) {
+    const int64_t most = int64_t(1) << 40;
+    if (s.rows > 1 && (row < s.cols || row > kStackMaxNumel))
+        return fail(st, MUON_ERR_BAD_SHAPE, "%s_row %lld is outside [cols = %lld, %lld]", name,
+                    (long long)row, (long long)s.cols, (long long)kStackMaxNumel);
+    if (s.count > 1 && (stride < 0 || stride > most))
+        return fail(st, MUON_ERR_BAD_SHAPE, "%s_stride %lld is outside [0, 2^40]", name,
+                    (long long)stride);
+    if (!apart || s.count <= 1) return MUON_OK;
+    // matrices one behind the other, or side by side within longer rows
+    const int64_t span = s.rows > 1 ? (s.rows - 1) * row + s.cols : s.cols;
+    const bool beside = stride >= s.cols && (s.rows == 1 || (s.count - 1) * stride + s.cols <= row);
+    if (stride < span && !beside)
+        return fail(st, MUON_ERR_OVERLAP, "%s_stride %lld lets matrices of %lld elements overlap", name,
+                    (long long)stride, (long long)span);
+    return MUON_OK;
+}
+
+Range span_of(const muon_stack_t& s, const void* p, int64_t stride, int64_t row, int dtype,
+              const char* name) {
+    const int64_t last = (s.count > 1 ? (s.count - 1) * stride : 0) + (s.rows > 1 ? (s.rows - 1) * row : 0);
+    return {p, size_t(last + s.cols) * dtype_bytes(dtype), name};
+}
+
+// Coefficients are finite, and the bound on the largest singular value, which is 1 at first,
+// stays where float32 holds everything that is worked out from it.  (The kernels work the
+// same bounds out for each matrix, from its own norm.)
+int plan_steps(const float* k, int n, std::vector<StackStep>* steps, Status* st) {
+    float top = 1.001f;
+    steps->resize(size_t(n));
+    for (int t = 0; t < n; ++t) {
+        StackStep& s = (*steps)[size_t(t)];
+        s.a = k[3 * t], s.b = k[3 * t + 1], s.c = k[3 * t + 2];
+        for (float v : {s.a, s.b, s.c})
+            if (!std::isfinite(v))
+                return fail(st, MUON_ERR_BAD_ARG, "coefficients of step %d are not finite", t);
+        const double gram = double(top) * top;
+        const double poly = std::fabs(double(s.a)) + std::fabs(double(s.b)) * gram +
+                            std::fabs(double(s.c)) * gram * gram;
+        stack_scale(s, top);
+        if (!(top < kStackMaxNorm) || !(poly < kStackMaxNorm))
+            return fail(st, MUON_ERR_BAD_ARG,
+                        "coefficients of step %d let singular values grow beyond 2^24", t);
+    }
+    return MUON_OK;
+}
+
+}  // namespace
+
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+int muon_stack_workspace_bytes(const muon_stack_t* stack, size_t* out_bytes) {
+    return guarded([&](Status& st) {
+        if (out_bytes == nullptr) return fail(&st, MUON_ERR_NULL_POINTER, "out_bytes is NULL");
+        TRY(check_stack(stack, &st));
+        *out_bytes = size_t(stack->count) * stack_matrix_bytes(stack_shape(stack->rows, stack->cols));
+        return int(MUON_OK);
+    });
+}
+
+int muon_orthogonalize_stack(const muon_stack_t* stack, const float* coefficients, int n_steps,
+                             float scale, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    return guarded([&](Status& st) {
+        TRY(check_stack(stack, &st));
+        if (n_steps < 0 || n_steps > kMaxNsSteps)
+            return fail(&st, MUON_ERR_BAD_ARG, "n_steps = %d is outside [0, %d]", n_steps, kMaxNsSteps);
+        if (n_steps > 0 && coefficients == nullptr)
+            return fail(&st, MUON_ERR_NULL_POINTER, "coefficients is NULL");
+        TRY(check_scalar(scale, "scale", &st));
+        std::vector<StackStep> steps;
+        TRY(plan_steps(coefficients, n_steps, &steps, &st));
+        const muon_stack_t& s = *stack;
+        if (s.count == 0) return int(MUON_OK);
+        TRY(check_strides(s, s.in_stride, s.in_row, false, "in", &st));
+        TRY(check_strides(s, s.out_stride, s.out_row, true, "out", &st));
+        TRY(check_pointer(s.in, "in", dtype_bytes(s.in_dtype), &st));
+        TRY(check_pointer(s.out, "out", dtype_bytes(s.out_dtype), &st));
+        TRY(check_pointer(workspace, "workspace", kWsAlign, &st));
+        const size_t one = stack_matrix_bytes(stack_shape(s.rows, s.cols));
+        if (workspace_bytes < one)
+            return fail(&st, MUON_ERR_WORKSPACE_TOO_SMALL,
+                        "workspace has %zu bytes; one matrix needs %zu", workspace_bytes, one);
+        const size_t used = std::min(workspace_bytes, size_t(s.count) * one);
+        const Range all[3] = {span_of(s, s.in, s.in_stride, s.in_row, s.in_dtype, "in"),
+                              span_of(s, s.out, s.out_stride, s.out_row, s.out_dtype, "out"),
+                              {workspace, used, "workspace"}};
+        TRY(check_no_alias(all, 3, &st));
+        return hip_status(launch_stack(s, steps.data(), n_steps, scale, workspace, used, stream),
+                          "orthogonalize stack", &st);
+    });
+}
+
+}  // extern "C"

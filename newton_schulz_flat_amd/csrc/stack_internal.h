@@ -1,0 +1,95 @@
+// Internal declarations of the orthogonalization of stacks.
+#pragma once
+
+#include <cmath>
+
+#include <hip/hip_runtime.h>
+
+#include "muon_internal.h"
+
+namespace muon {
+
+constexpr int64_t kStackMaxCount = int64_t(1) << 20;
+constexpr int64_t kStackMaxNumel = int64_t(1) << 31;
+// Bound on the iterate's largest singular value, under which its float16 pairs keep
+// their digits.
+constexpr float kStackMaxNorm = 16777216.f;
+
+// Coefficients of one step.
+struct StackStep {
+    float a, b, c;
+};
+
+// Exponents with which one step's matrices are stored: X 2^sx, A 2^sa, B 2^sb.
+struct StackScale {
+    int32_t sx, sa, sb, reserved;
+};
+
+// The exponent that brings magnitudes of up to `top` to at most 2^15, half of
+// float16's range.  Below 2^-240 (an X of 2^-120) it stays where it is.
+__host__ __device__ inline int stack_exponent(float top, int square) {
+    const int least = square ? -240 : -120;
+    int e = least;
+    if (top > 0.f) {
+        const uint32_t bits = __builtin_bit_cast(uint32_t, top);
+        e = int(bits >> 23) - 126;  // top < 2^e (subnormal ones: 2^-126)
+    }
+    return 15 - (e > least ? e : least);
+}
+
+// The largest |a x + b x^3 + c x^5| on [0, top]: at an end or where the derivative
+// a + 3 b y + 5 c y^2, y = x^2, is zero.
+__host__ __device__ inline float stack_largest(const StackStep& k, float top) {
+    const float a = k.a, b = k.b, c = k.c;
+    const auto value = [&](float x) { return fabsf(x * (a + x * x * (b + c * x * x))); };
+    float most = value(top);
+    const auto at = [&](float y) {
+        if (y > 0.f && y < top * top) most = fmaxf(most, value(sqrtf(y)));
+    };
+    if (c == 0.f) {
+        if (b != 0.f) at(-a / (3.f * b));
+    } else {
+        const float d = 9.f * b * b - 20.f * a * c;
+        if (d >= 0.f) {
+            at((-3.f * b + sqrtf(d)) / (10.f * c));
+            at((-3.f * b - sqrtf(d)) / (10.f * c));
+        }
+    }
+    return most;
+}
+
+// One step: the exponents of its matrices where the largest singular value (and with it every
+// entry) of X is at most `top`, and that bound for the next X.  Roundings, these of the
+// bound included, add a part in a thousand at most.  The largest entry of A is at most top^2; where
+// that leaves float32's range the exponent follows from top's.
+__host__ __device__ inline StackScale stack_scale(const StackStep& k, float& top) {
+    StackScale s;
+    s.sx = stack_exponent(top, 0);
+    s.sa = 2 * s.sx - 15;
+    const float gram = top * top, poly = fabsf(k.b) + fabsf(k.c) * gram;
+    s.sb = s.sa - (15 - stack_exponent(poly, 0));
+    s.reserved = 0;
+    top = 1.001f * stack_largest(k, top);
+    return s;
+}
+
+// The shape as the iteration sees it: r <= c, sides padded to whole blocks.
+struct StackShape {
+    int64_t r, c, rp, cp;
+    bool tall;
+};
+
+// Sides are padded to this many elements; one more padded block is never read.
+constexpr int64_t kStackPad = 64;
+// Partial sums of squares of one matrix, at most.
+constexpr int kStackPartials = 64;
+// Entries of one matrix's table of exponents: one a step, and the last X's; a multiple of 16.
+constexpr int kStackScales = (kMaxNsSteps + 1 + 15) / 16 * 16;
+
+StackShape stack_shape(int64_t rows, int64_t cols);
+// Workspace bytes of one matrix.
+size_t stack_matrix_bytes(const StackShape& s);
+hipError_t launch_stack(const muon_stack_t& stack, const StackStep* steps, int n_steps, float scale,
+                        void* workspace, size_t workspace_bytes, hipStream_t s);
+
+}  // namespace muon

@@ -1,0 +1,193 @@
+"""GPU tests of the orthogonalization of stacks, against float64.
+
+The tolerance of a case comes from the arithmetic itself: the same iteration in
+float64 with every X, A and B rounded to the pairs' 22 digits deviates from the
+exact one by some amount; the kernels drop one product of halves (as much again),
+sum in float32 (2^-24 a step of up to 3 K / 32 of them, growing as their square root) and
+round the scaled input, so eight times that deviation is allowed, and 2e-6 for
+matrices that it leaves nearly exact."""
+
+import numpy as np
+import pytest
+
+import newton_schulz_flat_amd as nsf
+from oracle import fp8_oracle as fo
+from tests.gpu_helpers import rel_fro, say
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+POLISHED = [nsf.QUINTIC[0]] * 3 + [(1.875, -1.25, 0.375)] * 2
+
+
+def tolerance(u, steps, want, out):
+    tol = 2e-6 + 8 * rel_fro(fo.newton_schulz(u, steps, digits=22), want)
+    return tol + (2.0 ** -8 if out == "bf16" else 0.0)
+
+
+def check(x, out, steps=nsf.QUINTIC, scale=None):
+    kind = "bf16" if out.dtype == torch.bfloat16 else "f32"
+    xs = x.double().cpu().numpy().reshape(-1, *x.shape[-2:])
+    os = out.double().cpu().numpy().reshape(-1, *x.shape[-2:])
+    s = max(1.0, x.shape[-2] / x.shape[-1]) ** 0.5 if scale is None else scale
+    for u, o in zip(xs, os):
+        want = fo.newton_schulz(u, steps)
+        tol = tolerance(u, steps, want, kind)
+        err = rel_fro(o, s * want)
+        assert err <= tol, (x.shape, err, tol)
+
+
+def stack(count, rows, cols, dtype="f32", seed=0, std=1e-3, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    x = std * torch.randn(count, rows, cols + pad, generator=g)
+    return x.to(DT[dtype]).cuda()[:, :, :cols]
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 1, 1), (3, 1, 70), (2, 5, 3), (7, 16, 16), (4, 33, 65),
+                                             (16, 48, 64), (2, 64, 64), (3, 64, 200), (2, 65, 64),
+                                             (5, 100, 129), (2, 128, 513), (3, 300, 77), (1, 257, 255),
+                                             (2, 320, 640), (300, 20, 24), (1, 700, 900)])
+@pytest.mark.parametrize("dtype,out,pad", [("f32", "f32", 0), ("bf16", "bf16", 0), ("f32", "bf16", 5),
+                                           ("bf16", "f32", 23)])
+def test_stack(count, rows, cols, dtype, out, pad):
+    say("stack", count, rows, cols, dtype, out, pad)
+    x = stack(count, rows, cols, dtype, seed=rows + cols, pad=pad)
+    held = torch.full((count, rows, cols + pad), 3.0, dtype=DT[out], device="cuda")
+    nsf.muon_orthogonalize_stack(x, held[:, :, :cols])
+    check(x[:4], held[:4, :, :cols])
+    assert (held[:, :, cols:] == 3.0).all()
+    # each matrix depends on itself alone
+    one = torch.empty(rows, cols, dtype=DT[out], device="cuda")
+    nsf.muon_orthogonalize_stack(x[count - 1], one)
+    assert rel_fro(one.double().cpu().numpy(), held[-1, :, :cols].double().cpu().numpy()) <= 1e-5 + (
+        2.0 ** -8 if out == "bf16" else 0)
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 90), (130, 70), (512, 512)])
+def test_coefficients_and_scale(rows, cols):
+    x = stack(2, rows, cols, seed=9)
+    for steps in ([], [nsf.QUINTIC[0]], POLISHED, [(2.0, -1.5, 0.5)] * 12,
+                  [(8.0, -22.0, 15.0), (1.0, -0.2, 0.0)] + POLISHED, [(0.01, 0.0, 0.0)] * 3):
+        for scale in (None, 1.0, -0.25):
+            say("coefficients", rows, cols, steps, scale)
+            out = torch.empty_like(x)
+            nsf.muon_orthogonalize_stack(x, out, coefficients=steps, scale=scale)
+            check(x, out, steps, scale)
+
+
+def test_coefficients_that_let_values_grow_are_refused():
+    x = stack(1, 40, 90)
+    out = torch.zeros_like(x)
+    # |8 x - 22 x^3 + 16 x^5| reaches 2 at x = 1, and 4 x - 3 x^3 + 0.6 x^5 3.2 there
+    steps = [(8.0, -22.0, 16.0), (4.0, -3.0, 0.6)] + POLISHED
+    with pytest.raises(nsf.MuonError, match="BAD_ARG.*grow"):
+        nsf.muon_orthogonalize_stack(x, out, coefficients=steps)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("std", [1e-30, 1e-12, 1.0, 1e15, 1e30])
+@pytest.mark.parametrize("rows,cols", [(24, 60), (200, 150)])
+def test_sizes_of_numbers(rows, cols, std):
+    say("std", rows, cols, std)
+    x = stack(1, rows, cols, seed=3, std=std)
+    out = torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, out)
+    check(x, out)
+
+
+@pytest.mark.parametrize("rows,cols", [(24, 60), (200, 150)])
+def test_zero_matrices_and_low_rank(rows, cols):
+    say("zero, low rank", rows, cols)
+    x = stack(3, rows, cols, seed=4)
+    x[0] = 0
+    x[1] = x[1, :, :1] @ x[1, :1, :]
+    x[2, 3:] = 0
+    out = torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, out)
+    assert (out[0] == 0).all()
+    for k in (1, 2):
+        u = x[k].double().cpu().numpy()
+        want = fo.newton_schulz(u, nsf.QUINTIC) * max(1.0, rows / cols) ** 0.5
+        # roundings in the null space grow by the first coefficient a step: 482 times 2^-22 of
+        # an iterate's norm at each of five steps
+        err = np.linalg.norm(out[k].double().cpu().numpy() - want)
+        assert err <= 5 * 482 * 2.0 ** -22 * np.linalg.norm(want) * 2
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("rows,cols", [(24, 60), (200, 150)])
+@pytest.mark.parametrize("steps", [0, 2])
+def test_nan_and_infinity_stay_in_their_matrix(rows, cols, bad, steps):
+    say("nan", rows, cols, bad, steps)
+    x = stack(3, rows, cols, seed=6)
+    clean, out = torch.empty_like(x), torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, clean, coefficients=nsf.QUINTIC[:steps])
+    x[1, 5, 7] = bad
+    nsf.muon_orthogonalize_stack(x, out, coefficients=nsf.QUINTIC[:steps])
+    assert torch.isnan(out[1]).all()
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[2], clean[2])
+
+
+def test_strides_and_overlapping_inputs():
+    """Matrices side by side in longer rows, one matrix for all, windows that overlap."""
+    say("strides")
+    base = stack(1, 90, 400, seed=2)[0]
+    side = base.view(90, 4, 100).transpose(0, 1)            # four 90 x 100, 100 apart
+    out = torch.empty(90, 4, 100, device="cuda").transpose(0, 1)
+    nsf.muon_orthogonalize_stack(side, out)
+    check(side, out)
+    same = base[:, :100].unsqueeze(0).expand(3, 90, 100)
+    got = torch.empty(3, 90, 100, device="cuda")
+    nsf.muon_orthogonalize_stack(same, got)
+    assert torch.equal(got[0], out[0]) and torch.equal(got[1], got[2])
+    windows = base.as_strided((5, 40, 64), (7, 400, 1))
+    got = torch.empty(5, 40, 64, device="cuda")
+    nsf.muon_orthogonalize_stack(windows, got)
+    check(windows, got)
+
+
+@pytest.mark.parametrize("rows,cols", [(24, 60), (200, 150)])
+def test_groups_that_fit_the_workspace(rows, cols):
+    say("groups", rows, cols)
+    x = stack(5, rows, cols, seed=8)
+    one, two = torch.empty_like(x), torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, one)
+    for fit in (1, 2):
+        ws = torch.empty(nsf.muon_stack_workspace_bytes(x[:fit]), dtype=torch.uint8, device="cuda")
+        nsf.muon_orthogonalize_stack(x, two, workspace=ws)
+        assert torch.equal(one, two)
+    with pytest.raises(nsf.MuonError, match="WORKSPACE"):
+        nsf.muon_orthogonalize_stack(x, two, workspace=ws[:256])
+
+
+@pytest.mark.parametrize("rows,cols", [(24, 60), (200, 150), (512, 768)])
+def test_replayed(rows, cols):
+    say("replay", rows, cols)
+    x = stack(3, rows, cols, seed=1)
+    out, want = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(nsf.muon_stack_workspace_bytes(x), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nsf.muon_orthogonalize_stack(x, out, workspace=ws)
+    for seed in (2, 3, 4):
+        x.copy_(stack(3, rows, cols, seed=seed))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        nsf.muon_orthogonalize_stack(x, want)
+        assert torch.equal(out, want)
+        check(x, out)
+
+
+def test_same_update_as_the_flat_entry_point():
+    """The float32 mode of muon_orthogonalize on a flat buffer and the stack agree."""
+    say("flat")
+    x = stack(3, 256, 192, seed=7)
+    descs = [(k * 256 * 192, 256, 192) for k in range(3)]
+    flat, out = torch.empty(3 * 256 * 192, device="cuda"), torch.empty_like(x)
+    nsf.muon_orthogonalize(x.reshape(-1), flat, descs, mode="f32")
+    nsf.muon_orthogonalize_stack(x, out)
+    for k in range(3):
+        assert rel_fro(out[k].double().cpu().numpy(),
+                       flat.view_as(x)[k].double().cpu().numpy()) <= 2e-5
