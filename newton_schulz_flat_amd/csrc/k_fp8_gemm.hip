@@ -15,6 +15,9 @@
 // the rounding of out to bfloat16 (1.7e-3), but not float32.  For float32 the codes
 // are widened to bfloat16, which is exact, and four v_mfma_f32_16x16x32_bf16 sum
 // the block in float32 (6e-8 over the same operands), at half the rate.
+#include <algorithm>
+#include <type_traits>
+
 #include "fp8_internal.h"
 #include "k_common.h"
 
@@ -41,24 +44,30 @@ struct ProductArgs {
     Operand a, b;
     void* out;
     int64_t out_row;
+    float* partial;  // [split][m][n] where the blocks of k are split, else null
     int32_t k;
     int32_t tiles_m, tiles_n;
+    int32_t splits, per_split;  // of the blocks of k
     int32_t out_bf16, accumulate;
 };
 
-// 16 bytes of a row of codes from byte `at` on, those from byte k on as zeros.
+// 16 bytes of a row of codes from byte `at` on, those from byte k on as zeros.  At the end of
+// a row its last 16 bytes are read and shifted, so that nothing behind it is touched.
 __device__ __forceinline__ i32x4 load_chunk(const uint8_t* row, int at, int k) {
     if (at + 16 <= k) return i32x4(*reinterpret_cast<const u32x4_any*>(row + at));
-    i32x4 w = {0, 0, 0, 0};
-    for (int j = 0; j < 16; ++j)
-        if (at + j < k) {
-            const int byte = int(uint32_t(row[at + j]) << (8 * (j & 3)));
-            w.x |= j < 4 ? byte : 0;
-            w.y |= (j >> 2) == 1 ? byte : 0;
-            w.z |= (j >> 2) == 2 ? byte : 0;
-            w.w |= j >= 12 ? byte : 0;
-        }
-    return w;
+    if (at >= k) return {0, 0, 0, 0};
+    uint64_t lo = 0, hi = 0;
+    if (k >= 16) {
+        const u32x4_any t = *reinterpret_cast<const u32x4_any*>(row + k - 16);
+        lo = t.x | uint64_t(t.y) << 32, hi = t.z | uint64_t(t.w) << 32;
+        int drop = 8 * (at + 16 - k);  // bits, 8 to 120
+        if (drop >= 64) lo = hi, hi = 0, drop -= 64;
+        if (drop > 0) lo = lo >> drop | hi << (64 - drop), hi >>= drop;
+    } else {
+#pragma unroll 1
+        for (int j = k - 1; j >= at; --j) hi = hi << 8 | lo >> 56, lo = lo << 8 | row[j];
+    }
+    return {int(uint32_t(lo)), int(lo >> 32), int(uint32_t(hi)), int(hi >> 32)};
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -83,18 +92,31 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
     return {w[0].x, w[0].y, w[1].x, w[1].y, w[2].x, w[2].y, w[3].x, w[3].y};
 }
 
+// A lane's 32 codes of one row and block, as the inner sum takes them.
+template <int F, bool EXACT>
+struct Wide {
+    std::conditional_t<EXACT, bf16x8[4], i32x8> v;
+    __device__ __forceinline__ void set(const i32x8& codes) {
+        if constexpr (EXACT) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v[t] = widen8<F>(codes[2 * t], codes[2 * t + 1]);
+        } else {
+            v = codes;
+        }
+    }
+};
+
 // One 16 x 16 product over a block of 128.
 template <int FA, int FB, bool EXACT>
-__device__ __forceinline__ f32x4 block_product(const i32x8& a, const i32x8& b) {
+__device__ __forceinline__ f32x4 block_product(const Wide<FA, EXACT>& a, const Wide<FB, EXACT>& b) {
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     if constexpr (EXACT) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<FA>(a[2 * t], a[2 * t + 1]),
-                                                          widen8<FB>(b[2 * t], b[2 * t + 1]), sum, 0, 0, 0);
+            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[t], b.v[t], sum, 0, 0, 0);
         return sum;
     } else {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, sum, FA, FB, 0, 0, 0, 0);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, sum, FA, FB, 0, 0, 0, 0);
     }
 }
 
@@ -102,11 +124,20 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) {
     return {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 }
 
-// Four neighbouring results of row i, from column j on.
-__device__ __forceinline__ void store_result(const ProductArgs& g, int i, int j, f32x4 v) {
+// Four neighbouring results of row i, from column j on; of one split of k where there are several.
+__device__ __forceinline__ void store_result(const ProductArgs& g, int split, int i, int j, f32x4 v) {
     if (i >= g.a.rows || j >= g.b.rows) return;
     const int left = g.b.rows - j;
-    if (g.out_bf16) {
+    if (g.partial != nullptr) {
+        float* p = g.partial + (int64_t(split) * g.a.rows + i) * g.b.rows + j;
+        if (left >= 4) {
+            *reinterpret_cast<f32x4_any*>(p) = v;
+        } else {
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                if (t < left) p[t] = v[t];
+        }
+    } else if (g.out_bf16) {
         uint16_t* p = static_cast<uint16_t*>(g.out) + int64_t(i) * g.out_row + j;
         const uint16_t h[4] = {bf16_rne(v.x), bf16_rne(v.y), bf16_rne(v.z), bf16_rne(v.w)};
         if (left >= 4) {
@@ -131,105 +162,316 @@ __device__ __forceinline__ void store_result(const ProductArgs& g, int i, int j,
     }
 }
 
-// Any alignment and length: 128 x 128 tiles, operands through registers into
-// double-buffered LDS.  Row r's 16-byte chunk c lies at chunk c ^ (r / 2 mod 8), so that the
-// fragment reads of 16 rows meet every bank.
-constexpr int kTile = 128;
-constexpr int kOpBytes = kTile * kFp8Block;
+// ------------------------------------------------------------------- tiles
 
-template <int FA, int FB, bool EXACT>
-__global__ __launch_bounds__(256) void fp8_any_kernel(const ProductArgs g) {
-    __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * kOpBytes];
-    __shared__ __attribute__((aligned(16))) float scales[2][2 * kTile];
-    const int m0 = blockIdx.x / g.tiles_n * kTile, n0 = blockIdx.x % g.tiles_n * kTile;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+template <int TILE>
+struct Geo {
+    static constexpr int kWaves = TILE == 256 ? 8 : 4;
+    static constexpr int kThreads = kWaves * 64;
+    static constexpr int kWm = TILE / 2, kWn = TILE / (kWaves / 2);  // of a wave
+    static constexpr int kMi = kWm / 16, kNj = kWn / 16;
+    static constexpr int kOp = TILE * kFp8Block;          // bytes of one operand's block
+    static constexpr int kLoads = kOp / (kThreads * 16);  // 16-byte loads of a thread
+    static constexpr int kMinWaves = TILE == 64 ? 4 : 2;  // waves a SIMD has registers for
+};
 
-    // this thread's chunks: rows tid / 8 + 32 p, chunk tid % 8; rows behind the last read the last
-    const int chunk = tid & 7;
-    const uint8_t *pa[4], *pb[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const int r = (tid >> 3) + 32 * p;
-        pa[p] = g.a.codes + int64_t(min(m0 + r, g.a.rows - 1)) * g.a.row_stride;
-        pb[p] = g.b.codes + int64_t(min(n0 + r, g.b.rows - 1)) * g.b.row_stride;
-    }
+// 16 bytes to LDS at lds + 16 * lane from base + offset, or 4 bytes at lds + 4 * lane from p,
+// without passing through registers.  Written as assembly because the compiler
+// cannot tell the two halves of the double buffer apart and would wait for the load
+// before every LDS read; it has no output registers, and the kernel waits for it
+// (wait_loads) before the barrier.
+__device__ __forceinline__ void load16_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(offset), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load16_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(p), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load4_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                 :
+                 : "v"(p), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const lds_byte*)p));
+}
+
+// What lies behind the last column of a row of codes.
+__device__ const uint32_t zeros[4] = {0, 0, 0, 0};
+
+// The tile of workgroup b of `tiles`: workgroups go to the 8 XCDs in turn, and each XCD
+// takes a contiguous run of tiles, in bands of 4 tile rows, column by column, so that
+// the 32 tiles it works on at once share 12 panels of a and b in its L2.
+__device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& ti, int& tj) {
+    const int tiles = tiles_m * tiles_n, x = b & 7, low = tiles >> 3, more = tiles & 7;
+    const int t = x * low + min(x, more) + (b >> 3);
+    const int band = t / (4 * tiles_n), rest = t - band * 4 * tiles_n;
+    const int high = min(4, tiles_m - band * 4);
+    ti = band * 4 + rest % high, tj = rest / high;
+}
+
+// One TILE x TILE tile of out over a range of blocks of k.  Blocks are double-buffered in
+// LDS; row r's 16-byte chunk c lies at chunk c ^ (r / 2 mod 8), so that the fragment reads
+// of 16 rows meet every bank.  DIRECT (rows of codes that start at multiples of 16
+// bytes and hold a multiple of 16): loads go from memory to LDS directly; else through
+// registers, by bytes at the end of a row.  Rows behind the last one read the last.
+// SQUARE: b's blocks are 128 x 128, and a wave's columns (64 or fewer, within 128) share one
+// scale.
+template <int TILE, bool DIRECT, int FA, int FB, bool EXACT, bool SQUARE>
+__global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8_tile_kernel(
+    const ProductArgs g) {
+    using G = Geo<TILE>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2 * G::kOp];
+    __shared__ __attribute__((aligned(16))) float scales[2][2 * TILE];
+    const int tiles = g.tiles_m * g.tiles_n;
+    const int split = blockIdx.x / tiles;
+    int ti, tj;
+    tile_of(blockIdx.x - split * tiles, g.tiles_m, g.tiles_n, ti, tj);
+    const int m0 = ti * TILE, n0 = tj * TILE;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = (wave / (G::kWaves / 2)) * G::kWm, wn = (wave % (G::kWaves / 2)) * G::kWn;
+    const int nk = (g.k + kFp8Block - 1) / kFp8Block;
+    const int first = split * g.per_split, last = min(nk, first + g.per_split);
+
+    // chunk tid % 8 of rows tid / 8 + p * rows of a pass (a multiple of 16: the swizzle is the
+    // same in every pass); direct loads put their chunks one behind the other, so they
+    // fetch the chunk that belongs there
+    constexpr int kRows = G::kThreads / 8;
+    const int lr = tid >> 3, x = (lr >> 1) & 7;
+    const int chunk = DIRECT ? (tid & 7) ^ x : tid & 7;
+    const uint8_t* a_base = g.a.codes + int64_t(m0) * g.a.row_stride;
+    const uint8_t* b_base = g.b.codes + int64_t(n0) * g.b.row_stride;
+    const auto a_row = [&](int p) { return min(lr + p * kRows, g.a.rows - 1 - m0); };
+    const auto b_row = [&](int p) { return min(lr + p * kRows, g.b.rows - 1 - n0); };
+
+    // the scales of a block: a's by the first TILE threads of 2 TILE, b's by the others
+    static_assert(2 * TILE <= G::kThreads || TILE == 256, "a scale a thread");
+    const bool scaling = tid < 2 * TILE;
     const float* ps;
     int64_t ps_step;
     {
-        const Operand& o = tid < kTile ? g.a : g.b;
-        const int r = min((tid < kTile ? m0 : n0) + (tid & (kTile - 1)), o.rows - 1);
-        ps = o.scales + int64_t(r >> o.shift) * o.scale_row;
+        const Operand& o = tid < TILE ? g.a : g.b;
+        const int r = min((tid < TILE ? m0 : n0) + (tid & (TILE - 1)), o.rows - 1);
+        ps = o.scales + int64_t(r >> o.shift) * o.scale_row + int64_t(first) * o.scale_col;
         ps_step = o.scale_col;
     }
 
-    f32x4 acc[4][4];
+    uint32_t a_off[G::kLoads], b_off[G::kLoads];
+    i32x4 ra[G::kLoads], rb[G::kLoads];
+    float rs = 0.f;
+    if constexpr (DIRECT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int p = 0; p < G::kLoads; ++p) {
+            a_off[p] = uint32_t(a_row(p)) * uint32_t(g.a.row_stride) + chunk * 16;
+            b_off[p] = uint32_t(b_row(p)) * uint32_t(g.b.row_stride) + chunk * 16;
+        }
+    }
+    const uint32_t lds0 = lds_address(lds), scales0 = lds_address(scales);
+    // DIRECT: starts the loads of block kb into a buffer; else: into registers
+    auto fetch = [&](int kb, int buf) {
+        const int at = kb * kFp8Block;
+        if constexpr (DIRECT) {
+            const uint32_t to = lds0 + buf * 2 * G::kOp + wave * 1024;
+            if (at + kFp8Block <= g.k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
-
-    i32x4 ra[4], rb[4];
-    float rs;
-    auto fetch = [&](int kb) {
-        const int at = kb * kFp8Block + chunk * 16;
+                for (int p = 0; p < G::kLoads; ++p) {
+                    load16_to_lds(a_base + at, a_off[p], to + p * G::kThreads * 16);
+                    load16_to_lds(b_base + at, b_off[p], to + G::kOp + p * G::kThreads * 16);
+                }
+            } else {
+                const bool there = at + chunk * 16 < g.k;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) ra[p] = load_chunk(pa[p], at, g.k), rb[p] = load_chunk(pb[p], at, g.k);
-        rs = ps[kb * ps_step];
+                for (int p = 0; p < G::kLoads; ++p) {
+                    load16_to_lds(there ? a_base + at + a_off[p] : reinterpret_cast<const uint8_t*>(zeros),
+                                  to + p * G::kThreads * 16);
+                    load16_to_lds(there ? b_base + at + b_off[p] : reinterpret_cast<const uint8_t*>(zeros),
+                                  to + G::kOp + p * G::kThreads * 16);
+                }
+            }
+            if (scaling) load4_to_lds(ps, scales0 + buf * 2 * TILE * 4 + wave * 256);
+        } else {
+#pragma unroll
+            for (int p = 0; p < G::kLoads; ++p) {
+                ra[p] = load_chunk(a_base + a_row(p) * g.a.row_stride, at + chunk * 16, g.k);
+                rb[p] = load_chunk(b_base + b_row(p) * g.b.row_stride, at + chunk * 16, g.k);
+            }
+            if (scaling) rs = *ps;
+        }
+        ps += ps_step;
     };
     auto put = [&](int buf) {
+        if constexpr (!DIRECT) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int r = (tid >> 3) + 32 * p;
-            const int at = r * kFp8Block + ((chunk ^ ((r >> 1) & 7)) << 4);
-            *reinterpret_cast<i32x4*>(&lds[buf][at]) = ra[p];
-            *reinterpret_cast<i32x4*>(&lds[buf][kOpBytes + at]) = rb[p];
+            for (int p = 0; p < G::kLoads; ++p) {
+                const int at = (lr + p * kRows) * kFp8Block + ((chunk ^ x) << 4);
+                *reinterpret_cast<i32x4*>(&lds[buf][at]) = ra[p];
+                *reinterpret_cast<i32x4*>(&lds[buf][G::kOp + at]) = rb[p];
+            }
+            if (scaling) scales[buf][tid] = rs;
         }
-        scales[buf][tid] = rs;
     };
     auto fragment = [&](const unsigned char* op, int row0) {
-        const int r = row0 + (lane & 15), q = lane >> 4, x = (r >> 1) & 7;
-        return join(*reinterpret_cast<const i32x4*>(op + r * kFp8Block + ((q ^ x) << 4)),
-                    *reinterpret_cast<const i32x4*>(op + r * kFp8Block + (((q + 4) ^ x) << 4)));
+        const int r = row0 + (lane & 15), q = lane >> 4, y = (r >> 1) & 7;
+        return join(*reinterpret_cast<const i32x4*>(op + r * kFp8Block + ((q ^ y) << 4)),
+                    *reinterpret_cast<const i32x4*>(op + r * kFp8Block + (((q + 4) ^ y) << 4)));
     };
 
-    const int nk = (g.k + kFp8Block - 1) / kFp8Block;
-    fetch(0);
-    put(0);
-    __syncthreads();
-    for (int kb = 0; kb < nk; ++kb) {
-        const int buf = kb & 1;
-        if (kb + 1 < nk) fetch(kb + 1);
-        i32x8 fb[4];
-        f32x4 sb[4];
+    f32x4 acc[G::kMi][G::kNj];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            fb[j] = fragment(lds[buf] + kOpBytes, wn + 16 * j);
-            sb[j] = *reinterpret_cast<const f32x4*>(&scales[buf][kTile + wn + 16 * j + 4 * (lane >> 4)]);
+    for (int i = 0; i < G::kMi; ++i)
+#pragma unroll
+        for (int j = 0; j < G::kNj; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
+
+    fetch(first, 0);
+    for (int kb = first; kb < last; ++kb) {
+        const int buf = (kb - first) & 1;
+        if constexpr (DIRECT)
+            wait_loads();
+        else
+            put(buf);
+        __syncthreads();
+        if (kb + 1 < last) fetch(kb + 1, buf ^ 1);
+        Wide<FB, EXACT> fb[G::kNj];
+        f32x4 sb[G::kNj];
+        const float sb1 = scales[buf][TILE + wn];
+#pragma unroll
+        for (int j = 0; j < G::kNj; ++j) {
+            fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
+            if constexpr (!SQUARE)
+                sb[j] = *reinterpret_cast<const f32x4*>(&scales[buf][TILE + wn + 16 * j + 4 * (lane >> 4)]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const i32x8 fa = fragment(lds[buf], wm + 16 * i);
+        for (int i = 0; i < G::kMi; ++i) {
+            Wide<FA, EXACT> fa;
+            fa.set(fragment(lds[buf], wm + 16 * i));
             const float sa = scales[buf][wm + 16 * i + (lane & 15)];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] += block_product<FB, FA, EXACT>(fb[j], fa) * (sb[j] * sa);
+            for (int j = 0; j < G::kNj; ++j) {
+                const f32x4 sum = block_product(fb[j], fa);
+                if constexpr (SQUARE)
+                    acc[i][j] += sum * (sb1 * sa);
+                else
+                    acc[i][j] += sum * (sb[j] * sa);
+            }
         }
-        if (kb + 1 < nk) put(buf ^ 1);
-        __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < G::kMi; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            store_result(g, m0 + wm + 16 * i + (lane & 15), n0 + wn + 16 * j + 4 * (lane >> 4), acc[i][j]);
+        for (int j = 0; j < G::kNj; ++j)
+            store_result(g, split, m0 + wm + 16 * i + (lane & 15), n0 + wn + 16 * j + 4 * (lane >> 4),
+                         acc[i][j]);
 }
 
-// out of k = 0: zeros.
-__global__ __launch_bounds__(256) void fp8_zero_kernel(const ProductArgs g) {
-    const int64_t groups = int64_t(g.a.rows) * ((g.b.rows + 3) / 4);
+// ------------------------------------------------------------ few rows of a
+
+// m <= 16 MI rows of a against 16 rows of b a workgroup: b is read once, straight
+// into the instruction's registers, each of the 16 waves (8 for MI > 1) taking a share of
+// k's blocks; the waves' sums are added through LDS in wave order.  Bound by b's bytes: loads of
+// kAhead blocks are on their way at once.
+template <int MI>
+struct FewGeo {
+    static constexpr int kWaves = MI == 1 ? 16 : 8;
+    static constexpr int kAhead = MI == 1 ? 4 : 2;
+};
+
+template <int MI, int FA, int FB, bool EXACT>
+__global__ __launch_bounds__(FewGeo<MI>::kWaves * 64) void fp8_few_kernel(const ProductArgs g) {
+    using G = FewGeo<MI>;
+    __shared__ f32x4 sums[G::kWaves][MI][64];
+    const int split = blockIdx.x / g.tiles_n, n0 = (blockIdx.x - split * g.tiles_n) * 16;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nk = (g.k + kFp8Block - 1) / kFp8Block;
+    const int first = split * g.per_split, last = min(nk, first + g.per_split);
+    const int q = lane >> 4;
+
+    const int br = min(n0 + (lane & 15), g.b.rows - 1);
+    const uint8_t* pb = g.b.codes + int64_t(br) * g.b.row_stride;
+    const uint8_t* pa[MI];
+    const float* sa[MI];
+    f32x4 acc[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int r = min(16 * i + (lane & 15), g.a.rows - 1);
+        pa[i] = g.a.codes + int64_t(r) * g.a.row_stride;
+        sa[i] = g.a.scales + int64_t(r >> g.a.shift) * g.a.scale_row;
+        acc[i] = {0.f, 0.f, 0.f, 0.f};
+    }
+    const float* sb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        sb[t] = g.b.scales + int64_t(min(n0 + 4 * q + t, g.b.rows - 1) >> g.b.shift) * g.b.scale_row;
+
+    for (int kb0 = first + wave; kb0 < last; kb0 += G::kWaves * G::kAhead) {
+        i32x8 fb[G::kAhead], fa[G::kAhead][MI];
+        f32x4 tb[G::kAhead];
+        float ta[G::kAhead][MI];
+#pragma unroll
+        for (int u = 0; u < G::kAhead; ++u) {
+            const int kb = kb0 + u * G::kWaves;
+            if (kb >= last) continue;
+            const int at = kb * kFp8Block + q * 16;
+            fb[u] = join(load_chunk(pb, at, g.k), load_chunk(pb, at + 64, g.k));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) tb[u][t] = sb[t][kb * g.b.scale_col];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                fa[u][i] = join(load_chunk(pa[i], at, g.k), load_chunk(pa[i], at + 64, g.k));
+                ta[u][i] = sa[i][kb * g.a.scale_col];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < G::kAhead; ++u) {
+            if (kb0 + u * G::kWaves >= last) continue;
+            Wide<FB, EXACT> wb;
+            wb.set(fb[u]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                Wide<FA, EXACT> wa;
+                wa.set(fa[u][i]);
+                acc[i] += block_product(wb, wa) * (tb[u] * ta[u][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave < MI) {
+        f32x4 total = sums[0][wave][lane];
+        for (int w = 1; w < G::kWaves; ++w) total += sums[w][wave][lane];
+        store_result(g, split, 16 * wave + (lane & 15), n0 + 4 * q, total);
+    }
+}
+
+// out (+)= the splits' sums, in their order; zeros where there are none (k = 0).
+__global__ __launch_bounds__(256) void fp8_join_kernel(ProductArgs g) {
+    const float* partial = g.partial;
+    g.partial = nullptr;
+    const int per = (g.b.rows + 3) / 4;
+    const int64_t groups = int64_t(g.a.rows) * per, all = int64_t(g.a.rows) * g.b.rows;
     for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < groups; t += int64_t(gridDim.x) * 256) {
-        const int per = (g.b.rows + 3) / 4;
-        store_result(g, int(t / per), int(t % per) * 4, f32x4{0.f, 0.f, 0.f, 0.f});
+        const int i = int(t / per), j = int(t - int64_t(i) * per) * 4, left = g.b.rows - j;
+        const float* p = partial + int64_t(i) * g.b.rows + j;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < g.splits; ++k, p += all) {
+            if (left >= 4) {
+                sum += f32x4(*reinterpret_cast<const f32x4_any*>(p));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < left) sum[e] += p[e];
+            }
+        }
+        store_result(g, 0, i, j, sum);
     }
 }
 
@@ -238,35 +480,127 @@ Operand operand_of(const muon_fp8_t& m) {
             int32_t(m.rows), m.block_rows == 1 ? 0 : 7};
 }
 
+// How a product runs.
+struct Shape {
+    int tile;        // 0: few rows of a
+    int mi;          // few rows: fragments of 16
+    int64_t tiles;   // workgroups of one split
+    int splits, per_split;
+};
+
+// Splits of nk blocks of k over `tiles` workgroups, at least `least` blocks each, so that
+// `want` workgroups run.
+void split(Shape& s, int64_t nk, int64_t want, int64_t least) {
+    int64_t n = std::min({want / std::max<int64_t>(s.tiles, 1), nk / least, int64_t(16)});
+    n = std::max<int64_t>(n, 1);
+    s.per_split = int((nk + n - 1) / n);
+    s.splits = int((nk + s.per_split - 1) / std::max(s.per_split, 1));
+}
+
+Shape shape_of(int64_t m, int64_t n, int64_t k) {
+    const int64_t nk = fp8_blocks(k);
+    Shape s{};
+    if (m <= 64) {
+        s.mi = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+        s.tiles = (n + 15) / 16;
+        split(s, nk, 512, 16);
+        return s;
+    }
+    for (int tile : {256, 128, 64}) {
+        s.tile = tile;
+        s.tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+        if (s.tiles >= (tile == 256 ? 200 : 256)) break;
+    }
+    split(s, nk, 512, 8);
+    return s;
+}
+
+template <int FA, int FB, bool EXACT>
+void enqueue(const Shape& sh, const ProductArgs& g, bool direct, hipStream_t s) {
+    const dim3 grid = dim3(unsigned(sh.tiles * sh.splits));
+    if (sh.tile == 0) {
+        switch (sh.mi) {
+            case 1: fp8_few_kernel<1, FA, FB, EXACT><<<grid, dim3(FewGeo<1>::kWaves * 64), 0, s>>>(g); break;
+            case 2: fp8_few_kernel<2, FA, FB, EXACT><<<grid, dim3(FewGeo<2>::kWaves * 64), 0, s>>>(g); break;
+            default: fp8_few_kernel<4, FA, FB, EXACT><<<grid, dim3(FewGeo<4>::kWaves * 64), 0, s>>>(g);
+        }
+        return;
+    }
+    const bool square = g.b.shift != 0;
+    const auto run = [&](auto tile) {
+        constexpr int kTile = decltype(tile)::value;
+        const dim3 block = dim3(Geo<kTile>::kThreads);
+        if (direct)
+            square ? fp8_tile_kernel<kTile, true, FA, FB, EXACT, true><<<grid, block, 0, s>>>(g)
+                   : fp8_tile_kernel<kTile, true, FA, FB, EXACT, false><<<grid, block, 0, s>>>(g);
+        else if constexpr (kTile != 256)
+            fp8_tile_kernel<kTile, false, FA, FB, EXACT, false><<<grid, block, 0, s>>>(g);
+    };
+    if (sh.tile == 256)
+        run(std::integral_constant<int, 256>{});
+    else if (sh.tile == 128)
+        run(std::integral_constant<int, 128>{});
+    else
+        run(std::integral_constant<int, 64>{});
+}
+
 template <int FA, int FB>
-hipError_t enqueue(ProductArgs g, hipStream_t s) {
-    LaunchTimer timer("fp8_matmul", s);
-    g.tiles_m = (g.a.rows + kTile - 1) / kTile, g.tiles_n = (g.b.rows + kTile - 1) / kTile;
-    const dim3 grid = dim3(unsigned(int64_t(g.tiles_m) * g.tiles_n));
-    g.out_bf16 ? fp8_any_kernel<FA, FB, false><<<grid, dim3(256), 0, s>>>(g)
-               : fp8_any_kernel<FA, FB, true><<<grid, dim3(256), 0, s>>>(g);
-    return hipGetLastError();
+void enqueue(const Shape& sh, const ProductArgs& g, bool direct, hipStream_t s) {
+    g.out_bf16 ? enqueue<FA, FB, false>(sh, g, direct, s) : enqueue<FA, FB, true>(sh, g, direct, s);
+}
+
+// Rows of codes that direct loads take.
+bool direct_rows(const muon_fp8_t& m) {
+    return reinterpret_cast<uintptr_t>(m.codes) % 16 == 0 && m.cols % 16 == 0 &&
+           (m.rows == 1 || (m.row_stride % 16 == 0 && m.row_stride < (int64_t(1) << 24)));
 }
 
 }  // namespace
 
-size_t fp8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (m == 0 || n == 0 || k == 0) return 0;
+    const Shape s = shape_of(m, n, k);
+    if (s.splits == 1) return 0;
+    return (size_t(s.splits) * m * n * sizeof(float) + kWsAlign - 1) / kWsAlign * kWsAlign;
+}
 
 hipError_t launch_fp8_matmul(const muon_fp8_t& a, const muon_fp8_t& b, void* out, int out_dtype,
-                             int64_t out_row_stride, bool accumulate, void*, hipStream_t s) {
+                             int64_t out_row_stride, bool accumulate, void* workspace, hipStream_t s) {
     ProductArgs g{};
     g.a = operand_of(a), g.b = operand_of(b);
     g.out = out, g.out_row = out_row_stride, g.k = int32_t(a.cols);
     g.out_bf16 = out_dtype == MUON_DTYPE_BF16, g.accumulate = accumulate;
+    const int64_t groups = a.rows * ((b.rows + 3) / 4);
+    const dim3 join_grid = dim3(unsigned(std::min<int64_t>((groups + 255) / 256, 1 << 16)));
     if (g.k == 0) {
         if (accumulate) return hipSuccess;
-        LaunchTimer timer("fp8_matmul", s);
-        fp8_zero_kernel<<<dim3(1024), dim3(256), 0, s>>>(g);
+        LaunchTimer timer("fp8_join", s);
+        fp8_join_kernel<<<join_grid, dim3(256), 0, s>>>(g);
         return hipGetLastError();
     }
-    if (a.format == MUON_FP8_E5M2)
-        return b.format == MUON_FP8_E5M2 ? enqueue<1, 1>(g, s) : enqueue<1, 0>(g, s);
-    return b.format == MUON_FP8_E5M2 ? enqueue<0, 1>(g, s) : enqueue<0, 0>(g, s);
+    Shape sh = shape_of(a.rows, b.rows, a.cols);
+    const bool direct = direct_rows(a) && direct_rows(b);
+    if (sh.tile == 256 && !direct) {
+        // loads through registers have none to spare at this size
+        sh.tile = 128;
+        sh.tiles = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
+    }
+    g.tiles_m = sh.tile ? int32_t((a.rows + sh.tile - 1) / sh.tile) : 1;
+    g.tiles_n = int32_t(sh.tile ? (b.rows + sh.tile - 1) / sh.tile : sh.tiles);
+    g.splits = sh.splits, g.per_split = sh.per_split;
+    g.partial = sh.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+    {
+        LaunchTimer timer("fp8_matmul", s);
+        if (a.format == MUON_FP8_E5M2)
+            b.format == MUON_FP8_E5M2 ? enqueue<1, 1>(sh, g, direct, s) : enqueue<1, 0>(sh, g, direct, s);
+        else
+            b.format == MUON_FP8_E5M2 ? enqueue<0, 1>(sh, g, direct, s) : enqueue<0, 0>(sh, g, direct, s);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || sh.splits == 1) return e;
+    LaunchTimer timer("fp8_join", s);
+    fp8_join_kernel<<<join_grid, dim3(256), 0, s>>>(g);
+    return hipGetLastError();
 }
 
 }  // namespace muon
