@@ -16,6 +16,7 @@
 // are widened to bfloat16, which is exact, and four v_mfma_f32_16x16x32_bf16 sum
 // the block in float32 (6e-8 over the same operands), at half the rate.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fp8_internal.h"
@@ -341,26 +342,25 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
         __syncthreads();
         if (kb + 1 < last) fetch(kb + 1, buf ^ 1);
         Wide<FB, EXACT> fb[G::kNj];
-        f32x4 sb[G::kNj];
-        const float sb1 = scales[buf][TILE + wn];
 #pragma unroll
-        for (int j = 0; j < G::kNj; ++j) {
-            fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
-            if constexpr (!SQUARE)
-                sb[j] = *reinterpret_cast<const f32x4*>(&scales[buf][TILE + wn + 16 * j + 4 * (lane >> 4)]);
-        }
+        for (int j = 0; j < G::kNj; ++j) fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
+        const float sb1 = scales[buf][TILE + wn];
 #pragma unroll
         for (int i = 0; i < G::kMi; ++i) {
             Wide<FA, EXACT> fa;
             fa.set(fragment(lds[buf], wm + 16 * i));
             const float sa = scales[buf][wm + 16 * i + (lane & 15)];
+            // b's scales of single rows are read anew for every i: held, they cost the 256-tile
+            // with widened codes 44 spilled registers and twice the time
+            int at = TILE + wn + 4 * (lane >> 4);
+            if constexpr (!SQUARE && EXACT) asm volatile("" : "+v"(at));
 #pragma unroll
             for (int j = 0; j < G::kNj; ++j) {
                 const f32x4 sum = block_product(fb[j], fa);
                 if constexpr (SQUARE)
                     acc[i][j] += sum * (sb1 * sa);
                 else
-                    acc[i][j] += sum * (sb[j] * sa);
+                    acc[i][j] += sum * (*reinterpret_cast<const f32x4*>(&scales[buf][at + 16 * j]) * sa);
             }
         }
     }
@@ -374,81 +374,63 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
 
 // ------------------------------------------------------------ few rows of a
 
-// m <= 16 MI rows of a against 16 rows of b a workgroup: b is read once, straight
-// into the instruction's registers, each of the 16 waves (8 for MI > 1) taking a share of
-// k's blocks; the waves' sums are added through LDS in wave order.  Bound by b's bytes: loads of
-// kAhead blocks are on their way at once.
-template <int MI>
-struct FewGeo {
-    static constexpr int kWaves = MI == 1 ? 16 : 8;
-    static constexpr int kAhead = MI == 1 ? 4 : 2;
-};
+// At most 16 rows of a against 16 rows of b a workgroup: b is read once, straight into the
+// instruction's registers, each of 16 waves taking a share of k's blocks; the waves'
+// sums are added through LDS in wave order.  Bound by b's bytes once it runs: one row over 14336,
+// 4096 rows of b (58.7 MB, cold) takes 13.7 us, where 1024 rows over 4096 (4 MB) take 5.2.  2
+// blocks on their way a wave; 4 take 14.8, 8 waves 15.7 (4 blocks) and 17.9 (8), 4 waves 20.7 and more,
+// nontemporal loads 15.1.
+constexpr int kFewWaves = 16, kFewAhead = 2, kFewRows = 16;
 
-template <int MI, int FA, int FB, bool EXACT>
-__global__ __launch_bounds__(FewGeo<MI>::kWaves * 64) void fp8_few_kernel(const ProductArgs g) {
-    using G = FewGeo<MI>;
-    __shared__ f32x4 sums[G::kWaves][MI][64];
+template <int FA, int FB, bool EXACT, bool SQUARE>
+__global__ __launch_bounds__(kFewWaves * 64) void fp8_few_kernel(const ProductArgs g) {
+    __shared__ f32x4 sums[kFewWaves][64];
     const int split = blockIdx.x / g.tiles_n, n0 = (blockIdx.x - split * g.tiles_n) * 16;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nk = (g.k + kFp8Block - 1) / kFp8Block;
     const int first = split * g.per_split, last = min(nk, first + g.per_split);
-    const int q = lane >> 4;
+    const int q = lane >> 4, ar = min(lane & 15, g.a.rows - 1), br = min(n0 + (lane & 15), g.b.rows - 1);
 
-    const int br = min(n0 + (lane & 15), g.b.rows - 1);
+    const uint8_t* pa = g.a.codes + int64_t(ar) * g.a.row_stride;
     const uint8_t* pb = g.b.codes + int64_t(br) * g.b.row_stride;
-    const uint8_t* pa[MI];
-    const float* sa[MI];
-    f32x4 acc[MI];
+    const float* sa = g.a.scales + int64_t(ar >> g.a.shift) * g.a.scale_row;
+    const float* sb[SQUARE ? 1 : 4];
+    if constexpr (SQUARE) {
+        sb[0] = g.b.scales + int64_t(n0 >> 7) * g.b.scale_row;
+    } else {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int r = min(16 * i + (lane & 15), g.a.rows - 1);
-        pa[i] = g.a.codes + int64_t(r) * g.a.row_stride;
-        sa[i] = g.a.scales + int64_t(r >> g.a.shift) * g.a.scale_row;
-        acc[i] = {0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t)
+            sb[t] = g.b.scales + int64_t(min(n0 + 4 * q + t, g.b.rows - 1)) * g.b.scale_row;
     }
-    const float* sb[4];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int kb0 = first + wave; kb0 < last; kb0 += kFewWaves * kFewAhead) {
+        i32x8 fb[kFewAhead], fa[kFewAhead];
+        f32x4 scale[kFewAhead];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        sb[t] = g.b.scales + int64_t(min(n0 + 4 * q + t, g.b.rows - 1) >> g.b.shift) * g.b.scale_row;
-
-    for (int kb0 = first + wave; kb0 < last; kb0 += G::kWaves * G::kAhead) {
-        i32x8 fb[G::kAhead], fa[G::kAhead][MI];
-        f32x4 tb[G::kAhead];
-        float ta[G::kAhead][MI];
-#pragma unroll
-        for (int u = 0; u < G::kAhead; ++u) {
-            const int kb = kb0 + u * G::kWaves;
+        for (int u = 0; u < kFewAhead; ++u) {
+            const int kb = kb0 + u * kFewWaves;
             if (kb >= last) continue;
             const int at = kb * kFp8Block + q * 16;
             fb[u] = join(load_chunk(pb, at, g.k), load_chunk(pb, at + 64, g.k));
+            fa[u] = join(load_chunk(pa, at, g.k), load_chunk(pa, at + 64, g.k));
+            const float s = sa[kb * g.a.scale_col];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) tb[u][t] = sb[t][kb * g.b.scale_col];
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                fa[u][i] = join(load_chunk(pa[i], at, g.k), load_chunk(pa[i], at + 64, g.k));
-                ta[u][i] = sa[i][kb * g.a.scale_col];
-            }
+            for (int t = 0; t < 4; ++t) scale[u][t] = s * sb[SQUARE ? 0 : t][kb * g.b.scale_col];
         }
 #pragma unroll
-        for (int u = 0; u < G::kAhead; ++u) {
-            if (kb0 + u * G::kWaves >= last) continue;
+        for (int u = 0; u < kFewAhead; ++u) {
+            if (kb0 + u * kFewWaves >= last) continue;
             Wide<FB, EXACT> wb;
-            wb.set(fb[u]);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                Wide<FA, EXACT> wa;
-                wa.set(fa[u][i]);
-                acc[i] += block_product(wb, wa) * (tb[u] * ta[u][i]);
-            }
+            Wide<FA, EXACT> wa;
+            wb.set(fb[u]), wa.set(fa[u]);
+            acc += block_product(wb, wa) * scale[u];
         }
     }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sums[wave][i][lane] = acc[i];
+    sums[wave][lane] = acc;
     __syncthreads();
-    if (wave < MI) {
-        f32x4 total = sums[0][wave][lane];
-        for (int w = 1; w < G::kWaves; ++w) total += sums[w][wave][lane];
-        store_result(g, split, 16 * wave + (lane & 15), n0 + 4 * q, total);
+    if (wave == 0) {
+        for (int w = 1; w < kFewWaves; ++w) acc += sums[w][lane];
+        store_result(g, split, lane & 15, n0 + 4 * q, acc);
     }
 }
 
@@ -483,50 +465,62 @@ Operand operand_of(const muon_fp8_t& m) {
 // How a product runs.
 struct Shape {
     int tile;        // 0: few rows of a
-    int mi;          // few rows: fragments of 16
     int64_t tiles;   // workgroups of one split
     int splits, per_split;
 };
 
-// Splits of nk blocks of k over `tiles` workgroups, at least `least` blocks each, so that
-// `want` workgroups run.
-void split(Shape& s, int64_t nk, int64_t want, int64_t least) {
-    int64_t n = std::min({want / std::max<int64_t>(s.tiles, 1), nk / least, int64_t(16)});
-    n = std::max<int64_t>(n, 1);
-    s.per_split = int((nk + n - 1) / n);
-    s.splits = int((nk + s.per_split - 1) / std::max(s.per_split, 1));
+// About how many microseconds a product takes in `tiles` workgroups of one size and `splits`
+// splits of its nk blocks of k, from measurements of 21 shapes (100 x 700 over 300 to 8192 x
+// 4096 over 4096): a block takes the longer the more workgroups share a CU, up to `most` of them.
+// Off by 20% at most there; what it chooses takes at most 10% more than the best, where
+// 256-tiles throughout take 5 times the best (100 x 700), 64-tiles 1.7 times (4096^3).
+float estimate(int64_t m, int64_t n, int64_t nk, int tile, int64_t tiles, int64_t splits) {
+    const float most = tile == 256 ? 1.f : tile == 128 ? 2.f : 4.f;
+    const float once = tile == 256 ? 0.f : tile == 128 ? 0.55f : 0.4f;
+    const float more = tile == 256 ? 2.f : tile == 128 ? 0.4f : 0.15f;
+    const float per = float((nk + splits - 1) / splits);
+    const float load = float(tiles * splits) / 256.f;  // workgroups a CU
+    const float full = std::floor(load / most), rest = load - full * most;
+    float t = 2.5f + per * full * (once + more * most);
+    if (rest > 0.f) t += per * (tile == 256 ? more : once + more * std::max(rest, 0.4f));
+    if (splits > 1) t += 2.5f + float(splits * m) * float(n) * 1e-6f;
+    return t;
 }
 
 Shape shape_of(int64_t m, int64_t n, int64_t k) {
     const int64_t nk = fp8_blocks(k);
-    Shape s{};
-    if (m <= 64) {
-        s.mi = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-        s.tiles = (n + 15) / 16;
-        split(s, nk, 512, 16);
-        return s;
+    Shape best{};
+    if (m <= kFewRows) {
+        best.tiles = (n + 15) / 16;
+        // 1024 rows of b over k = 14336: 7.5 us in 4 splits, 10.5 in one; over 4096 6.2 and 5.0
+        const int64_t splits = std::clamp<int64_t>(std::min(256 / best.tiles, nk / 28), 1, 4);
+        best.per_split = int((nk + splits - 1) / splits);
+    } else {
+        float least = 0.f;
+        for (int tile : {256, 128, 64}) {
+            const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+            for (int64_t splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+                if (splits > 1 && (tiles * splits > 1024 || nk < 4 * splits)) break;
+                const float t = estimate(m, n, nk, tile, tiles, splits);
+                if (best.tiles == 0 || t < least)
+                    least = t, best = {tile, tiles, int(splits), int((nk + splits - 1) / splits)};
+            }
+        }
     }
-    for (int tile : {256, 128, 64}) {
-        s.tile = tile;
-        s.tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
-        if (s.tiles >= (tile == 256 ? 200 : 256)) break;
-    }
-    split(s, nk, 512, 8);
-    return s;
+    best.splits = int((nk + best.per_split - 1) / std::max(best.per_split, 1));
+    return best;
 }
 
 template <int FA, int FB, bool EXACT>
 void enqueue(const Shape& sh, const ProductArgs& g, bool direct, hipStream_t s) {
     const dim3 grid = dim3(unsigned(sh.tiles * sh.splits));
+    const bool square = g.b.shift != 0;
     if (sh.tile == 0) {
-        switch (sh.mi) {
-            case 1: fp8_few_kernel<1, FA, FB, EXACT><<<grid, dim3(FewGeo<1>::kWaves * 64), 0, s>>>(g); break;
-            case 2: fp8_few_kernel<2, FA, FB, EXACT><<<grid, dim3(FewGeo<2>::kWaves * 64), 0, s>>>(g); break;
-            default: fp8_few_kernel<4, FA, FB, EXACT><<<grid, dim3(FewGeo<4>::kWaves * 64), 0, s>>>(g);
-        }
+        const dim3 block = dim3(kFewWaves * 64);
+        square ? fp8_few_kernel<FA, FB, EXACT, true><<<grid, block, 0, s>>>(g)
+               : fp8_few_kernel<FA, FB, EXACT, false><<<grid, block, 0, s>>>(g);
         return;
     }
-    const bool square = g.b.shift != 0;
     const auto run = [&](auto tile) {
         constexpr int kTile = decltype(tile)::value;
         const dim3 block = dim3(Geo<kTile>::kThreads);
