@@ -38,6 +38,7 @@ SOURCES = [
     "k_fp8_gemm.hip",
     "muon_stack.cpp",
     "k_stack.hip",
+    "k_stack_small.hip",
 ]
 # Sources whose arithmetic must round every operation separately.
 NO_CONTRACT = {"k_elementwise.hip", "k_norm_cast.hip", "k_clip.hip", "k_adamw.hip",

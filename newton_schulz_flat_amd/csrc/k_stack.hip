@@ -24,41 +24,15 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "k_common.h"
-#include "stack_internal.h"
+#include "stack_device.h"
 
 namespace muon {
 
 namespace {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 enum Stage { kA = 0, kB = 1, kX = 2 };
 
 // ------------------------------------------------------------- norm and split
-
-struct InArgs {
-    const void* in;
-    void* out;  // split with no steps: the result itself
-    int64_t in_stride, in_row, out_stride, out_row;
-    double* partial;  // [matrix][kStackPartials]
-    _Float16* x;      // first iterate, [matrix][rp][2 cp]
-    int32_t rows, cols;
-    int32_t rp, cp;
-    int32_t parts;  // partial sums of one matrix
-    float scale;
-    StackScale* scales;  // [matrix][kStackScales]
-    int32_t n_steps;
-    StackStep steps[kMaxNsSteps];
-};
-
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ float load_one(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(uint16_t* p, float v) { *p = bf16_rne(v); }
 
 // Sum of squares in float64 (squares of float32 are exact there): part b % parts of matrix
 // b / parts, rows in turn, then over the workgroup in fixed order.
@@ -81,57 +55,23 @@ __global__ __launch_bounds__(256) void stack_norm_kernel(const InArgs a) {
         a.partial[int64_t(matrix) * kStackPartials + part] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
-// v 2^s as a pair, where v is already scaled.
-struct Pair {
-    _Float16 hi, lo;
-};
-__device__ __forceinline__ Pair split(float v) {
-    const _Float16 hi = static_cast<_Float16>(v);
-    return {hi, static_cast<_Float16>(v - static_cast<float>(hi))};
-}
-// 2^e for e <= 127; 0 below 2^-126, where what it multiplies is lost beside its sum's other term.
-__device__ __forceinline__ float power_of_two(int e) {
-    return e < -126 ? 0.f : __uint_as_float(uint32_t(127 + e) << 23);
-}
-
-// Element (i, j) of a matrix of pairs with padded row length cp: its high half; the low
-// one lies 32 further on.
-__device__ __forceinline__ int64_t pair_at(int64_t i, int j, int64_t cp) {
-    return i * (2 * cp) + (j >> 5) * 64 + (j & 31);
-}
-
-// 1 / (||U|| + 1e-7) of a matrix; an infinite norm makes the whole matrix NaN, like a NaN does.
-__device__ __forceinline__ float inverse_norm(const InArgs& a, int matrix, double* norm) {
-    double sum = 0.;
-    for (int p = 0; p < a.parts; ++p) sum += a.partial[int64_t(matrix) * kStackPartials + p];
-    *norm = sqrt(sum);
-    return *norm > 1.7e308 ? __uint_as_float(0x7fc00000u) : float(1. / (*norm + 1e-7));
-}
-
 // X = U / (||U|| + 1e-7) in the iteration's orientation, zero in the padding, 64 x 64 tiles.
 // A matrix's first tile also works out its exponents.
 template <typename T, bool TALL>
 __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
     __shared__ float tile[64][65];
-    __shared__ float inverse;
-    __shared__ int exponent;
     const int across = a.cp / 64, per = a.rp / 64 * across;
     const int matrix = blockIdx.x / per, t = blockIdx.x % per;
     const int i0 = t / across * 64, j0 = t % across * 64;  // in the iteration's orientation
-    if (threadIdx.x == 0) {
-        double norm;
-        inverse = inverse_norm(a, matrix, &norm);
-        // (a NaN: any exponents will do)
-        float top = norm <= 1.7e308 ? 1.001f * float(norm / (norm + 1e-7)) : 1.f;
-        exponent = stack_exponent(top, 0);
-        if (t == 0) {
-            StackScale* out = a.scales + int64_t(matrix) * kStackScales;
-            for (int k = 0; k < a.n_steps; ++k) out[k] = stack_scale(a.steps[k], top);
-            out[a.n_steps] = {stack_exponent(top, 0), 0, 0, 0};
-        }
+    const double norm = matrix_norm(a.partial + int64_t(matrix) * kStackPartials, a.parts);
+    const float inv = inverse_of(norm);
+    float top = first_bound(norm);
+    const float up = power_of_two(stack_exponent(top, 0));
+    if (t == 0 && threadIdx.x == 0) {
+        StackScale* out = a.scales + int64_t(matrix) * kStackScales;
+        for (int k = 0; k < a.n_steps; ++k) out[k] = stack_scale(a.steps[k], top);
+        out[a.n_steps] = {stack_exponent(top, 0), 0, 0, 0};
     }
-    __syncthreads();
-    const float inv = inverse;
     const T* u = static_cast<const T*>(a.in) + matrix * a.in_stride;
     const int x = threadIdx.x & 63;
     for (int y = threadIdx.x >> 6; y < 64; y += 4) {
@@ -140,7 +80,6 @@ __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
         tile[y][x] = there ? load_one(u + int64_t(i) * a.in_row + j) * inv : 0.f;
     }
     __syncthreads();
-    const float up = power_of_two(exponent);
     _Float16* out = a.x + int64_t(matrix) * a.rp * 2 * a.cp;
     for (int y = threadIdx.x >> 6; y < 64; y += 4) {
         const Pair p = split((TALL ? tile[x][y] : tile[y][x]) * up);
@@ -152,8 +91,7 @@ __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
 template <typename TI, typename TO>
 __global__ __launch_bounds__(256) void stack_scaled_kernel(const InArgs a) {
     const int matrix = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-    double norm;
-    const float inv = inverse_norm(a, matrix, &norm);
+    const float inv = inverse_of(matrix_norm(a.partial + int64_t(matrix) * kStackPartials, a.parts));
     const TI* u = static_cast<const TI*>(a.in) + matrix * a.in_stride;
     TO* o = static_cast<TO*>(a.out) + matrix * a.out_stride;
     const uint32_t numel = uint32_t(a.rows) * uint32_t(a.cols);
@@ -182,23 +120,6 @@ struct ProductArgs {
     float scale;
 };
 
-// 16 bytes from memory at base + offset to LDS at lds + 16 * lane, without passing
-// through registers.  Written as assembly because the compiler cannot tell the two halves
-// of the double buffer apart and would wait for the load before every LDS read; it has no
-// output registers, and the kernel waits for it (wait_loads) before the barrier.
-__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :
-                 : "v"(offset), "s"(base), "s"(lds)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-typedef __attribute__((address_space(3))) unsigned char lds_byte;
-__device__ __forceinline__ uint32_t lds_address(const unsigned char* p) {
-    return uint32_t(reinterpret_cast<uintptr_t>((const lds_byte*)p));
-}
-
 template <int TILE>
 struct Geo {
     static constexpr int kWaves = TILE == 256 ? 8 : 4;
@@ -210,48 +131,6 @@ struct Geo {
     static constexpr int kLds = 4 * kOp;
     static constexpr int kMinWaves = TILE == 256 ? 2 : TILE == 128 ? 2 : 4;
 };
-
-// Transposing LDS read: within 16 lanes, lane g points at 4 neighbouring elements of row
-// g / 4 of a 4 x 16 block, at column 4 (g % 4), and receives column g.
-__device__ __forceinline__ uint2 read_turned(const unsigned char* p) {
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-    return __builtin_bit_cast(
-        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(const_cast<unsigned char*>(p))));
-}
-
-__device__ __forceinline__ f32x4 mfma(f16x8 q, f16x8 p, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(q, p, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ void store_pairs(_Float16* p, const float v[4]) {
-    f16x4 hi, lo;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const Pair s = split(v[t]);
-        hi[t] = s.hi, lo[t] = s.lo;
-    }
-    *reinterpret_cast<f16x4*>(p) = hi;
-    *reinterpret_cast<f16x4*>(p + 32) = lo;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_result(const ProductArgs& g, int matrix, int i, int j,
-                                             const float v[4]) {
-    T* o = static_cast<T*>(g.out) + matrix * g.out_stride;
-    if (g.tall) {
-        // O's rows are the iterate's columns
-        if (i < g.cols)
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (j + t < g.rows) store_one(o + int64_t(j + t) * g.out_row + i, v[t]);
-    } else if (i < g.rows) {
-        o += int64_t(i) * g.out_row + j;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (j + t < g.cols) store_one(o + t, v[t]);
-    }
-}
 
 template <int TILE, int STAGE>
 __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void stack_gemm_kernel(
@@ -406,9 +285,11 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void sta
             if constexpr (STAGE == kX) {
                 if (g.last) {
                     if (g.out_bf16)
-                        store_result<uint16_t>(g, matrix, m, n, v);
+                        store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                     g.rows, g.cols, m, n, v);
                     else
-                        store_result<float>(g, matrix, m, n, v);
+                        store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                     g.rows, g.cols, m, n, v);
                     continue;
                 }
             }
@@ -453,8 +334,9 @@ int tile_for(int stage, int64_t rp, int64_t cp, int64_t count) {
     return 64;
 }
 
-hipError_t run_stage(int stage, const ProductArgs& g, int64_t count, hipStream_t s) {
-    switch (tile_for(stage, g.rp, g.cp, count)) {
+// The tile goes by the whole stack's count, so that groups of it are summed in the same order.
+hipError_t run_stage(int stage, const ProductArgs& g, int64_t count, int64_t all, hipStream_t s) {
+    switch (tile_for(stage, g.rp, g.cp, all)) {
         case 256: return enqueue_stage<256>(stage, g, count, s);
         case 128: return enqueue_stage<128>(stage, g, count, s);
         default: return enqueue_stage<64>(stage, g, count, s);
@@ -521,6 +403,8 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
+    if (sh.r <= 128)
+        return launch_stack_strips(st, sh, count, in.out, x[0], x[1], b, scales, steps, n, scale, s);
     for (int t = 0; t < n; ++t) {
         ProductArgs g{};
         g.x = x[t & 1], g.x_next = x[(t + 1) & 1], g.a = a, g.b = b;
@@ -529,7 +413,7 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
         g.tall = sh.tall, g.out_bf16 = st.out_dtype == MUON_DTYPE_BF16, g.last = t + 1 == n;
         g.scales = scales + t, g.step = steps[t], g.scale = scale;
         for (int stage : {kA, kB, kX})
-            if ((e = run_stage(stage, g, count, s)) != hipSuccess) return e;
+            if ((e = run_stage(stage, g, count, st.count, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -539,6 +423,7 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
 hipError_t launch_stack(const muon_stack_t& stack, const StackStep* steps, int n_steps, float scale,
                         void* workspace, size_t workspace_bytes, hipStream_t s) {
     const StackShape sh = stack_shape(stack.rows, stack.cols);
+    if (n_steps > 0 && stack_is_whole(sh)) return launch_stack_whole(stack, sh, steps, n_steps, scale, s);
     // a grid counts below 2^32 work-items: at most 2^22 tiles of 64 x 64 in a group
     const int64_t per = sh.rp / 64 * (sh.cp / 64);
     const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(int64_t(workspace_bytes / stack_matrix_bytes(sh)),

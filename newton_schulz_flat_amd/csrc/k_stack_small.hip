@@ -1,0 +1,518 @@
+// Newton-Schulz of stacks of matrices with a short side, on the pairs of float16 of k_stack.hip.
+//
+// stack_whole: matrices that fit a CU's LDS (shorter side up to 64).  One workgroup and one
+// launch a matrix: norm, split, all iterations and the result, X and A and B in LDS.
+//
+// stack_strip and stack_poly: shorter side up to 128.  B (r x r) is small, so one pass over X
+// makes the next iterate and its Gram matrix at once: a workgroup takes strips of 64
+// columns, X <- a X + B X in place, and adds X X^T of the strip to its own partial
+// Gram matrix; stack_poly adds a matrix's partial ones in order and makes B = b A + c A A of
+// them.  Two launches and one read and write of X a step, where the stages of k_stack.hip take
+// three and two reads.
+#include <algorithm>
+
+#include "stack_device.h"
+
+namespace muon {
+
+namespace {
+
+// Where a matrix of pairs lies in LDS: rows of `row_bytes` (a multiple of 256), chunk c (16 bytes)
+// of row r at chunk c ^ turn(r).  turn is a bijection of r mod 16, so 16 rows' reads of one chunk
+// meet every bank, and it takes the rows of one transposing read (0-3 and 8-11 mod 16, or
+// these + 4) to chunks of different 32 bytes.
+__device__ __forceinline__ int turn(int r) {
+    return (r & 3) << 1 | (r >> 3 & 1) << 3 | (r >> 2 & 1);
+}
+
+// Operand of 16 rows from row0 on, K step ks (32 columns), half 0 (high) or 1.
+__device__ __forceinline__ f16x8 rows_operand(const unsigned char* m, int row_bytes, int row0, int ks, int half) {
+    const int lane = threadIdx.x & 63, r = row0 + (lane & 15), c = ks * 8 + half * 4 + (lane >> 4);
+    return *reinterpret_cast<const f16x8*>(m + r * row_bytes + ((c ^ turn(r)) << 4));
+}
+// Operand of 16 columns from col0 on, K step ks (32 rows).
+__device__ __forceinline__ f16x8 turned_operand(const unsigned char* m, int row_bytes, int col0, int ks, int half) {
+    const int lane = threadIdx.x & 63, l = lane & 15, k = ks * 32 + (lane >> 4) * 8 + (l >> 2);
+    const int c = (col0 >> 5) * 8 + half * 4 + ((col0 >> 4) & 1) * 2 + ((l & 3) >> 1);
+    const uint2 lo = read_turned(m + k * row_bytes + ((c ^ turn(k)) << 4) + (l & 1) * 8);
+    const uint2 hi = read_turned(m + (k + 4) * row_bytes + ((c ^ turn(k + 4)) << 4) + (l & 1) * 8);
+    return __builtin_bit_cast(f16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
+}
+// Address of the high halves of elements (i, j..j+3), j a multiple of 4; the low ones' chunk
+// differs in bit 2, so does its place.
+__device__ __forceinline__ unsigned char* quad_at(unsigned char* m, int row_bytes, int i, int j, int half) {
+    const int c = (j >> 5) * 8 + half * 4 + ((j & 31) >> 3);
+    return m + i * row_bytes + ((c ^ turn(i)) << 4) + (j & 4) * 2;
+}
+__device__ __forceinline__ void put_quad(unsigned char* m, int row_bytes, int i, int j, const float v[4]) {
+    f16x4 hi, lo;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const Pair p = split(v[t]);
+        hi[t] = p.hi, lo[t] = p.lo;
+    }
+    *reinterpret_cast<f16x4*>(quad_at(m, row_bytes, i, j, 0)) = hi;
+    *reinterpret_cast<f16x4*>(quad_at(m, row_bytes, i, j, 1)) = lo;
+}
+__device__ __forceinline__ void get_quad(unsigned char* m, int row_bytes, int i, int j, float v[4]) {
+    const f16x4 hi = *reinterpret_cast<const f16x4*>(quad_at(m, row_bytes, i, j, 0));
+    const f16x4 lo = *reinterpret_cast<const f16x4*>(quad_at(m, row_bytes, i, j, 1));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = float(hi[t]) + float(lo[t]);
+}
+// acc += the three products of the halves.
+__device__ __forceinline__ f32x4 product(f16x8 qh, f16x8 ql, f16x8 ph, f16x8 pl, f32x4 acc) {
+    acc = mfma(ql, ph, acc);
+    acc = mfma(qh, pl, acc);
+    return mfma(qh, ph, acc);
+}
+
+// -------------------------------------------------------- one workgroup a matrix
+
+struct WholeArgs {
+    InArgs in;
+    int32_t out_bf16, tall;
+};
+
+// RP: rows, padded (32 or 64).  Waves share the tiles of 16 x 16 of A and B and the columns
+// of X; a column's new values depend on it and B alone, so X is renewed in place.
+template <int RP, typename T>
+__global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
+    extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+    __shared__ double sums[4];
+    const InArgs& g = w.in;
+    constexpr int kSquare = RP < 64 ? 256 : RP * 4;  // bytes of a row of A and B
+    constexpr int kF = RP / 16, kSteps = RP / 32;
+    const int x_row = g.cp * 4;
+    unsigned char *x = lds, *a = x + RP * x_row, *b = a + RP * kSquare;
+    const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const T* u = static_cast<const T*>(g.in) + matrix * g.in_stride;
+
+    // rows of U in turn to the waves, 64 columns at a time, or several short rows at once
+    const int wide = g.cols >= 64 ? 6 : 32 - __builtin_clz(g.cols - 1 | 1), at_once = 64 >> wide;
+    const int i0 = wave * at_once + (lane >> wide), j0 = lane & ((1 << wide) - 1);
+    double sum = 0.;
+#pragma unroll 4
+    for (int i = i0; i < g.rows; i += 4 * at_once)
+#pragma unroll 4
+        for (int j = j0; j < g.cols; j += 64) {
+            const double v = load_one(u + int64_t(i) * g.in_row + j);
+            sum = fma(v, v, sum);
+        }
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) sums[wave] = sum;
+    // zeros everywhere, for the padding
+    for (int at = tid * 16; at < RP * (x_row + 2 * kSquare); at += 256 * 16)
+        *reinterpret_cast<u32x4*>(lds + at) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+    const double norm = sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
+    const float inv = inverse_of(norm);
+    float top = first_bound(norm);
+    int sx = stack_exponent(top, 0);
+    const float up = power_of_two(sx);
+#pragma unroll 4
+    for (int i = i0; i < g.rows; i += 4 * at_once)
+#pragma unroll 4
+        for (int j = j0; j < g.cols; j += 64) {
+            const Pair p = split(load_one(u + int64_t(i) * g.in_row + j) * inv * up);
+            const int m = w.tall ? j : i, n = w.tall ? i : j;
+            unsigned char* at = quad_at(x, x_row, m, n & ~3, 0) + (n & 3) * 2;
+            unsigned char* low = quad_at(x, x_row, m, n & ~3, 1) + (n & 3) * 2;
+            *reinterpret_cast<_Float16*>(at) = p.hi;
+            *reinterpret_cast<_Float16*>(low) = p.lo;
+        }
+    __syncthreads();
+
+    const int k_steps = g.cp / 32;
+    constexpr int kMine = kF * kF / 4;  // tiles of A of a wave: of one row of tiles
+    const int fi = wave * kMine / kF;
+    for (int t = 0; t < g.n_steps; ++t) {
+        const StackScale s = stack_scale(g.steps[t], top);
+        // A = X X^T
+        f32x4 acc[kMine];
+        const auto store = [&](unsigned char* to) {
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int fj = (wave * kMine + q) % kF;
+                const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
+                put_quad(to, kSquare, fi * 16 + (lane & 15), fj * 16 + 4 * (lane >> 4), v);
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) acc[q] = {0.f, 0.f, 0.f, 0.f};
+        for (int ks = 0; ks < k_steps; ++ks) {
+            const f16x8 ph = rows_operand(x, x_row, fi * 16, ks, 0), pl = rows_operand(x, x_row, fi * 16, ks, 1);
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int fj = (wave * kMine + q) % kF;
+                acc[q] = product(rows_operand(x, x_row, fj * 16, ks, 0), rows_operand(x, x_row, fj * 16, ks, 1),
+                                 ph, pl, acc[q]);
+            }
+        }
+        const float down_a = power_of_two(s.sa - 2 * sx);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) acc[q] *= down_a;
+        store(a);
+        __syncthreads();
+        // B = b A + c A A, with this wave's tiles of A still in registers
+        const float down_b = g.steps[t].c * power_of_two(s.sb - 2 * s.sa), own_b = g.steps[t].b * power_of_two(s.sb - s.sa);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int fj = (wave * kMine + q) % kF;
+            f32x4 aa = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks)
+                aa = product(rows_operand(a, kSquare, fj * 16, ks, 0), rows_operand(a, kSquare, fj * 16, ks, 1),
+                             rows_operand(a, kSquare, fi * 16, ks, 0), rows_operand(a, kSquare, fi * 16, ks, 1), aa);
+            acc[q] = acc[q] * own_b + aa * down_b;
+        }
+        store(b);
+        __syncthreads();
+        // X <- a X + B X, 16 columns at a time
+        const bool last = t + 1 == g.n_steps;
+        const int next = stack_exponent(top, 0), to = last ? 0 : next;
+        float down_x = power_of_two(to - sx - s.sb), own_x = g.steps[t].a * power_of_two(to - sx);
+        if (last) down_x *= g.scale, own_x *= g.scale;
+        f16x8 bh[kF][kSteps], bl[kF][kSteps];
+#pragma unroll
+        for (int i = 0; i < kF; ++i)
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                bh[i][ks] = rows_operand(b, kSquare, i * 16, ks, 0);
+                bl[i][ks] = rows_operand(b, kSquare, i * 16, ks, 1);
+            }
+        for (int cf = wave; cf < g.cp / 16; cf += 4) {
+            f16x8 qh[kSteps], ql[kSteps];
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                qh[ks] = turned_operand(x, x_row, cf * 16, ks, 0);
+                ql[ks] = turned_operand(x, x_row, cf * 16, ks, 1);
+            }
+            f32x4 y[kF];
+#pragma unroll
+            for (int i = 0; i < kF; ++i) {
+                y[i] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) y[i] = product(qh[ks], ql[ks], bh[i][ks], bl[i][ks], y[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kF; ++i) {
+                const int m = i * 16 + (lane & 15), n = cf * 16 + 4 * (lane >> 4);
+                float v[4];
+                get_quad(x, x_row, m, n, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = own_x * v[e] + down_x * y[i][e];
+                if (!last)
+                    put_quad(x, x_row, m, n, v);
+                else if (w.out_bf16)
+                    store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, w.tall,
+                                 g.rows, g.cols, m, n, v);
+                else
+                    store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, w.tall, g.rows,
+                                 g.cols, m, n, v);
+            }
+        }
+        sx = next;
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------- strips of 64 columns
+
+struct StripArgs {
+    _Float16* x;    // [matrix][rp][2 cp]
+    float* gram;    // [matrix][part][tile of 16 x 16][lane][4]
+    _Float16* b;    // [matrix][row tile][K step][half][lane][8]
+    const StackScale* scales;  // this step's, of matrix 0
+    StackStep step;
+    void* out;
+    int64_t out_stride, out_row;
+    int32_t cp, parts, per;  // strips of 64 columns of one part
+    int32_t rows, cols, tall, out_bf16, last;
+    float scale;
+};
+
+template <int RP>
+struct StripGeo {
+    static constexpr int kWaves = RP / 16, kThreads = kWaves * 64;
+    static constexpr int kF = RP / 16, kSteps = RP / 32;
+    // tiles of the Gram matrix of a wave: 2 rows by kGn columns; of a strip: 2 by 2
+    static constexpr int kGn = kF * kF / kWaves / 2;
+    static constexpr int kOp = RP * 256;  // bytes of a strip
+    static constexpr int kLoads = kOp / (kThreads * 16);
+};
+
+// FIRST: X is only read (the Gram matrix of the first iterate).
+template <int RP, bool FIRST>
+__global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(const StripArgs g) {
+    using G = StripGeo<RP>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][G::kOp];
+    const int matrix = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int strips = g.cp / 64, first = part * g.per, end = min(strips, first + g.per);
+    const int64_t x_row = int64_t(g.cp) * 4;
+    unsigned char* x = reinterpret_cast<unsigned char*>(g.x) + int64_t(matrix) * RP * x_row;
+    const uint32_t lds0 = lds_address(lds[0]);
+    // wave's place: rows of tiles 2 * wr, 2 * wr + 1
+    const int wr = wave % (G::kF / 2), wc = wave / (G::kF / 2);
+
+    // a thread's chunks: chunk tid % 16 of rows tid / 16 + p * rows of a pass
+    constexpr int kRows = G::kThreads / 16;
+    uint32_t off[G::kLoads];
+#pragma unroll
+    for (int p = 0; p < G::kLoads; ++p) {
+        const int r = (tid >> 4) + p * kRows;
+        off[p] = uint32_t(r * x_row) + (((tid & 15) ^ turn(r)) << 4);
+    }
+    const auto fetch = [&](int strip, int buf) {
+#pragma unroll
+        for (int p = 0; p < G::kLoads; ++p)
+            load_to_lds(x + strip * 256, off[p], lds0 + buf * G::kOp + p * G::kThreads * 16 + wave * 1024);
+    };
+
+    StackScale s = {0, 0, 0, 0};
+    float down = 0.f, own = 0.f;
+    f16x8 bh[2][G::kSteps], bl[2][G::kSteps];
+    if constexpr (!FIRST) {
+        const StackScale* ex = g.scales + int64_t(matrix) * kStackScales;
+        s = ex[0];
+        const int to = g.last ? 0 : ex[1].sx;
+        down = power_of_two(to - s.sx - s.sb), own = g.step.a * power_of_two(to - s.sx);
+        if (g.last) down *= g.scale, own *= g.scale;
+        const f16x8* b = reinterpret_cast<const f16x8*>(g.b) + int64_t(matrix) * RP * RP / 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int ks = 0; ks < G::kSteps; ++ks) {
+                const f16x8* q = b + (((wr * 2 + i) * G::kSteps + ks) * 2) * 64 + lane;
+                bh[i][ks] = q[0], bl[i][ks] = q[64];
+            }
+    }
+    f32x4 gram[2][G::kGn];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < G::kGn; ++j) gram[i][j] = {0.f, 0.f, 0.f, 0.f};
+
+    fetch(first, 0);
+    for (int strip = first; strip < end; ++strip) {
+        unsigned char* m = lds[(strip - first) & 1];
+        wait_loads();
+        __syncthreads();
+        if (strip + 1 < end) fetch(strip + 1, (strip + 1 - first) & 1);
+        if constexpr (!FIRST) {
+            f32x4 y[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                y[0][j] = y[1][j] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < G::kSteps; ++ks) {
+                    const f16x8 qh = turned_operand(m, 256, (wc * 2 + j) * 16, ks, 0);
+                    const f16x8 ql = turned_operand(m, 256, (wc * 2 + j) * 16, ks, 1);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) y[i][j] = product(qh, ql, bh[i][ks], bl[i][ks], y[i][j]);
+                }
+            }
+            float v[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = (wr * 2 + i) * 16 + (lane & 15), col = (wc * 2 + j) * 16 + 4 * (lane >> 4);
+                    get_quad(m, 256, row, col, v[i][j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][j][e] = own * v[i][j][e] + down * y[i][j][e];
+                    if (g.last) {
+                        if (g.out_bf16)
+                            store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                         g.rows, g.cols, row, strip * 64 + col, v[i][j]);
+                        else
+                            store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                         g.rows, g.cols, row, strip * 64 + col, v[i][j]);
+                    }
+                }
+            if (g.last) continue;
+            __syncthreads();  // every wave has read the old strip
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    put_quad(m, 256, (wr * 2 + i) * 16 + (lane & 15), (wc * 2 + j) * 16 + 4 * (lane >> 4), v[i][j]);
+            __syncthreads();
+            // back to memory as it was read
+#pragma unroll
+            for (int p = 0; p < G::kLoads; ++p)
+                *reinterpret_cast<u32x4*>(x + strip * 256 + off[p]) =
+                    *reinterpret_cast<const u32x4*>(m + p * G::kThreads * 16 + tid * 16);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            f16x8 ph[2], pl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ph[i] = rows_operand(m, 256, (wr * 2 + i) * 16, ks, 0);
+                pl[i] = rows_operand(m, 256, (wr * 2 + i) * 16, ks, 1);
+            }
+#pragma unroll
+            for (int j = 0; j < G::kGn; ++j) {
+                const f16x8 qh = rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 0);
+                const f16x8 ql = rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) gram[i][j] = product(qh, ql, ph[i], pl[i], gram[i][j]);
+            }
+        }
+    }
+    if (!FIRST && g.last) return;
+    f32x4* to = reinterpret_cast<f32x4*>(g.gram) + (int64_t(matrix) * g.parts + part) * (RP * RP / 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < G::kGn; ++j)
+            to[((wr * 2 + i) * G::kF + wc * G::kGn + j) * 64 + lane] = gram[i][j];
+}
+
+// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.
+template <int RP>
+__global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_poly_kernel(const StripArgs g) {
+    using G = StripGeo<RP>;
+    constexpr int kRow = RP * 4;
+    __shared__ __attribute__((aligned(1024))) unsigned char a[RP * kRow];
+    const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % (G::kF / 2), wc = wave / (G::kF / 2);
+    const StackScale s = g.scales[int64_t(matrix) * kStackScales];
+    const f32x4* from = reinterpret_cast<const f32x4*>(g.gram) + int64_t(matrix) * g.parts * (RP * RP / 4);
+    f32x4 acc[2][G::kGn];
+    const float down_a = power_of_two(s.sa - 2 * s.sx);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < G::kGn; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < g.parts; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < G::kGn; ++j)
+                acc[i][j] += from[p * (RP * RP / 4) + ((wr * 2 + i) * G::kF + wc * G::kGn + j) * 64 + lane];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < G::kGn; ++j) {
+            acc[i][j] *= down_a;
+            const float v[4] = {acc[i][j].x, acc[i][j].y, acc[i][j].z, acc[i][j].w};
+            put_quad(a, kRow, (wr * 2 + i) * 16 + (lane & 15), (wc * G::kGn + j) * 16 + 4 * (lane >> 4), v);
+        }
+    __syncthreads();
+    const float down = g.step.c * power_of_two(s.sb - 2 * s.sa), own = g.step.b * power_of_two(s.sb - s.sa);
+    unsigned char* b = reinterpret_cast<unsigned char*>(g.b) + int64_t(matrix) * RP * RP * 4;
+#pragma unroll
+    for (int j = 0; j < G::kGn; ++j) {
+        f32x4 aa[2];
+        aa[0] = aa[1] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < G::kSteps; ++ks) {
+            const f16x8 qh = rows_operand(a, kRow, (wc * G::kGn + j) * 16, ks, 0);
+            const f16x8 ql = rows_operand(a, kRow, (wc * G::kGn + j) * 16, ks, 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                aa[i] = product(qh, ql, rows_operand(a, kRow, (wr * 2 + i) * 16, ks, 0),
+                                rows_operand(a, kRow, (wr * 2 + i) * 16, ks, 1), aa[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // element (m, n..n+3) in the order in which stack_strip's lanes take it
+            const int m = lane & 15, n = (wc * G::kGn + j) * 16 + 4 * (lane >> 4);
+            f16x4 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Pair p = split(own * acc[i][j][e] + down * aa[i][e]);
+                hi[e] = p.hi, lo[e] = p.lo;
+            }
+            unsigned char* at = b + ((((wr * 2 + i) * G::kSteps + (n >> 5)) * 2) * 64 + ((n & 31) >> 3) * 16 + m) * 16 +
+                                (n & 4) * 2;
+            *reinterpret_cast<f16x4*>(at) = hi;
+            *reinterpret_cast<f16x4*>(at + 1024) = lo;
+        }
+    }
+}
+
+}  // namespace
+
+bool stack_is_whole(const StackShape& sh) { return stack_whole_lds(sh) <= kStackWholeLds; }
+
+hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, const StackStep* steps, int n,
+                              float scale, hipStream_t s) {
+    WholeArgs w{};
+    InArgs& in = w.in;
+    in.in = st.in, in.out = st.out;
+    in.in_stride = st.in_stride, in.in_row = st.in_row;
+    in.out_stride = st.out_stride, in.out_row = st.out_row;
+    in.rows = int32_t(st.rows), in.cols = int32_t(st.cols);
+    in.cp = int32_t(sh.cp), in.n_steps = n, in.scale = scale;
+    std::copy(steps, steps + n, in.steps);
+    w.tall = sh.tall, w.out_bf16 = st.out_dtype == MUON_DTYPE_BF16;
+    const size_t lds = stack_whole_lds(sh);
+    const dim3 grid = dim3(unsigned(st.count)), block = dim3(256);
+    const auto run = [&](auto kernel) {
+        if (lds > 64 * 1024) {
+            // has to be told
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                     int(kStackWholeLds));
+            if (e != hipSuccess) return e;
+        }
+        LaunchTimer timer("stack_whole", s);
+        kernel<<<grid, block, lds, s>>>(w);
+        return hipGetLastError();
+    };
+    const bool bf16 = st.in_dtype == MUON_DTYPE_BF16;
+    if (sh.r <= 32) return bf16 ? run(stack_whole_kernel<32, uint16_t>) : run(stack_whole_kernel<32, float>);
+    return bf16 ? run(stack_whole_kernel<64, uint16_t>) : run(stack_whole_kernel<64, float>);
+}
+
+namespace {
+
+template <int RP>
+hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, const StackStep* steps, int n,
+                      hipStream_t s) {
+    const dim3 grid = dim3(unsigned(g.parts * count)), block = dim3(StripGeo<RP>::kThreads);
+    {
+        LaunchTimer timer("stack_gram", s);
+        stack_strip_kernel<RP, true><<<grid, block, 0, s>>>(g);
+    }
+    hipError_t e = hipGetLastError();
+    for (int t = 0; t < n && e == hipSuccess; ++t) {
+        g.scales = scales + t, g.step = steps[t], g.last = t + 1 == n;
+        {
+            LaunchTimer timer("stack_poly", s);
+            stack_poly_kernel<RP><<<dim3(unsigned(count)), block, 0, s>>>(g);
+        }
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        LaunchTimer timer("stack_strip", s);
+        stack_strip_kernel<RP, false><<<grid, block, 0, s>>>(g);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int64_t count, void* out, void* x,
+                               void* gram, void* b, const StackScale* scales, const StackStep* steps, int n,
+                               float scale, hipStream_t s) {
+    StripArgs g{};
+    g.x = static_cast<_Float16*>(x), g.gram = static_cast<float*>(gram), g.b = static_cast<_Float16*>(b);
+    g.out = out, g.out_stride = st.out_stride, g.out_row = st.out_row;
+    g.cp = int32_t(sh.cp), g.rows = int32_t(st.rows), g.cols = int32_t(st.cols);
+    g.tall = sh.tall, g.out_bf16 = st.out_dtype == MUON_DTYPE_BF16, g.scale = scale;
+    // about a workgroup a CU for the whole stack (not for `count`, so that groups make the same
+    // sums), and no more partial Gram matrices than the second iterate's place holds
+    const int64_t strips = sh.cp / 64, want = std::max<int64_t>(1, 256 / st.count);
+    const int64_t parts = std::min({strips, want, sh.cp / sh.rp, int64_t(32)});
+    g.per = int32_t((strips + parts - 1) / parts);
+    g.parts = int32_t((strips + g.per - 1) / g.per);
+    return sh.rp == 64 ? run_strips<64>(g, count, scales, steps, n, s)
+                       : run_strips<128>(g, count, scales, steps, n, s);
+}
+
+}  // namespace muon

@@ -1,0 +1,135 @@
+// Device helpers of the orthogonalization of stacks: pairs of float16, their products, loads to
+// LDS, and where a matrix begins and ends.
+#pragma once
+
+#include "k_common.h"
+#include "stack_internal.h"
+
+namespace muon {
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
+__device__ __forceinline__ float load_one(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(uint16_t* p, float v) { *p = bf16_rne(v); }
+
+// v 2^s as a pair, where v is already scaled.
+struct Pair {
+    _Float16 hi, lo;
+};
+__device__ __forceinline__ Pair split(float v) {
+    const _Float16 hi = static_cast<_Float16>(v);
+    return {hi, static_cast<_Float16>(v - static_cast<float>(hi))};
+}
+// 2^e for e <= 127; 0 below 2^-126, where what it multiplies is lost beside its sum's other term.
+__device__ __forceinline__ float power_of_two(int e) {
+    return e < -126 ? 0.f : __uint_as_float(uint32_t(127 + e) << 23);
+}
+
+// Element (i, j) of a matrix of pairs with padded row length cp: its high half; the low
+// one lies 32 further on.
+__device__ __forceinline__ int64_t pair_at(int64_t i, int j, int64_t cp) {
+    return i * (2 * cp) + (j >> 5) * 64 + (j & 31);
+}
+
+// 16 bytes from memory at base + offset to LDS at lds + 16 * lane, without passing
+// through registers.  Written as assembly because the compiler cannot tell the two halves
+// of the double buffer apart and would wait for the load before every LDS read; it has no
+// output registers, and the kernel waits for it (wait_loads) before the barrier.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(offset), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+__device__ __forceinline__ uint32_t lds_address(const unsigned char* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const lds_byte*)p));
+}
+
+// Transposing LDS read: within 16 lanes, lane g points at 4 neighbouring elements of row
+// g / 4 of a 4 x 16 block, at column 4 (g % 4), and receives column g.
+__device__ __forceinline__ uint2 read_turned(const unsigned char* p) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    return __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(const_cast<unsigned char*>(p))));
+}
+
+__device__ __forceinline__ f32x4 mfma(f16x8 q, f16x8 p, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(q, p, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void store_pairs(_Float16* p, const float v[4]) {
+    f16x4 hi, lo;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const Pair s = split(v[t]);
+        hi[t] = s.hi, lo[t] = s.lo;
+    }
+    *reinterpret_cast<f16x4*>(p) = hi;
+    *reinterpret_cast<f16x4*>(p + 32) = lo;
+}
+
+// Four neighbouring elements (i, j..j+3) of a matrix in the iteration's orientation to O in its
+// own: o, rows x cols with out_row elements between rows.
+template <typename T>
+__device__ __forceinline__ void store_result(T* o, int64_t out_row, bool tall, int rows, int cols, int i,
+                                             int j, const float v[4]) {
+    if (tall) {
+        // O's rows are the iterate's columns
+        if (i < cols)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (j + t < rows) store_one(o + int64_t(j + t) * out_row + i, v[t]);
+    } else if (i < rows) {
+        o += int64_t(i) * out_row + j;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (j + t < cols) store_one(o + t, v[t]);
+    }
+}
+
+struct InArgs {
+    const void* in;
+    void* out;  // split with no steps: the result itself
+    int64_t in_stride, in_row, out_stride, out_row;
+    double* partial;  // [matrix][kStackPartials]
+    _Float16* x;      // first iterate, [matrix][rp][2 cp]
+    int32_t rows, cols;
+    int32_t rp, cp;
+    int32_t parts;  // partial sums of one matrix
+    float scale;
+    StackScale* scales;  // [matrix][kStackScales]
+    int32_t n_steps;
+    StackStep steps[kMaxNsSteps];
+};
+
+// ||U|| of a matrix from its partial sums: every wave adds them by itself, in the same order.
+__device__ __forceinline__ double matrix_norm(const double* partial, int parts) {
+    const int lane = threadIdx.x & 63;
+    static_assert(kStackPartials == 64, "a lane each");
+    double sum = lane < parts ? partial[lane] : 0.;
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    return sqrt(sum);
+}
+// 1 / (||U|| + 1e-7); an infinite norm makes the whole matrix NaN, like a NaN does.
+__device__ __forceinline__ float inverse_of(double norm) {
+    return norm > 1.7e308 ? __uint_as_float(0x7fc00000u) : float(1. / (norm + 1e-7));
+}
+// The bound on the largest singular value of U / (||U|| + 1e-7) (a NaN: any will do).
+__device__ __forceinline__ float first_bound(double norm) {
+    return norm <= 1.7e308 ? 1.001f * float(norm / (norm + 1e-7)) : 1.f;
+}
+
+}  // namespace
+
+}  // namespace muon

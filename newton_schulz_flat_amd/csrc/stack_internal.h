@@ -87,6 +87,22 @@ constexpr int kStackPartials = 64;
 constexpr int kStackScales = (kMaxNsSteps + 1 + 15) / 16 * 16;
 
 StackShape stack_shape(int64_t rows, int64_t cols);
+
+// LDS of a matrix that one workgroup takes as a whole: X, A and B (whose rows are 256 bytes at
+// least).
+inline size_t stack_whole_lds(const StackShape& s) {
+    const int64_t rp = s.r <= 32 ? 32 : 64;
+    return s.r > 64 ? ~size_t(0) : size_t(rp * s.cp * 4 + 2 * rp * 256);
+}
+constexpr size_t kStackWholeLds = 156 * 1024;
+bool stack_is_whole(const StackShape& s);
+hipError_t launch_stack_whole(const muon_stack_t& stack, const StackShape& s, const StackStep* steps,
+                              int n_steps, float scale, hipStream_t stream);
+// Shorter side up to 128: all steps from the first iterate and its exponents on.  `count` matrices
+// of the stack; gram: room for rp * cp floats a matrix.
+hipError_t launch_stack_strips(const muon_stack_t& stack, const StackShape& s, int64_t count, void* out,
+                               void* x, void* gram, void* b, const StackScale* scales,
+                               const StackStep* steps, int n_steps, float scale, hipStream_t stream);
 // Workspace bytes of one matrix.
 size_t stack_matrix_bytes(const StackShape& s);
 hipError_t launch_stack(const muon_stack_t& stack, const StackStep* steps, int n_steps, float scale,
