@@ -109,7 +109,8 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
     const double norm = sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
     const float inv = inverse_of(norm);
     float top = first_bound(norm);
-    int sx = stack_exponent(top, 0);
+    const bool small = top < kStackSmallBound;
+    int sx = small ? stack_exponent(top, 0) : g.plan.scales[0].sx;
     const float up = power_of_two(sx);
 #pragma unroll 4
     for (int i = i0; i < g.rows; i += 4 * at_once)
@@ -127,8 +128,9 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
     const int k_steps = g.cp / 32;
     constexpr int kMine = kF * kF / 4;  // tiles of A of a wave: of one row of tiles
     const int fi = wave * kMine / kF;
-    for (int t = 0; t < g.n_steps; ++t) {
-        const StackScale s = stack_scale(g.steps[t], top);
+    for (int t = 0; t < g.plan.n; ++t) {
+        const StackStep step = g.plan.steps[t];
+        const StackScale s = small ? stack_scale(step, top) : g.plan.scales[t];
         // A = X X^T
         f32x4 acc[kMine];
         const auto store = [&](unsigned char* to) {
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
         store(a);
         __syncthreads();
         // B = b A + c A A, with this wave's tiles of A still in registers
-        const float down_b = g.steps[t].c * power_of_two(s.sb - 2 * s.sa), own_b = g.steps[t].b * power_of_two(s.sb - s.sa);
+        const float down_b = step.c * power_of_two(s.sb - 2 * s.sa), own_b = step.b * power_of_two(s.sb - s.sa);
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
             const int fj = (wave * kMine + q) % kF;
@@ -170,9 +172,9 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
         store(b);
         __syncthreads();
         // X <- a X + B X, 16 columns at a time
-        const bool last = t + 1 == g.n_steps;
-        const int next = stack_exponent(top, 0), to = last ? 0 : next;
-        float down_x = power_of_two(to - sx - s.sb), own_x = g.steps[t].a * power_of_two(to - sx);
+        const bool last = t + 1 == g.plan.n;
+        const int next = small ? stack_exponent(top, 0) : g.plan.scales[t + 1].sx, to = last ? 0 : next;
+        float down_x = power_of_two(to - sx - s.sb), own_x = step.a * power_of_two(to - sx);
         if (last) down_x *= g.scale, own_x *= g.scale;
         f16x8 bh[kF][kSteps], bl[kF][kSteps];
 #pragma unroll
@@ -221,7 +223,7 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
 // ------------------------------------------------------------- strips of 64 columns
 
 struct StripArgs {
-    _Float16* x;    // [matrix][rp][2 cp]
+    _Float16* x;    // [matrix][cp / 32][rp][64]
     float* gram;    // [matrix][part][tile of 16 x 16][lane][4]
     _Float16* b;    // [matrix][row tile][K step][half][lane][8]
     const StackScale* scales;  // this step's, of matrix 0
@@ -251,8 +253,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
     const int matrix = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int strips = g.cp / 64, first = part * g.per, end = min(strips, first + g.per);
-    const int64_t x_row = int64_t(g.cp) * 4;
-    unsigned char* x = reinterpret_cast<unsigned char*>(g.x) + int64_t(matrix) * RP * x_row;
+    unsigned char* x = reinterpret_cast<unsigned char*>(g.x) + int64_t(matrix) * RP * g.cp * 4;
     const uint32_t lds0 = lds_address(lds[0]);
     // wave's place: rows of tiles 2 * wr, 2 * wr + 1
     const int wr = wave % (G::kF / 2), wc = wave / (G::kF / 2);
@@ -263,15 +264,16 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
 #pragma unroll
     for (int p = 0; p < G::kLoads; ++p) {
         const int r = (tid >> 4) + p * kRows;
-        off[p] = uint32_t(r * x_row) + (((tid & 15) ^ turn(r)) << 4);
+        const int c = (tid & 15) ^ turn(r);
+        off[p] = (c >> 3) * RP * 128 + r * 128 + (c & 7) * 16;
     }
     const auto fetch = [&](int strip, int buf) {
 #pragma unroll
         for (int p = 0; p < G::kLoads; ++p)
-            load_to_lds(x + strip * 256, off[p], lds0 + buf * G::kOp + p * G::kThreads * 16 + wave * 1024);
+            load_to_lds(x + int64_t(strip) * G::kOp, off[p], lds0 + buf * G::kOp + p * G::kThreads * 16 + wave * 1024);
     };
 
-    StackScale s = {0, 0, 0, 0};
+    StackScale s{};
     float down = 0.f, own = 0.f;
     f16x8 bh[2][G::kSteps], bl[2][G::kSteps];
     if constexpr (!FIRST) {
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
             // back to memory as it was read
 #pragma unroll
             for (int p = 0; p < G::kLoads; ++p)
-                *reinterpret_cast<u32x4*>(x + strip * 256 + off[p]) =
+                *reinterpret_cast<u32x4*>(x + int64_t(strip) * G::kOp + off[p]) =
                     *reinterpret_cast<const u32x4*>(m + p * G::kThreads * 16 + tid * 16);
         }
 #pragma unroll
@@ -372,67 +374,60 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
             to[((wr * 2 + i) * G::kF + wc * G::kGn + j) * 64 + lane] = gram[i][j];
 }
 
-// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.
+// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.  16 waves,
+// each with tiles of one row of tiles.
+constexpr int kPolyThreads = 1024;
+
 template <int RP>
-__global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_poly_kernel(const StripArgs g) {
-    using G = StripGeo<RP>;
-    constexpr int kRow = RP * 4;
+__global__ __launch_bounds__(kPolyThreads) void stack_poly_kernel(const StripArgs g) {
+    constexpr int kRow = RP * 4, kF = RP / 16, kSteps = RP / 32, kMine = kF * kF / 16;
     __shared__ __attribute__((aligned(1024))) unsigned char a[RP * kRow];
     const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % (G::kF / 2), wc = wave / (G::kF / 2);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), fi = wave * kMine / kF, fj = wave * kMine % kF;
     const StackScale s = g.scales[int64_t(matrix) * kStackScales];
-    const f32x4* from = reinterpret_cast<const f32x4*>(g.gram) + int64_t(matrix) * g.parts * (RP * RP / 4);
-    f32x4 acc[2][G::kGn];
-    const float down_a = power_of_two(s.sa - 2 * s.sx);
+    const f32x4* from = reinterpret_cast<const f32x4*>(g.gram) + int64_t(matrix) * g.parts * (RP * RP / 4) +
+                        wave * kMine * 64 + lane;
+    f32x4 acc[kMine];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < G::kGn; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < kMine; ++q) acc[q] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int p = 0; p < g.parts; ++p)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int q = 0; q < kMine; ++q) acc[q] += from[p * (RP * RP / 4) + q * 64];
+    const float down_a = power_of_two(s.sa - 2 * s.sx);
 #pragma unroll
-            for (int j = 0; j < G::kGn; ++j)
-                acc[i][j] += from[p * (RP * RP / 4) + ((wr * 2 + i) * G::kF + wc * G::kGn + j) * 64 + lane];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < G::kGn; ++j) {
-            acc[i][j] *= down_a;
-            const float v[4] = {acc[i][j].x, acc[i][j].y, acc[i][j].z, acc[i][j].w};
-            put_quad(a, kRow, (wr * 2 + i) * 16 + (lane & 15), (wc * G::kGn + j) * 16 + 4 * (lane >> 4), v);
-        }
+    for (int q = 0; q < kMine; ++q) {
+        acc[q] *= down_a;
+        const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
+        put_quad(a, kRow, fi * 16 + (lane & 15), (fj + q) * 16 + 4 * (lane >> 4), v);
+    }
     __syncthreads();
     const float down = g.step.c * power_of_two(s.sb - 2 * s.sa), own = g.step.b * power_of_two(s.sb - s.sa);
     unsigned char* b = reinterpret_cast<unsigned char*>(g.b) + int64_t(matrix) * RP * RP * 4;
+    f32x4 aa[kMine];
 #pragma unroll
-    for (int j = 0; j < G::kGn; ++j) {
-        f32x4 aa[2];
-        aa[0] = aa[1] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < kMine; ++q) aa[q] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < G::kSteps; ++ks) {
-            const f16x8 qh = rows_operand(a, kRow, (wc * G::kGn + j) * 16, ks, 0);
-            const f16x8 ql = rows_operand(a, kRow, (wc * G::kGn + j) * 16, ks, 1);
+    for (int ks = 0; ks < kSteps; ++ks) {
+        const f16x8 ph = rows_operand(a, kRow, fi * 16, ks, 0), pl = rows_operand(a, kRow, fi * 16, ks, 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                aa[i] = product(qh, ql, rows_operand(a, kRow, (wr * 2 + i) * 16, ks, 0),
-                                rows_operand(a, kRow, (wr * 2 + i) * 16, ks, 1), aa[i]);
+        for (int q = 0; q < kMine; ++q)
+            aa[q] = product(rows_operand(a, kRow, (fj + q) * 16, ks, 0), rows_operand(a, kRow, (fj + q) * 16, ks, 1),
+                            ph, pl, aa[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+        // element (m, n..n+3) in the order in which stack_strip's lanes take it
+        const int m = lane & 15, n = (fj + q) * 16 + 4 * (lane >> 4);
+        f16x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const Pair p = split(own * acc[q][e] + down * aa[q][e]);
+            hi[e] = p.hi, lo[e] = p.lo;
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            // element (m, n..n+3) in the order in which stack_strip's lanes take it
-            const int m = lane & 15, n = (wc * G::kGn + j) * 16 + 4 * (lane >> 4);
-            f16x4 hi, lo;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Pair p = split(own * acc[i][j][e] + down * aa[i][e]);
-                hi[e] = p.hi, lo[e] = p.lo;
-            }
-            unsigned char* at = b + ((((wr * 2 + i) * G::kSteps + (n >> 5)) * 2) * 64 + ((n & 31) >> 3) * 16 + m) * 16 +
-                                (n & 4) * 2;
-            *reinterpret_cast<f16x4*>(at) = hi;
-            *reinterpret_cast<f16x4*>(at + 1024) = lo;
-        }
+        unsigned char* at = b + (((fi * kSteps + (n >> 5)) * 2) * 64 + ((n & 31) >> 3) * 16 + m) * 16 + (n & 4) * 2;
+        *reinterpret_cast<f16x4*>(at) = hi;
+        *reinterpret_cast<f16x4*>(at + 1024) = lo;
     }
 }
 
@@ -440,7 +435,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_poly_kernel(cons
 
 bool stack_is_whole(const StackShape& sh) { return stack_whole_lds(sh) <= kStackWholeLds; }
 
-hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, const StackStep* steps, int n,
+hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, const StackPlan& plan,
                               float scale, hipStream_t s) {
     WholeArgs w{};
     InArgs& in = w.in;
@@ -448,8 +443,7 @@ hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, cons
     in.in_stride = st.in_stride, in.in_row = st.in_row;
     in.out_stride = st.out_stride, in.out_row = st.out_row;
     in.rows = int32_t(st.rows), in.cols = int32_t(st.cols);
-    in.cp = int32_t(sh.cp), in.n_steps = n, in.scale = scale;
-    std::copy(steps, steps + n, in.steps);
+    in.cp = int32_t(sh.cp), in.plan = plan, in.scale = scale;
     w.tall = sh.tall, w.out_bf16 = st.out_dtype == MUON_DTYPE_BF16;
     const size_t lds = stack_whole_lds(sh);
     const dim3 grid = dim3(unsigned(st.count)), block = dim3(256);
@@ -473,19 +467,18 @@ hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, cons
 namespace {
 
 template <int RP>
-hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, const StackStep* steps, int n,
-                      hipStream_t s) {
+hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, const StackPlan& plan, hipStream_t s) {
     const dim3 grid = dim3(unsigned(g.parts * count)), block = dim3(StripGeo<RP>::kThreads);
     {
         LaunchTimer timer("stack_gram", s);
         stack_strip_kernel<RP, true><<<grid, block, 0, s>>>(g);
     }
     hipError_t e = hipGetLastError();
-    for (int t = 0; t < n && e == hipSuccess; ++t) {
-        g.scales = scales + t, g.step = steps[t], g.last = t + 1 == n;
+    for (int t = 0; t < plan.n && e == hipSuccess; ++t) {
+        g.scales = scales + t, g.step = plan.steps[t], g.last = t + 1 == plan.n;
         {
             LaunchTimer timer("stack_poly", s);
-            stack_poly_kernel<RP><<<dim3(unsigned(count)), block, 0, s>>>(g);
+            stack_poly_kernel<RP><<<dim3(unsigned(count)), dim3(kPolyThreads), 0, s>>>(g);
         }
         if ((e = hipGetLastError()) != hipSuccess) return e;
         LaunchTimer timer("stack_strip", s);
@@ -498,7 +491,7 @@ hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, cons
 }  // namespace
 
 hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int64_t count, void* out, void* x,
-                               void* gram, void* b, const StackScale* scales, const StackStep* steps, int n,
+                               void* gram, void* b, const StackScale* scales, const StackPlan& plan,
                                float scale, hipStream_t s) {
     StripArgs g{};
     g.x = static_cast<_Float16*>(x), g.gram = static_cast<float*>(gram), g.b = static_cast<_Float16*>(b);
@@ -511,8 +504,8 @@ hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int
     const int64_t parts = std::min({strips, want, sh.cp / sh.rp, int64_t(32)});
     g.per = int32_t((strips + parts - 1) / parts);
     g.parts = int32_t((strips + g.per - 1) / g.per);
-    return sh.rp == 64 ? run_strips<64>(g, count, scales, steps, n, s)
-                       : run_strips<128>(g, count, scales, steps, n, s);
+    return sh.rp == 64 ? run_strips<64>(g, count, scales, plan, s)
+                       : run_strips<128>(g, count, scales, plan, s);
 }
 
 }  // namespace muon

@@ -2,7 +2,6 @@
 // contracts, in include/muon_step.h), and the exponents of its float16 pairs.
 #include <algorithm>
 #include <cmath>
-#include <vector>
 
 #include "abi_checks.h"
 #include "stack_internal.h"
@@ -18,10 +17,52 @@ StackShape stack_shape(int64_t rows, int64_t cols) {
     return s;
 }
 
-// Two iterates, A and B, 4 bytes an element, the partial sums of squares and the exponents.
-size_t stack_matrix_bytes(const StackShape& s) {
-    return size_t(2 * s.rp * s.cp + 2 * s.rp * s.rp) * 4 + kStackPartials * sizeof(double) +
-           kStackScales * sizeof(StackScale);
+// About how many microseconds a stage takes: the K steps of a workgroup, which last the longer
+// the more workgroups share a CU, and where several share a tile the second pass that adds
+// their sums.
+static double stack_estimate(const StackTiling& t, int64_t count) {
+    const double most = t.tile == 256 ? 1 : t.tile == 128 ? 2 : 2;
+    const double once = t.tile == 256 ? 2.4 : t.tile == 128 ? 0.9 : 0.35, more = t.tile == 128 ? 1.0 : t.tile == 64 ? 0.25 : 0;
+    const double load = double(t.workers) * double(count) / 256, full = std::floor(load / most);
+    const double rest = load - full * most;
+    double us = 4 + full * double(t.per) * (once + more * (most - 1));
+    if (rest > 0) us += double(t.per) * (once + more * std::max(rest - 1, 0.0));
+    if (t.slots() > 0) us += 5 + double(t.slots()) * double(count) * double(t.slot_bytes()) * 2 / 4e6;
+    return us;
+}
+
+StackTiling stack_tiling(int stage, const StackShape& s, int64_t count) {
+    StackTiling best{};
+    double least = 0;
+    for (int tile : {256, 128, 64}) {
+        const int64_t tm = (s.rp + tile - 1) / tile, tn = (s.cp + tile - 1) / tile;
+        StackTiling t{tile, stage == kStageX ? tm * tn : tm * (tm + 1) / 2, (stage == kStageA ? s.cp : s.rp) / 32,
+                      0, 0};
+        const int64_t resident = tile == 256 ? 256 : 512;
+        for (int64_t workers : {t.tiles, 256 / count, resident / count, 2 * resident / count}) {
+            // (a tile's steps are shared where there are few tiles, and not below 4 steps each)
+            if (workers != t.tiles && (workers <= t.tiles / 4 || workers * 4 > t.tiles * t.steps || workers < 2))
+                continue;
+            t.workers = workers;
+            t.per = workers == t.tiles ? t.steps : (t.tiles * t.steps + workers - 1) / workers;
+            const double us = stack_estimate(t, count);
+            if (best.tile == 0 || us < least) least = us, best = t;
+        }
+    }
+    return best;
+}
+
+// Two iterates, A and B, 4 bytes an element, the partial sums of squares, the exponents, and the
+// sums of tiles that several workgroups share.
+size_t stack_matrix_bytes(const StackShape& s, int64_t count) {
+    size_t shared = 0;
+    if (s.r > 128)
+        for (int stage : {kStageA, kStageB, kStageX}) {
+            const StackTiling t = stack_tiling(stage, s, count);
+            shared = std::max(shared, size_t(t.slots()) * t.slot_bytes());
+        }
+    return size_t(2 * s.rp * s.cp + 2 * s.rp * s.rp) * 4 + size_t(stack_part_slots(s.r, s.c)) * sizeof(double) +
+           kStackScales * sizeof(StackScale) + shared;
 }
 
 namespace {
@@ -70,12 +111,12 @@ Range span_of(const muon_stack_t& s, const void* p, int64_t stride, int64_t row,
 
 // Coefficients are finite, and the bound on the largest singular value, which is 1 at first,
 // stays where float32 holds everything that is worked out from it.  (The kernels work the
-// same bounds out for each matrix, from its own norm.)
-int plan_steps(const float* k, int n, std::vector<StackStep>* steps, Status* st) {
+// same bounds out from a matrix's own norm where that is small.)
+int plan_steps(const float* k, int n, StackPlan* plan, Status* st) {
     float top = 1.001f;
-    steps->resize(size_t(n));
+    plan->n = n;
     for (int t = 0; t < n; ++t) {
-        StackStep& s = (*steps)[size_t(t)];
+        StackStep& s = plan->steps[t];
         s.a = k[3 * t], s.b = k[3 * t + 1], s.c = k[3 * t + 2];
         for (float v : {s.a, s.b, s.c})
             if (!std::isfinite(v))
@@ -83,11 +124,12 @@ int plan_steps(const float* k, int n, std::vector<StackStep>* steps, Status* st)
         const double gram = double(top) * top;
         const double poly = std::fabs(double(s.a)) + std::fabs(double(s.b)) * gram +
                             std::fabs(double(s.c)) * gram * gram;
-        stack_scale(s, top);
+        plan->scales[t] = stack_scale(s, top);
         if (!(top < kStackMaxNorm) || !(poly < kStackMaxNorm))
             return fail(st, MUON_ERR_BAD_ARG,
                         "coefficients of step %d let singular values grow beyond 2^24", t);
     }
+    plan->scales[n] = {int16_t(stack_exponent(top, 0)), 0, 0, 0};
     return MUON_OK;
 }
 
@@ -103,7 +145,8 @@ int muon_stack_workspace_bytes(const muon_stack_t* stack, size_t* out_bytes) {
     return guarded([&](Status& st) {
         if (out_bytes == nullptr) return fail(&st, MUON_ERR_NULL_POINTER, "out_bytes is NULL");
         TRY(check_stack(stack, &st));
-        *out_bytes = size_t(stack->count) * stack_matrix_bytes(stack_shape(stack->rows, stack->cols));
+        *out_bytes = size_t(stack->count) *
+                     stack_matrix_bytes(stack_shape(stack->rows, stack->cols), std::max<int64_t>(stack->count, 1));
         return int(MUON_OK);
     });
 }
@@ -118,8 +161,8 @@ int muon_orthogonalize_stack(const muon_stack_t* stack, const float* coefficient
         if (n_steps > 0 && coefficients == nullptr)
             return fail(&st, MUON_ERR_NULL_POINTER, "coefficients is NULL");
         TRY(check_scalar(scale, "scale", &st));
-        std::vector<StackStep> steps;
-        TRY(plan_steps(coefficients, n_steps, &steps, &st));
+        StackPlan plan;
+        TRY(plan_steps(coefficients, n_steps, &plan, &st));
         const muon_stack_t& s = *stack;
         if (s.count == 0) return int(MUON_OK);
         TRY(check_strides(s, s.in_stride, s.in_row, false, "in", &st));
@@ -127,7 +170,7 @@ int muon_orthogonalize_stack(const muon_stack_t* stack, const float* coefficient
         TRY(check_pointer(s.in, "in", dtype_bytes(s.in_dtype), &st));
         TRY(check_pointer(s.out, "out", dtype_bytes(s.out_dtype), &st));
         TRY(check_pointer(workspace, "workspace", kWsAlign, &st));
-        const size_t one = stack_matrix_bytes(stack_shape(s.rows, s.cols));
+        const size_t one = stack_matrix_bytes(stack_shape(s.rows, s.cols), s.count);
         if (workspace_bytes < one)
             return fail(&st, MUON_ERR_WORKSPACE_TOO_SMALL,
                         "workspace has %zu bytes; one matrix needs %zu", workspace_bytes, one);
@@ -136,7 +179,7 @@ int muon_orthogonalize_stack(const muon_stack_t* stack, const float* coefficient
                               span_of(s, s.out, s.out_stride, s.out_row, s.out_dtype, "out"),
                               {workspace, used, "workspace"}};
         TRY(check_no_alias(all, 3, &st));
-        return hip_status(launch_stack(s, steps.data(), n_steps, scale, workspace, used, stream),
+        return hip_status(launch_stack(s, plan, scale, workspace, used, stream),
                           "orthogonalize stack", &st);
     });
 }

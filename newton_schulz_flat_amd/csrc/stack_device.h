@@ -32,10 +32,13 @@ __device__ __forceinline__ float power_of_two(int e) {
     return e < -126 ? 0.f : __uint_as_float(uint32_t(127 + e) << 23);
 }
 
-// Element (i, j) of a matrix of pairs with padded row length cp: its high half; the low
-// one lies 32 further on.
-__device__ __forceinline__ int64_t pair_at(int64_t i, int j, int64_t cp) {
-    return i * (2 * cp) + (j >> 5) * 64 + (j & 31);
+// Element (i, j) of a matrix of pairs with rp rows (padded): its high half; the low one lies 32
+// further on.  Blocks of 32 columns lie one behind the other, each rp rows of 128 bytes: a K step of
+// a tile is one contiguous piece, whatever the matrix's width.  (Row after row, a K step of 14336
+// columns is 256 lines 57344 bytes apart, all in a few of L2's channels: stage A took 3.9 us a
+// K step, TODO here.)
+__device__ __forceinline__ int64_t pair_at(int64_t i, int j, int64_t rp) {
+    return ((j >> 5) * rp + i) * 64 + (j & 31);
 }
 
 // 16 bytes from memory at base + offset to LDS at lds + 16 * lane, without passing
@@ -48,7 +51,11 @@ __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, u
                  : "v"(offset), "s"(base), "s"(lds)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits until at most N loads are on their way.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
 __device__ __forceinline__ uint32_t lds_address(const unsigned char* p) {
@@ -102,22 +109,21 @@ struct InArgs {
     const void* in;
     void* out;  // split with no steps: the result itself
     int64_t in_stride, in_row, out_stride, out_row;
-    double* partial;  // [matrix][kStackPartials]
-    _Float16* x;      // first iterate, [matrix][rp][2 cp]
+    double* partial;  // [matrix][part_slots]
+    _Float16* x;      // first iterate, [matrix][cp / 32][rp][64]
     int32_t rows, cols;
     int32_t rp, cp;
-    int32_t parts;  // partial sums of one matrix
+    int32_t parts, part_slots;  // partial sums of one matrix, and their room
     float scale;
     StackScale* scales;  // [matrix][kStackScales]
-    int32_t n_steps;
-    StackStep steps[kMaxNsSteps];
+    StackPlan plan;
 };
+static_assert(sizeof(InArgs) + 64 <= 4096, "kernel arguments");
 
 // ||U|| of a matrix from its partial sums: every wave adds them by itself, in the same order.
 __device__ __forceinline__ double matrix_norm(const double* partial, int parts) {
-    const int lane = threadIdx.x & 63;
-    static_assert(kStackPartials == 64, "a lane each");
-    double sum = lane < parts ? partial[lane] : 0.;
+    double sum = 0.;
+    for (int p = threadIdx.x & 63; p < parts; p += 64) sum += partial[p];
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     return sqrt(sum);
 }

@@ -1,6 +1,7 @@
 // Internal declarations of the orthogonalization of stacks.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 
 #include <hip/hip_runtime.h>
@@ -22,7 +23,7 @@ struct StackStep {
 
 // Exponents with which one step's matrices are stored: X 2^sx, A 2^sa, B 2^sb.
 struct StackScale {
-    int32_t sx, sa, sb, reserved;
+    int16_t sx, sa, sb, reserved;
 };
 
 // The exponent that brings magnitudes of up to `top` to at most 2^15, half of
@@ -63,12 +64,9 @@ __host__ __device__ inline float stack_largest(const StackStep& k, float top) {
 // bound included, add a part in a thousand at most.  The largest entry of A is at most top^2; where
 // that leaves float32's range the exponent follows from top's.
 __host__ __device__ inline StackScale stack_scale(const StackStep& k, float& top) {
-    StackScale s;
-    s.sx = stack_exponent(top, 0);
-    s.sa = 2 * s.sx - 15;
+    const int sx = stack_exponent(top, 0), sa = 2 * sx - 15;
     const float gram = top * top, poly = fabsf(k.b) + fabsf(k.c) * gram;
-    s.sb = s.sa - (15 - stack_exponent(poly, 0));
-    s.reserved = 0;
+    const StackScale s = {int16_t(sx), int16_t(sa), int16_t(sa - (15 - stack_exponent(poly, 0))), 0};
     top = 1.001f * stack_largest(k, top);
     return s;
 }
@@ -81,12 +79,24 @@ struct StackShape {
 
 // Sides are padded to this many elements; one more padded block is never read.
 constexpr int64_t kStackPad = 64;
-// Partial sums of squares of one matrix, at most.
-constexpr int kStackPartials = 64;
-// Entries of one matrix's table of exponents: one a step, and the last X's; a multiple of 16.
-constexpr int kStackScales = (kMaxNsSteps + 1 + 15) / 16 * 16;
+// Partial sums of squares of one matrix, and the room for them.
+constexpr int64_t kStackPartials = 1024;
+inline int64_t stack_parts(int64_t r, int64_t c) { return std::min(kStackPartials, (r * c + 8191) / 8192); }
+inline int64_t stack_part_slots(int64_t r, int64_t c) { return (stack_parts(r, c) + 31) / 32 * 32; }
+// Entries of one matrix's table of exponents: one a step, and the last X's; a multiple of 32.
+constexpr int kStackScales = (kMaxNsSteps + 1 + 31) / 32 * 32;
 
 StackShape stack_shape(int64_t rows, int64_t cols);
+
+// The steps of a call with their exponents for a bound of 1 on the first iterate, which is
+// every matrix's but those whose norm is not far above 1e-7: these, below kStackSmallBound, have
+// theirs worked out by the kernels.
+struct StackPlan {
+    StackStep steps[kMaxNsSteps];
+    StackScale scales[kMaxNsSteps + 1];
+    int32_t n;
+};
+constexpr float kStackSmallBound = 0.5f;
 
 // LDS of a matrix that one workgroup takes as a whole: X, A and B (whose rows are 256 bytes at
 // least).
@@ -96,16 +106,30 @@ inline size_t stack_whole_lds(const StackShape& s) {
 }
 constexpr size_t kStackWholeLds = 156 * 1024;
 bool stack_is_whole(const StackShape& s);
-hipError_t launch_stack_whole(const muon_stack_t& stack, const StackShape& s, const StackStep* steps,
-                              int n_steps, float scale, hipStream_t stream);
+hipError_t launch_stack_whole(const muon_stack_t& stack, const StackShape& s, const StackPlan& plan,
+                              float scale, hipStream_t stream);
 // Shorter side up to 128: all steps from the first iterate and its exponents on.  `count` matrices
 // of the stack; gram: room for rp * cp floats a matrix.
 hipError_t launch_stack_strips(const muon_stack_t& stack, const StackShape& s, int64_t count, void* out,
                                void* x, void* gram, void* b, const StackScale* scales,
-                               const StackStep* steps, int n_steps, float scale, hipStream_t stream);
-// Workspace bytes of one matrix.
-size_t stack_matrix_bytes(const StackShape& s);
-hipError_t launch_stack(const muon_stack_t& stack, const StackStep* steps, int n_steps, float scale,
+                               const StackPlan& plan, float scale, hipStream_t stream);
+// Workspace bytes of one matrix of a stack of `count`.
+size_t stack_matrix_bytes(const StackShape& s, int64_t count);
+
+// How a stage's products run, for every matrix of a stack of `count`: tiles, and the workgroups
+// that share one matrix's K steps.
+enum StackStage { kStageA = 0, kStageB = 1, kStageX = 2 };
+struct StackTiling {
+    int tile;
+    int64_t tiles;    // of one matrix
+    int64_t steps;    // K steps of a tile
+    int64_t workers;  // workgroups of one matrix; tiles where each takes one tile
+    int64_t per;      // K steps of a workgroup
+    int64_t slots() const { return workers == tiles ? 0 : workers + tiles; }
+    size_t slot_bytes() const { return size_t(tile) * tile * 4; }
+};
+StackTiling stack_tiling(int stage, const StackShape& s, int64_t count);
+hipError_t launch_stack(const muon_stack_t& stack, const StackPlan& plan, float scale,
                         void* workspace, size_t workspace_bytes, hipStream_t s);
 
 }  // namespace muon
