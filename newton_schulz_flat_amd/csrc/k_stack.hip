@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void stack_norm_kernel(const InArgs a) {
 template <typename T, bool TALL>
 __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
     __shared__ float tile[64][65];
-    const int across = a.cp / 64, per = a.rp / 64 * across;
+    const int across = a.cp / 64, per = (a.rp + 63) / 64 * across;
     const int matrix = blockIdx.x / per, t = blockIdx.x % per;
     const int i0 = t / across * 64, j0 = t % across * 64;  // in the iteration's orientation
     const double norm = matrix_norm(a.partial + int64_t(matrix) * a.part_slots, a.parts);
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
     }
     __syncthreads();
     _Float16* out = a.x + int64_t(matrix) * a.rp * 2 * a.cp;
-    for (int y = threadIdx.x >> 6; y < 64; y += 4) {
+    for (int y = threadIdx.x >> 6; y < min(64, a.rp - i0); y += 4) {
         const Pair p = split((TALL ? tile[x][y] : tile[y][x]) * up);
         _Float16* q = out + pair_at(i0 + y, j0 + x, a.rp);
         q[0] = p.hi, q[32] = p.lo;
@@ -491,7 +491,7 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
     }
     {
         LaunchTimer timer("stack_split", s);
-        const dim3 grid = dim3(unsigned(sh.rp / 64 * (sh.cp / 64) * count));
+        const dim3 grid = dim3(unsigned((sh.rp + 63) / 64 * (sh.cp / 64) * count));
         if (bf16)
             sh.tall ? stack_split_kernel<uint16_t, true><<<grid, dim3(256), 0, s>>>(in)
                     : stack_split_kernel<uint16_t, false><<<grid, dim3(256), 0, s>>>(in);
@@ -525,7 +525,7 @@ hipError_t launch_stack(const muon_stack_t& stack, const StackPlan& plan, float 
     const StackShape sh = stack_shape(stack.rows, stack.cols);
     if (plan.n > 0 && stack_is_whole(sh)) return launch_stack_whole(stack, sh, plan, scale, s);
     // a grid counts below 2^32 work-items: at most 2^22 tiles of 64 x 64 in a group
-    const int64_t per = sh.rp / 64 * (sh.cp / 64);
+    const int64_t per = (sh.rp + 63) / 64 * (sh.cp / 64);
     const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(int64_t(workspace_bytes / stack_matrix_bytes(sh, stack.count)),
                                                                (int64_t(1) << 22) / std::max<int64_t>(per, kStackPartials)));
     for (int64_t at = 0; at < stack.count; at += fit) {

@@ -74,15 +74,19 @@ struct WholeArgs {
     int32_t out_bf16, tall;
 };
 
-// RP: rows, padded (32 or 64).  Waves share the tiles of 16 x 16 of A and B and the columns
-// of X; a column's new values depend on it and B alone, so X is renewed in place.
+// RP: rows, padded (32 or 64).  16 waves: A and B in tiles of 16 x 16, a wave each (of 32 rows
+// there are 4 tiles, and four waves share A's K steps); X in blocks of 16 tiles, which are all read
+// before they are renewed in place.  The matrices are small: what counts is the number
+// of waves that wait for LDS at once (64 x 64: 4 waves 24 us, 16 waves TODO).
+constexpr int kWholeThreads = 1024;
+
 template <int RP, typename T>
-__global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
+__global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeArgs w) {
     extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
-    __shared__ double sums[4];
+    __shared__ double sums[16];
     const InArgs& g = w.in;
-    constexpr int kSquare = RP < 64 ? 256 : RP * 4;  // bytes of a row of A and B
-    constexpr int kF = RP / 16, kSteps = RP / 32;
+    constexpr int kSquare = 256;  // bytes of a row of A and B
+    constexpr int kF = RP / 16, kSteps = RP / 32, kShare = 16 / (kF * kF);
     const int x_row = g.cp * 4;
     unsigned char *x = lds, *a = x + RP * x_row, *b = a + RP * kSquare;
     const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
@@ -94,7 +98,7 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
     const int i0 = wave * at_once + (lane >> wide), j0 = lane & ((1 << wide) - 1);
     double sum = 0.;
 #pragma unroll 4
-    for (int i = i0; i < g.rows; i += 4 * at_once)
+    for (int i = i0; i < g.rows; i += 16 * at_once)
 #pragma unroll 4
         for (int j = j0; j < g.cols; j += 64) {
             const double v = load_one(u + int64_t(i) * g.in_row + j);
@@ -103,116 +107,107 @@ __global__ __launch_bounds__(256) void stack_whole_kernel(const WholeArgs w) {
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) sums[wave] = sum;
     // zeros everywhere, for the padding
-    for (int at = tid * 16; at < RP * (x_row + 2 * kSquare); at += 256 * 16)
+    for (int at = tid * 16; at < RP * (x_row + 2 * kSquare); at += kWholeThreads * 16)
         *reinterpret_cast<u32x4*>(lds + at) = u32x4{0, 0, 0, 0};
     __syncthreads();
-    const double norm = sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
+    double norm = 0.;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) norm += sums[k];
+    norm = sqrt(norm);
     const float inv = inverse_of(norm);
     float top = first_bound(norm);
     const bool small = top < kStackSmallBound;
     int sx = small ? stack_exponent(top, 0) : g.plan.scales[0].sx;
     const float up = power_of_two(sx);
 #pragma unroll 4
-    for (int i = i0; i < g.rows; i += 4 * at_once)
+    for (int i = i0; i < g.rows; i += 16 * at_once)
 #pragma unroll 4
         for (int j = j0; j < g.cols; j += 64) {
             const Pair p = split(load_one(u + int64_t(i) * g.in_row + j) * inv * up);
             const int m = w.tall ? j : i, n = w.tall ? i : j;
-            unsigned char* at = quad_at(x, x_row, m, n & ~3, 0) + (n & 3) * 2;
-            unsigned char* low = quad_at(x, x_row, m, n & ~3, 1) + (n & 3) * 2;
-            *reinterpret_cast<_Float16*>(at) = p.hi;
-            *reinterpret_cast<_Float16*>(low) = p.lo;
+            *reinterpret_cast<_Float16*>(quad_at(x, x_row, m, n & ~3, 0) + (n & 3) * 2) = p.hi;
+            *reinterpret_cast<_Float16*>(quad_at(x, x_row, m, n & ~3, 1) + (n & 3) * 2) = p.lo;
         }
     __syncthreads();
 
     const int k_steps = g.cp / 32;
-    constexpr int kMine = kF * kF / 4;  // tiles of A of a wave: of one row of tiles
-    const int fi = wave * kMine / kF;
+    // this wave's tile of A and B, and its share of A's K steps; its row of tiles of X
+    const int tile = wave % (kF * kF), share = wave / (kF * kF), fi = tile / kF, fj = tile % kF;
+    const int m = fi * 16 + (lane & 15);
+    constexpr int kBlock = 16 * 16 / kF;  // columns of a block of 16 tiles of X
     for (int t = 0; t < g.plan.n; ++t) {
         const StackStep step = g.plan.steps[t];
         const StackScale s = small ? stack_scale(step, top) : g.plan.scales[t];
         // A = X X^T
-        f32x4 acc[kMine];
-        const auto store = [&](unsigned char* to) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int ks = share; ks < k_steps; ks += kShare)
+            acc = product(rows_operand(x, x_row, fj * 16, ks, 0), rows_operand(x, x_row, fj * 16, ks, 1),
+                          rows_operand(x, x_row, fi * 16, ks, 0), rows_operand(x, x_row, fi * 16, ks, 1), acc);
+        if constexpr (kShare > 1) {
+            // the first wave of a tile adds the others' sums in their order
+            f32x4* sums_a = reinterpret_cast<f32x4*>(b + RP * kSquare);
+            if (share > 0) sums_a[(tile * (kShare - 1) + share - 1) * 64 + lane] = acc;
+            __syncthreads();
+            if (share == 0)
 #pragma unroll
-            for (int q = 0; q < kMine; ++q) {
-                const int fj = (wave * kMine + q) % kF;
-                const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
-                put_quad(to, kSquare, fi * 16 + (lane & 15), fj * 16 + 4 * (lane >> 4), v);
-            }
-        };
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) acc[q] = {0.f, 0.f, 0.f, 0.f};
-        for (int ks = 0; ks < k_steps; ++ks) {
-            const f16x8 ph = rows_operand(x, x_row, fi * 16, ks, 0), pl = rows_operand(x, x_row, fi * 16, ks, 1);
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) {
-                const int fj = (wave * kMine + q) % kF;
-                acc[q] = product(rows_operand(x, x_row, fj * 16, ks, 0), rows_operand(x, x_row, fj * 16, ks, 1),
-                                 ph, pl, acc[q]);
-            }
+                for (int k = 0; k < kShare - 1; ++k) acc += sums_a[(tile * (kShare - 1) + k) * 64 + lane];
         }
         const float down_a = power_of_two(s.sa - 2 * sx);
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) acc[q] *= down_a;
-        store(a);
+        const auto put = [&](unsigned char* to) {
+            const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+            put_quad(to, kSquare, m, fj * 16 + 4 * (lane >> 4), v);
+        };
+        acc *= down_a;
+        if (share == 0) put(a);
         __syncthreads();
-        // B = b A + c A A, with this wave's tiles of A still in registers
-        const float down_b = step.c * power_of_two(s.sb - 2 * s.sa), own_b = step.b * power_of_two(s.sb - s.sa);
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) {
-            const int fj = (wave * kMine + q) % kF;
+        // B = b A + c A A, with this wave's tile of A still in registers
+        if (share == 0) {
+            const float down_b = step.c * power_of_two(s.sb - 2 * s.sa), own_b = step.b * power_of_two(s.sb - s.sa);
             f32x4 aa = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks)
                 aa = product(rows_operand(a, kSquare, fj * 16, ks, 0), rows_operand(a, kSquare, fj * 16, ks, 1),
                              rows_operand(a, kSquare, fi * 16, ks, 0), rows_operand(a, kSquare, fi * 16, ks, 1), aa);
-            acc[q] = acc[q] * own_b + aa * down_b;
+            acc = acc * own_b + aa * down_b;
+            put(b);
         }
-        store(b);
         __syncthreads();
-        // X <- a X + B X, 16 columns at a time
+        // X <- a X + B X
         const bool last = t + 1 == g.plan.n;
         const int next = small ? stack_exponent(top, 0) : g.plan.scales[t + 1].sx, to = last ? 0 : next;
         float down_x = power_of_two(to - sx - s.sb), own_x = step.a * power_of_two(to - sx);
         if (last) down_x *= g.scale, own_x *= g.scale;
-        f16x8 bh[kF][kSteps], bl[kF][kSteps];
+        const int xi = wave % kF, xm = xi * 16 + (lane & 15);
+        f16x8 bh[kSteps], bl[kSteps];
 #pragma unroll
-        for (int i = 0; i < kF; ++i)
+        for (int ks = 0; ks < kSteps; ++ks) {
+            bh[ks] = rows_operand(b, kSquare, xi * 16, ks, 0);
+            bl[ks] = rows_operand(b, kSquare, xi * 16, ks, 1);
+        }
+        for (int at = 0; at < g.cp; at += kBlock) {
+            const int col = at + wave / kF * 16, n = col + 4 * (lane >> 4);
+            float v[4];
+            if (col < g.cp) {
+                f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-                bh[i][ks] = rows_operand(b, kSquare, i * 16, ks, 0);
-                bl[i][ks] = rows_operand(b, kSquare, i * 16, ks, 1);
+                for (int ks = 0; ks < kSteps; ++ks)
+                    y = product(turned_operand(x, x_row, col, ks, 0), turned_operand(x, x_row, col, ks, 1), bh[ks],
+                                bl[ks], y);
+                get_quad(x, x_row, xm, n, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = own_x * v[e] + down_x * y[e];
             }
-        for (int cf = wave; cf < g.cp / 16; cf += 4) {
-            f16x8 qh[kSteps], ql[kSteps];
-#pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-                qh[ks] = turned_operand(x, x_row, cf * 16, ks, 0);
-                ql[ks] = turned_operand(x, x_row, cf * 16, ks, 1);
-            }
-            f32x4 y[kF];
-#pragma unroll
-            for (int i = 0; i < kF; ++i) {
-                y[i] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) y[i] = product(qh[ks], ql[ks], bh[i][ks], bl[i][ks], y[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kF; ++i) {
-                const int m = i * 16 + (lane & 15), n = cf * 16 + 4 * (lane >> 4);
-                float v[4];
-                get_quad(x, x_row, m, n, v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = own_x * v[e] + down_x * y[i][e];
-                if (!last)
-                    put_quad(x, x_row, m, n, v);
-                else if (w.out_bf16)
-                    store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, w.tall,
-                                 g.rows, g.cols, m, n, v);
+            if (!last) {
+                __syncthreads();
+                if (col < g.cp) put_quad(x, x_row, xm, n, v);
+            } else if (col < g.cp) {
+                if (w.out_bf16)
+                    store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, w.tall, g.rows,
+                                 g.cols, xm, n, v);
                 else
                     store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, w.tall, g.rows,
-                                 g.cols, m, n, v);
+                                 g.cols, xm, n, v);
             }
         }
         sx = next;
@@ -235,47 +230,48 @@ struct StripArgs {
     float scale;
 };
 
+// Waves in 2 columns of RP / 16: each has one row of 16 x 16 tiles, of the strip 2 of its 4 tiles,
+// of the Gram matrix half.
 template <int RP>
 struct StripGeo {
-    static constexpr int kWaves = RP / 16, kThreads = kWaves * 64;
     static constexpr int kF = RP / 16, kSteps = RP / 32;
-    // tiles of the Gram matrix of a wave: 2 rows by kGn columns; of a strip: 2 by 2
-    static constexpr int kGn = kF * kF / kWaves / 2;
+    static constexpr int kWaves = 2 * kF, kThreads = kWaves * 64;
+    static constexpr int kGn = kF / 2;
     static constexpr int kOp = RP * 256;  // bytes of a strip
     static constexpr int kLoads = kOp / (kThreads * 16);
+    static constexpr int kStages = 3;     // strips in LDS: two on their way
 };
 
 // FIRST: X is only read (the Gram matrix of the first iterate).
 template <int RP, bool FIRST>
 __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(const StripArgs g) {
     using G = StripGeo<RP>;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][G::kOp];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[G::kStages][G::kOp];
     const int matrix = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int strips = g.cp / 64, first = part * g.per, end = min(strips, first + g.per);
     unsigned char* x = reinterpret_cast<unsigned char*>(g.x) + int64_t(matrix) * RP * g.cp * 4;
     const uint32_t lds0 = lds_address(lds[0]);
-    // wave's place: rows of tiles 2 * wr, 2 * wr + 1
-    const int wr = wave % (G::kF / 2), wc = wave / (G::kF / 2);
+    const int wr = wave % G::kF, wc = wave / G::kF;
 
     // a thread's chunks: chunk tid % 16 of rows tid / 16 + p * rows of a pass
     constexpr int kRows = G::kThreads / 16;
     uint32_t off[G::kLoads];
 #pragma unroll
     for (int p = 0; p < G::kLoads; ++p) {
-        const int r = (tid >> 4) + p * kRows;
-        const int c = (tid & 15) ^ turn(r);
+        const int r = (tid >> 4) + p * kRows, c = (tid & 15) ^ turn(r);
         off[p] = (c >> 3) * RP * 128 + r * 128 + (c & 7) * 16;
     }
-    const auto fetch = [&](int strip, int buf) {
+    const auto fetch = [&](int strip, int stage) {
 #pragma unroll
         for (int p = 0; p < G::kLoads; ++p)
-            load_to_lds(x + int64_t(strip) * G::kOp, off[p], lds0 + buf * G::kOp + p * G::kThreads * 16 + wave * 1024);
+            load_to_lds(x + int64_t(strip) * G::kOp, off[p],
+                        lds0 + stage * G::kOp + p * G::kThreads * 16 + wave * 1024);
     };
 
     StackScale s{};
     float down = 0.f, own = 0.f;
-    f16x8 bh[2][G::kSteps], bl[2][G::kSteps];
+    f16x8 bh[G::kSteps], bl[G::kSteps];
     if constexpr (!FIRST) {
         const StackScale* ex = g.scales + int64_t(matrix) * kStackScales;
         s = ex[0];
@@ -284,103 +280,90 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
         if (g.last) down *= g.scale, own *= g.scale;
         const f16x8* b = reinterpret_cast<const f16x8*>(g.b) + int64_t(matrix) * RP * RP / 4;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int ks = 0; ks < G::kSteps; ++ks) {
-                const f16x8* q = b + (((wr * 2 + i) * G::kSteps + ks) * 2) * 64 + lane;
-                bh[i][ks] = q[0], bl[i][ks] = q[64];
-            }
+        for (int ks = 0; ks < G::kSteps; ++ks) {
+            const f16x8* q = b + ((wr * G::kSteps + ks) * 2) * 64 + lane;
+            bh[ks] = q[0], bl[ks] = q[64];
+        }
     }
-    f32x4 gram[2][G::kGn];
+    f32x4 gram[G::kGn];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < G::kGn; ++j) gram[i][j] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < G::kGn; ++j) gram[j] = {0.f, 0.f, 0.f, 0.f};
 
+    // Before a strip is used all loads and stores but the youngest strip's loads are waited for:
+    // those come last, and there are none behind the last strip, where everything is
     fetch(first, 0);
+    if (first + 1 < end) fetch(first + 1, 1);
+    int stage = 0;
     for (int strip = first; strip < end; ++strip) {
-        unsigned char* m = lds[(strip - first) & 1];
-        wait_loads();
+        unsigned char* m = lds[stage];
+        if (strip + 1 < end)
+            wait_loads<G::kLoads>();
+        else
+            wait_loads<0>();
         __syncthreads();
-        if (strip + 1 < end) fetch(strip + 1, (strip + 1 - first) & 1);
+        const int row = wr * 16 + (lane & 15);
+        float v[2][4];
         if constexpr (!FIRST) {
-            f32x4 y[2][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                y[0][j] = y[1][j] = {0.f, 0.f, 0.f, 0.f};
+                f32x4 y = {0.f, 0.f, 0.f, 0.f};
+                const int col = (wc * 2 + j) * 16;
 #pragma unroll
-                for (int ks = 0; ks < G::kSteps; ++ks) {
-                    const f16x8 qh = turned_operand(m, 256, (wc * 2 + j) * 16, ks, 0);
-                    const f16x8 ql = turned_operand(m, 256, (wc * 2 + j) * 16, ks, 1);
+                for (int ks = 0; ks < G::kSteps; ++ks)
+                    y = product(turned_operand(m, 256, col, ks, 0), turned_operand(m, 256, col, ks, 1), bh[ks],
+                                bl[ks], y);
+                get_quad(m, 256, row, col + 4 * (lane >> 4), v[j]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) y[i][j] = product(qh, ql, bh[i][ks], bl[i][ks], y[i][j]);
+                for (int e = 0; e < 4; ++e) v[j][e] = own * v[j][e] + down * y[e];
+                if (g.last) {
+                    if (g.out_bf16)
+                        store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                     g.rows, g.cols, row, strip * 64 + col + 4 * (lane >> 4), v[j]);
+                    else
+                        store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
+                                     g.rows, g.cols, row, strip * 64 + col + 4 * (lane >> 4), v[j]);
                 }
             }
-            float v[2][2][4];
+            if (!g.last) {
+                __syncthreads();  // every wave has read the old strip
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int j = 0; j < 2; ++j) put_quad(m, 256, row, (wc * 2 + j) * 16 + 4 * (lane >> 4), v[j]);
+                __syncthreads();
+                // back to memory as it was read
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = (wr * 2 + i) * 16 + (lane & 15), col = (wc * 2 + j) * 16 + 4 * (lane >> 4);
-                    get_quad(m, 256, row, col, v[i][j]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[i][j][e] = own * v[i][j][e] + down * y[i][j][e];
-                    if (g.last) {
-                        if (g.out_bf16)
-                            store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
-                                         g.rows, g.cols, row, strip * 64 + col, v[i][j]);
-                        else
-                            store_result(static_cast<float*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
-                                         g.rows, g.cols, row, strip * 64 + col, v[i][j]);
-                    }
-                }
-            if (g.last) continue;
-            __syncthreads();  // every wave has read the old strip
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    put_quad(m, 256, (wr * 2 + i) * 16 + (lane & 15), (wc * 2 + j) * 16 + 4 * (lane >> 4), v[i][j]);
-            __syncthreads();
-            // back to memory as it was read
-#pragma unroll
-            for (int p = 0; p < G::kLoads; ++p)
-                *reinterpret_cast<u32x4*>(x + int64_t(strip) * G::kOp + off[p]) =
-                    *reinterpret_cast<const u32x4*>(m + p * G::kThreads * 16 + tid * 16);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f16x8 ph[2], pl[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ph[i] = rows_operand(m, 256, (wr * 2 + i) * 16, ks, 0);
-                pl[i] = rows_operand(m, 256, (wr * 2 + i) * 16, ks, 1);
-            }
-#pragma unroll
-            for (int j = 0; j < G::kGn; ++j) {
-                const f16x8 qh = rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 0);
-                const f16x8 ql = rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 1);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) gram[i][j] = product(qh, ql, ph[i], pl[i], gram[i][j]);
+                for (int p = 0; p < G::kLoads; ++p)
+                    *reinterpret_cast<u32x4*>(x + int64_t(strip) * G::kOp + off[p]) =
+                        *reinterpret_cast<const u32x4*>(m + p * G::kThreads * 16 + tid * 16);
             }
         }
+        if (strip + 2 < end) fetch(strip + 2, stage == 0 ? 2 : stage - 1);
+        if (FIRST || !g.last) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const f16x8 ph = rows_operand(m, 256, wr * 16, ks, 0), pl = rows_operand(m, 256, wr * 16, ks, 1);
+#pragma unroll
+                for (int j = 0; j < G::kGn; ++j)
+                    gram[j] = product(rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 0),
+                                      rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 1), ph, pl, gram[j]);
+            }
+        }
+        stage = stage == 2 ? 0 : stage + 1;
     }
     if (!FIRST && g.last) return;
     f32x4* to = reinterpret_cast<f32x4*>(g.gram) + (int64_t(matrix) * g.parts + part) * (RP * RP / 4);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < G::kGn; ++j)
-            to[((wr * 2 + i) * G::kF + wc * G::kGn + j) * 64 + lane] = gram[i][j];
+    for (int j = 0; j < G::kGn; ++j) to[(wr * G::kF + wc * G::kGn + j) * 64 + lane] = gram[j];
 }
 
-// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.  16 waves,
-// each with tiles of one row of tiles.
-constexpr int kPolyThreads = 1024;
+// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.  Up to 16
+// waves, each with tiles of one row of tiles.
+template <int RP>
+constexpr int kPolyThreads = RP == 32 ? 256 : 1024;
 
 template <int RP>
-__global__ __launch_bounds__(kPolyThreads) void stack_poly_kernel(const StripArgs g) {
-    constexpr int kRow = RP * 4, kF = RP / 16, kSteps = RP / 32, kMine = kF * kF / 16;
+__global__ __launch_bounds__(kPolyThreads<RP>) void stack_poly_kernel(const StripArgs g) {
+    constexpr int kRow = RP == 32 ? 256 : RP * 4;
+    constexpr int kF = RP / 16, kSteps = RP / 32, kMine = kF * kF / (kPolyThreads<RP> / 64);
     __shared__ __attribute__((aligned(1024))) unsigned char a[RP * kRow];
     const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), fi = wave * kMine / kF, fj = wave * kMine % kF;
@@ -446,7 +429,7 @@ hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, cons
     in.cp = int32_t(sh.cp), in.plan = plan, in.scale = scale;
     w.tall = sh.tall, w.out_bf16 = st.out_dtype == MUON_DTYPE_BF16;
     const size_t lds = stack_whole_lds(sh);
-    const dim3 grid = dim3(unsigned(st.count)), block = dim3(256);
+    const dim3 grid = dim3(unsigned(st.count)), block = dim3(kWholeThreads);
     const auto run = [&](auto kernel) {
         if (lds > 64 * 1024) {
             // has to be told
@@ -478,7 +461,7 @@ hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, cons
         g.scales = scales + t, g.step = plan.steps[t], g.last = t + 1 == plan.n;
         {
             LaunchTimer timer("stack_poly", s);
-            stack_poly_kernel<RP><<<dim3(unsigned(count)), dim3(kPolyThreads), 0, s>>>(g);
+            stack_poly_kernel<RP><<<dim3(unsigned(count)), dim3(kPolyThreads<RP>), 0, s>>>(g);
         }
         if ((e = hipGetLastError()) != hipSuccess) return e;
         LaunchTimer timer("stack_strip", s);
@@ -500,10 +483,12 @@ hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int
     g.tall = sh.tall, g.out_bf16 = st.out_dtype == MUON_DTYPE_BF16, g.scale = scale;
     // about a workgroup a CU for the whole stack (not for `count`, so that groups make the same
     // sums), and no more partial Gram matrices than the second iterate's place holds
-    const int64_t strips = sh.cp / 64, want = std::max<int64_t>(1, 256 / st.count);
+    const int64_t strips = sh.cp / 64, resident = sh.rp == 128 ? 256 : 768;
+    const int64_t want = std::max<int64_t>(1, resident / st.count);
     const int64_t parts = std::min({strips, want, sh.cp / sh.rp, int64_t(32)});
     g.per = int32_t((strips + parts - 1) / parts);
     g.parts = int32_t((strips + g.per - 1) / g.per);
+    if (sh.rp == 32) return run_strips<32>(g, count, scales, plan, s);
     return sh.rp == 64 ? run_strips<64>(g, count, scales, plan, s)
                        : run_strips<128>(g, count, scales, plan, s);
 }

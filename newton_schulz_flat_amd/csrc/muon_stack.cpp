@@ -12,7 +12,7 @@ StackShape stack_shape(int64_t rows, int64_t cols) {
     StackShape s;
     s.tall = rows > cols;
     s.r = std::min(rows, cols), s.c = std::max(rows, cols);
-    s.rp = (s.r + kStackPad - 1) / kStackPad * kStackPad;
+    s.rp = s.r <= 32 ? 32 : (s.r + kStackPad - 1) / kStackPad * kStackPad;
     s.cp = (s.c + kStackPad - 1) / kStackPad * kStackPad;
     return s;
 }

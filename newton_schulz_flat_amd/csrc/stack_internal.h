@@ -77,7 +77,7 @@ struct StackShape {
     bool tall;
 };
 
-// Sides are padded to this many elements; one more padded block is never read.
+// Sides are padded to this many elements, a shorter one of up to 32 to 32.
 constexpr int64_t kStackPad = 64;
 // Partial sums of squares of one matrix, and the room for them.
 constexpr int64_t kStackPartials = 1024;
@@ -101,8 +101,8 @@ constexpr float kStackSmallBound = 0.5f;
 // LDS of a matrix that one workgroup takes as a whole: X, A and B (whose rows are 256 bytes at
 // least).
 inline size_t stack_whole_lds(const StackShape& s) {
-    const int64_t rp = s.r <= 32 ? 32 : 64;
-    return s.r > 64 ? ~size_t(0) : size_t(rp * s.cp * 4 + 2 * rp * 256);
+    // (of 32 rows, A's tiles are summed in four shares: three places of 4 KB)
+    return s.r > 64 ? ~size_t(0) : size_t(s.rp * s.cp * 4 + 2 * s.rp * 256 + (s.rp == 32 ? 3 * 4096 : 0));
 }
 constexpr size_t kStackWholeLds = 156 * 1024;
 bool stack_is_whole(const StackShape& s);
