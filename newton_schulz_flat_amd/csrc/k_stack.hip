@@ -502,7 +502,8 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
     if (sh.r <= 128)
-        return launch_stack_strips(st, sh, count, in.out, x[0], x[1], b, scales, plan, scale, s);
+        return launch_stack_strips(st, sh, count, in.out, x[0], x[1],
+                                   reinterpret_cast<unsigned char*>(b) + a_bytes, b, scales, plan, scale, s);
     for (int t = 0; t < n; ++t) {
         ProductArgs g{};
         g.x = x[t & 1], g.x_next = x[(t + 1) & 1], g.a = a, g.b = b;

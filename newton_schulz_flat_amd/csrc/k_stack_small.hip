@@ -17,48 +17,67 @@ namespace muon {
 
 namespace {
 
-// Where a matrix of pairs lies in LDS: rows of `row_bytes` (a multiple of 256), chunk c (16 bytes)
-// of row r at chunk c ^ turn(r).  turn is a bijection of r mod 16, so 16 rows' reads of one chunk
-// meet every bank, and it takes the rows of one transposing read (0-3 and 8-11 mod 16, or
-// these + 4) to chunks of different 32 bytes.
-__device__ __forceinline__ int turn(int r) {
-    return (r & 3) << 1 | (r >> 3 & 1) << 3 | (r >> 2 & 1);
-}
+// Where a matrix of pairs lies in LDS: rows of row_bytes (a multiple of 256), chunk c (16 bytes) of
+// row r at chunk c ^ turn(r).  A 16-byte read of 16 rows at two neighbouring chunks is served in
+// groups of rows 0-3 and 12-15 of one with 4-11 of the other: turn leaves out bit 2, which the chunk
+// makes up for.  A transposing read takes rows 0-3 and 8-11 mod 16, or these + 4, to 32 bytes each, which
+// turn, always even, leaves together and sends to all 256.  (A turn of all four bits: half of the
+// reads' cycles were conflicts.)
+__device__ __forceinline__ int turn(int r) { return (r & 3) << 1 | (r >> 3 & 1) << 3; }
+
+// A lane's part of the addresses in a matrix with rows of row_bytes.  What a call adds to it (K
+// step, half, place of the tile) it adds as constants: those below 256 bytes by exclusive or, like
+// turn itself.  Worked out anew for every operand, addresses took more time than the products.
+struct Place {
+    int row_bytes, rows, turned, quad;
+    __device__ __forceinline__ explicit Place(int bytes) : row_bytes(bytes) {
+        const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4, k = g * 8 + (l >> 2);
+        rows = l * bytes + ((g ^ turn(l)) << 4);
+        turned = k * bytes + ((((l & 3) >> 1) ^ turn(k & 15)) << 4) + (l & 1) * 8;
+        quad = l * bytes + (((g >> 1) ^ turn(l)) << 4) + (g & 1) * 8;
+    }
+};
 
 // Operand of 16 rows from row0 on, K step ks (32 columns), half 0 (high) or 1.
-__device__ __forceinline__ f16x8 rows_operand(const unsigned char* m, int row_bytes, int row0, int ks, int half) {
-    const int lane = threadIdx.x & 63, r = row0 + (lane & 15), c = ks * 8 + half * 4 + (lane >> 4);
-    return *reinterpret_cast<const f16x8*>(m + r * row_bytes + ((c ^ turn(r)) << 4));
+__device__ __forceinline__ f16x8 rows_operand(const unsigned char* m, const Place& p, int row0, int ks, int half) {
+    return *reinterpret_cast<const f16x8*>(m + (p.rows ^ ((ks & 1) * 128 + half * 64)) + (ks >> 1) * 256 +
+                                           row0 * p.row_bytes);
 }
-// Operand of 16 columns from col0 on, K step ks (32 rows).
-__device__ __forceinline__ f16x8 turned_operand(const unsigned char* m, int row_bytes, int col0, int ks, int half) {
-    const int lane = threadIdx.x & 63, l = lane & 15, k = ks * 32 + (lane >> 4) * 8 + (l >> 2);
-    const int c = (col0 >> 5) * 8 + half * 4 + ((col0 >> 4) & 1) * 2 + ((l & 3) >> 1);
-    const uint2 lo = read_turned(m + k * row_bytes + ((c ^ turn(k)) << 4) + (l & 1) * 8);
-    const uint2 hi = read_turned(m + (k + 4) * row_bytes + ((c ^ turn(k + 4)) << 4) + (l & 1) * 8);
+// Operand of 16 columns from 16 * tile on, K step ks (32 rows).
+__device__ __forceinline__ f16x8 turned_operand(const unsigned char* m, const Place& p, int tile, int ks, int half) {
+    const int low = ((tile >> 1) & 1) * 128 + half * 64 + (tile & 1) * 32;
+    const unsigned char* at = m + (tile >> 2) * 256 + ks * 32 * p.row_bytes;
+    // the second read's rows are 4 further on, where turn is the same
+    const uint2 lo = read_turned(at + (p.turned ^ low));
+    const uint2 hi = read_turned(at + (p.turned ^ low) + 4 * p.row_bytes);
     return __builtin_bit_cast(f16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
 }
-// Address of the high halves of elements (i, j..j+3), j a multiple of 4; the low ones' chunk
-// differs in bit 2, so does its place.
-__device__ __forceinline__ unsigned char* quad_at(unsigned char* m, int row_bytes, int i, int j, int half) {
-    const int c = (j >> 5) * 8 + half * 4 + ((j & 31) >> 3);
-    return m + i * row_bytes + ((c ^ turn(i)) << 4) + (j & 4) * 2;
+// This lane's four neighbouring elements of the 16 x 16 tile (ti, tj): row lane % 16, columns
+// from 4 (lane / 16) on.
+__device__ __forceinline__ unsigned char* quad_at(unsigned char* m, const Place& p, int ti, int tj, int half) {
+    return m + (p.quad ^ (((tj >> 1) & 1) * 128 + half * 64 + (tj & 1) * 32)) + (tj >> 2) * 256 +
+           ti * 16 * p.row_bytes;
 }
-__device__ __forceinline__ void put_quad(unsigned char* m, int row_bytes, int i, int j, const float v[4]) {
+__device__ __forceinline__ void put_quad(unsigned char* m, const Place& p, int ti, int tj, const float v[4]) {
     f16x4 hi, lo;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const Pair p = split(v[t]);
-        hi[t] = p.hi, lo[t] = p.lo;
+        const Pair s = split(v[t]);
+        hi[t] = s.hi, lo[t] = s.lo;
     }
-    *reinterpret_cast<f16x4*>(quad_at(m, row_bytes, i, j, 0)) = hi;
-    *reinterpret_cast<f16x4*>(quad_at(m, row_bytes, i, j, 1)) = lo;
+    *reinterpret_cast<f16x4*>(quad_at(m, p, ti, tj, 0)) = hi;
+    *reinterpret_cast<f16x4*>(quad_at(m, p, ti, tj, 1)) = lo;
 }
-__device__ __forceinline__ void get_quad(unsigned char* m, int row_bytes, int i, int j, float v[4]) {
-    const f16x4 hi = *reinterpret_cast<const f16x4*>(quad_at(m, row_bytes, i, j, 0));
-    const f16x4 lo = *reinterpret_cast<const f16x4*>(quad_at(m, row_bytes, i, j, 1));
+__device__ __forceinline__ void get_quad(unsigned char* m, const Place& p, int ti, int tj, float v[4]) {
+    const f16x4 hi = *reinterpret_cast<const f16x4*>(quad_at(m, p, ti, tj, 0));
+    const f16x4 lo = *reinterpret_cast<const f16x4*>(quad_at(m, p, ti, tj, 1));
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = float(hi[t]) + float(lo[t]);
+}
+// One element (i, j) of either half.
+__device__ __forceinline__ _Float16* element_at(unsigned char* m, int row_bytes, int i, int j, int half) {
+    const int c = (j >> 5) * 8 + half * 4 + ((j & 31) >> 3);
+    return reinterpret_cast<_Float16*>(m + i * row_bytes + ((c ^ turn(i)) << 4)) + (j & 7);
 }
 // acc += the three products of the halves.
 __device__ __forceinline__ f32x4 product(f16x8 qh, f16x8 ql, f16x8 ph, f16x8 pl, f32x4 acc) {
@@ -125,15 +144,15 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
         for (int j = j0; j < g.cols; j += 64) {
             const Pair p = split(load_one(u + int64_t(i) * g.in_row + j) * inv * up);
             const int m = w.tall ? j : i, n = w.tall ? i : j;
-            *reinterpret_cast<_Float16*>(quad_at(x, x_row, m, n & ~3, 0) + (n & 3) * 2) = p.hi;
-            *reinterpret_cast<_Float16*>(quad_at(x, x_row, m, n & ~3, 1) + (n & 3) * 2) = p.lo;
+            *element_at(x, x_row, m, n, 0) = p.hi;
+            *element_at(x, x_row, m, n, 1) = p.lo;
         }
     __syncthreads();
 
     const int k_steps = g.cp / 32;
     // this wave's tile of A and B, and its share of A's K steps; its row of tiles of X
     const int tile = wave % (kF * kF), share = wave / (kF * kF), fi = tile / kF, fj = tile % kF;
-    const int m = fi * 16 + (lane & 15);
+    const Place in_x(x_row), in_square(kSquare);
     constexpr int kBlock = 16 * 16 / kF;  // columns of a block of 16 tiles of X
     for (int t = 0; t < g.plan.n; ++t) {
         const StackStep step = g.plan.steps[t];
@@ -142,8 +161,8 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
         for (int ks = share; ks < k_steps; ks += kShare)
-            acc = product(rows_operand(x, x_row, fj * 16, ks, 0), rows_operand(x, x_row, fj * 16, ks, 1),
-                          rows_operand(x, x_row, fi * 16, ks, 0), rows_operand(x, x_row, fi * 16, ks, 1), acc);
+            acc = product(rows_operand(x, in_x, fj * 16, ks, 0), rows_operand(x, in_x, fj * 16, ks, 1),
+                          rows_operand(x, in_x, fi * 16, ks, 0), rows_operand(x, in_x, fi * 16, ks, 1), acc);
         if constexpr (kShare > 1) {
             // the first wave of a tile adds the others' sums in their order
             f32x4* sums_a = reinterpret_cast<f32x4*>(b + RP * kSquare);
@@ -156,7 +175,7 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
         const float down_a = power_of_two(s.sa - 2 * sx);
         const auto put = [&](unsigned char* to) {
             const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-            put_quad(to, kSquare, m, fj * 16 + 4 * (lane >> 4), v);
+            put_quad(to, in_square, fi, fj, v);
         };
         acc *= down_a;
         if (share == 0) put(a);
@@ -167,8 +186,8 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
             f32x4 aa = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks)
-                aa = product(rows_operand(a, kSquare, fj * 16, ks, 0), rows_operand(a, kSquare, fj * 16, ks, 1),
-                             rows_operand(a, kSquare, fi * 16, ks, 0), rows_operand(a, kSquare, fi * 16, ks, 1), aa);
+                aa = product(rows_operand(a, in_square, fj * 16, ks, 0), rows_operand(a, in_square, fj * 16, ks, 1),
+                             rows_operand(a, in_square, fi * 16, ks, 0), rows_operand(a, in_square, fi * 16, ks, 1), aa);
             acc = acc * own_b + aa * down_b;
             put(b);
         }
@@ -182,25 +201,25 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
         f16x8 bh[kSteps], bl[kSteps];
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
-            bh[ks] = rows_operand(b, kSquare, xi * 16, ks, 0);
-            bl[ks] = rows_operand(b, kSquare, xi * 16, ks, 1);
+            bh[ks] = rows_operand(b, in_square, xi * 16, ks, 0);
+            bl[ks] = rows_operand(b, in_square, xi * 16, ks, 1);
         }
         for (int at = 0; at < g.cp; at += kBlock) {
-            const int col = at + wave / kF * 16, n = col + 4 * (lane >> 4);
+            const int xj = at / 16 + wave / kF, col = xj * 16, n = col + 4 * (lane >> 4);
             float v[4];
             if (col < g.cp) {
                 f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks)
-                    y = product(turned_operand(x, x_row, col, ks, 0), turned_operand(x, x_row, col, ks, 1), bh[ks],
+                    y = product(turned_operand(x, in_x, xj, ks, 0), turned_operand(x, in_x, xj, ks, 1), bh[ks],
                                 bl[ks], y);
-                get_quad(x, x_row, xm, n, v);
+                get_quad(x, in_x, xi, xj, v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = own_x * v[e] + down_x * y[e];
             }
             if (!last) {
                 __syncthreads();
-                if (col < g.cp) put_quad(x, x_row, xm, n, v);
+                if (col < g.cp) put_quad(x, in_x, xi, xj, v);
             } else if (col < g.cp) {
                 if (w.out_bf16)
                     store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, w.tall, g.rows,
@@ -219,7 +238,8 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
 
 struct StripArgs {
     _Float16* x;    // [matrix][cp / 32][rp][64]
-    float* gram;    // [matrix][part][tile of 16 x 16][lane][4]
+    const float* gram;  // [matrix][part][tile of 16 x 16][lane][4]
+    float* gram_next;   // of the next iterate
     _Float16* b;    // [matrix][row tile][K step][half][lane][8]
     const StackScale* scales;  // this step's, of matrix 0
     StackStep step;
@@ -238,14 +258,72 @@ struct StripGeo {
     static constexpr int kWaves = 2 * kF, kThreads = kWaves * 64;
     static constexpr int kGn = kF / 2;
     static constexpr int kOp = RP * 256;  // bytes of a strip
-    static constexpr int kLoads = kOp / (kThreads * 16);
-    static constexpr int kStages = 3;     // strips in LDS: two on their way
+    // Half of the waves load strips, the other half stores them: one counter covers a wave's
+    // loads and stores, and waiting for the next strip must not wait for the last one's stores.
+    static constexpr int kMovers = kThreads / 2;
+    static constexpr int kLoads = kOp / (kMovers * 16);
+    static constexpr int kStages = 3;  // strips in LDS: two on their way
 };
 
-// FIRST: X is only read (the Gram matrix of the first iterate).
-template <int RP, bool FIRST>
+// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order: WAVES waves, each
+// with tiles of one row of tiles, A in LDS at a.  Returns this wave's tiles of B, stored 2^sb.
+template <int RP, int WAVES>
+struct Poly {
+    static constexpr int kRow = RP == 32 ? 256 : RP * 4, kBytes = RP * kRow;
+    static constexpr int kF = RP / 16, kSteps = RP / 32, kMine = kF * kF / WAVES;
+    static_assert(kMine >= 1 && kF % kMine == 0, "tiles of one row");
+    f32x4 b[kMine];
+    int fi, fj;
+
+    __device__ __forceinline__ void run(const StripArgs& g, int matrix, const StackScale& s, unsigned char* a) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        fi = wave * kMine / kF, fj = wave * kMine % kF;
+        const f32x4* from = reinterpret_cast<const f32x4*>(g.gram) + int64_t(matrix) * g.parts * (RP * RP / 4) +
+                            wave * kMine * 64 + lane;
+        f32x4 acc[kMine];
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) acc[q] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int p = 0; p < g.parts; ++p)
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) acc[q] += from[p * (RP * RP / 4) + q * 64];
+        const Place in_a(kRow);
+        const float down_a = power_of_two(s.sa - 2 * s.sx);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            acc[q] *= down_a;
+            put(a, in_a, q, acc[q]);
+        }
+        __syncthreads();
+        const float down = g.step.c * power_of_two(s.sb - 2 * s.sa), own = g.step.b * power_of_two(s.sb - s.sa);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) b[q] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+            const f16x8 ph = rows_operand(a, in_a, fi * 16, ks, 0), pl = rows_operand(a, in_a, fi * 16, ks, 1);
+#pragma unroll
+            for (int q = 0; q < kMine; ++q)
+                b[q] = product(rows_operand(a, in_a, (fj + q) * 16, ks, 0),
+                               rows_operand(a, in_a, (fj + q) * 16, ks, 1), ph, pl, b[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) b[q] = acc[q] * own + b[q] * down;
+    }
+    __device__ __forceinline__ void put(unsigned char* m, const Place& place, int q, const f32x4& t) const {
+        const float v[4] = {t.x, t.y, t.z, t.w};
+        put_quad(m, place, fi, fj + q, v);
+    }
+};
+
+// MODE kGram: X is only read (the Gram matrix of the first iterate).  kStep: B comes from
+// stack_poly_kernel.  kWholeStep: the workgroup makes B of the partial Gram matrices itself, which
+// saves a launch of 5 to 7 us where they are few.
+enum StripMode { kGram, kStep, kWholeStep };
+
+template <int RP, int MODE>
 __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(const StripArgs g) {
     using G = StripGeo<RP>;
+    constexpr bool FIRST = MODE == kGram;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[G::kStages][G::kOp];
     const int matrix = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -253,20 +331,24 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
     unsigned char* x = reinterpret_cast<unsigned char*>(g.x) + int64_t(matrix) * RP * g.cp * 4;
     const uint32_t lds0 = lds_address(lds[0]);
     const int wr = wave % G::kF, wc = wave / G::kF;
+    const Place in_strip(256);
 
-    // a thread's chunks: chunk tid % 16 of rows tid / 16 + p * rows of a pass
-    constexpr int kRows = G::kThreads / 16;
+    // a mover's chunks: chunk tid % 16 of rows tid / 16 + p * rows of a pass
+    constexpr int kRows = G::kMovers / 16;
+    const bool loads = wave < G::kWaves / 2;
+    const int mover = loads ? tid : tid - G::kMovers;
     uint32_t off[G::kLoads];
 #pragma unroll
     for (int p = 0; p < G::kLoads; ++p) {
-        const int r = (tid >> 4) + p * kRows, c = (tid & 15) ^ turn(r);
+        const int r = (mover >> 4) + p * kRows, c = (mover & 15) ^ turn(r);
         off[p] = (c >> 3) * RP * 128 + r * 128 + (c & 7) * 16;
     }
     const auto fetch = [&](int strip, int stage) {
+        if (!loads) return;
 #pragma unroll
         for (int p = 0; p < G::kLoads; ++p)
             load_to_lds(x + int64_t(strip) * G::kOp, off[p],
-                        lds0 + stage * G::kOp + p * G::kThreads * 16 + wave * 1024);
+                        lds0 + stage * G::kOp + p * G::kMovers * 16 + wave * 1024);
     };
 
     StackScale s{};
@@ -278,6 +360,8 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
         const int to = g.last ? 0 : ex[1].sx;
         down = power_of_two(to - s.sx - s.sb), own = g.step.a * power_of_two(to - s.sx);
         if (g.last) down *= g.scale, own *= g.scale;
+    }
+    if constexpr (MODE == kStep) {
         const f16x8* b = reinterpret_cast<const f16x8*>(g.b) + int64_t(matrix) * RP * RP / 4;
 #pragma unroll
         for (int ks = 0; ks < G::kSteps; ++ks) {
@@ -289,32 +373,55 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
 #pragma unroll
     for (int j = 0; j < G::kGn; ++j) gram[j] = {0.f, 0.f, 0.f, 0.f};
 
-    // Before a strip is used all loads and stores but the youngest strip's loads are waited for:
-    // those come last, and there are none behind the last strip, where everything is
     fetch(first, 0);
+    if constexpr (MODE == kWholeStep) {
+        // A and then B where the later strips will lie
+        using P = Poly<RP, G::kWaves>;
+        static_assert(P::kBytes <= 2 * G::kOp, "two strips");
+        P poly;
+        poly.run(g, matrix, s, lds[1]);
+        __syncthreads();
+        const Place in_b(P::kRow);
+#pragma unroll
+        for (int q = 0; q < P::kMine; ++q) poly.put(lds[1], in_b, q, poly.b[q]);
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < G::kSteps; ++ks) {
+            bh[ks] = rows_operand(lds[1], in_b, wr * 16, ks, 0);
+            bl[ks] = rows_operand(lds[1], in_b, wr * 16, ks, 1);
+        }
+        __syncthreads();
+    }
     if (first + 1 < end) fetch(first + 1, 1);
     int stage = 0;
     for (int strip = first; strip < end; ++strip) {
         unsigned char* m = lds[stage];
-        if (strip + 1 < end)
-            wait_loads<G::kLoads>();
-        else
-            wait_loads<0>();
+        if (loads) {
+            // all but the next strip's loads (and, of the results' stores, none: loads return in
+            // their order, so what is left are these)
+            if (strip + 1 < end)
+                wait_loads<G::kLoads>();
+            else
+                wait_loads<0>();
+        }
         __syncthreads();
         const int row = wr * 16 + (lane & 15);
         float v[2][4];
         if constexpr (!FIRST) {
+            f32x4 y[2];
+            y[0] = y[1] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < G::kSteps; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    y[j] = product(turned_operand(m, in_strip, wc * 2 + j, ks, 0),
+                                   turned_operand(m, in_strip, wc * 2 + j, ks, 1), bh[ks], bl[ks], y[j]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                f32x4 y = {0.f, 0.f, 0.f, 0.f};
                 const int col = (wc * 2 + j) * 16;
+                get_quad(m, in_strip, wr, wc * 2 + j, v[j]);
 #pragma unroll
-                for (int ks = 0; ks < G::kSteps; ++ks)
-                    y = product(turned_operand(m, 256, col, ks, 0), turned_operand(m, 256, col, ks, 1), bh[ks],
-                                bl[ks], y);
-                get_quad(m, 256, row, col + 4 * (lane >> 4), v[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = own * v[j][e] + down * y[e];
+                for (int e = 0; e < 4; ++e) v[j][e] = own * v[j][e] + down * y[j][e];
                 if (g.last) {
                     if (g.out_bf16)
                         store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
@@ -327,88 +434,58 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
             if (!g.last) {
                 __syncthreads();  // every wave has read the old strip
 #pragma unroll
-                for (int j = 0; j < 2; ++j) put_quad(m, 256, row, (wc * 2 + j) * 16 + 4 * (lane >> 4), v[j]);
+                for (int j = 0; j < 2; ++j) put_quad(m, in_strip, wr, wc * 2 + j, v[j]);
                 __syncthreads();
                 // back to memory as it was read
+                if (!loads)
 #pragma unroll
-                for (int p = 0; p < G::kLoads; ++p)
-                    *reinterpret_cast<u32x4*>(x + int64_t(strip) * G::kOp + off[p]) =
-                        *reinterpret_cast<const u32x4*>(m + p * G::kThreads * 16 + tid * 16);
+                    for (int p = 0; p < G::kLoads; ++p)
+                        *reinterpret_cast<u32x4*>(x + int64_t(strip) * G::kOp + off[p]) =
+                            *reinterpret_cast<const u32x4*>(m + (p * G::kMovers + mover) * 16);
             }
         }
         if (strip + 2 < end) fetch(strip + 2, stage == 0 ? 2 : stage - 1);
         if (FIRST || !g.last) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const f16x8 ph = rows_operand(m, 256, wr * 16, ks, 0), pl = rows_operand(m, 256, wr * 16, ks, 1);
+                const f16x8 ph = rows_operand(m, in_strip, wr * 16, ks, 0), pl = rows_operand(m, in_strip, wr * 16, ks, 1);
 #pragma unroll
                 for (int j = 0; j < G::kGn; ++j)
-                    gram[j] = product(rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 0),
-                                      rows_operand(m, 256, (wc * G::kGn + j) * 16, ks, 1), ph, pl, gram[j]);
+                    gram[j] = product(rows_operand(m, in_strip, (wc * G::kGn + j) * 16, ks, 0),
+                                      rows_operand(m, in_strip, (wc * G::kGn + j) * 16, ks, 1), ph, pl, gram[j]);
             }
         }
         stage = stage == 2 ? 0 : stage + 1;
     }
     if (!FIRST && g.last) return;
-    f32x4* to = reinterpret_cast<f32x4*>(g.gram) + (int64_t(matrix) * g.parts + part) * (RP * RP / 4);
+    f32x4* to = reinterpret_cast<f32x4*>(g.gram_next) + (int64_t(matrix) * g.parts + part) * (RP * RP / 4);
 #pragma unroll
     for (int j = 0; j < G::kGn; ++j) to[(wr * G::kF + wc * G::kGn + j) * 64 + lane] = gram[j];
 }
 
-// B = b A + c A A of a matrix, A the sum of its partial Gram matrices, in their order.  Up to 16
-// waves, each with tiles of one row of tiles.
+// B of a matrix, in the order in which stack_strip_kernel's lanes take it.
 template <int RP>
 constexpr int kPolyThreads = RP == 32 ? 256 : 1024;
 
 template <int RP>
 __global__ __launch_bounds__(kPolyThreads<RP>) void stack_poly_kernel(const StripArgs g) {
-    constexpr int kRow = RP == 32 ? 256 : RP * 4;
-    constexpr int kF = RP / 16, kSteps = RP / 32, kMine = kF * kF / (kPolyThreads<RP> / 64);
-    __shared__ __attribute__((aligned(1024))) unsigned char a[RP * kRow];
-    const int matrix = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), fi = wave * kMine / kF, fj = wave * kMine % kF;
-    const StackScale s = g.scales[int64_t(matrix) * kStackScales];
-    const f32x4* from = reinterpret_cast<const f32x4*>(g.gram) + int64_t(matrix) * g.parts * (RP * RP / 4) +
-                        wave * kMine * 64 + lane;
-    f32x4 acc[kMine];
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) acc[q] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int p = 0; p < g.parts; ++p)
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) acc[q] += from[p * (RP * RP / 4) + q * 64];
-    const float down_a = power_of_two(s.sa - 2 * s.sx);
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-        acc[q] *= down_a;
-        const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
-        put_quad(a, kRow, fi * 16 + (lane & 15), (fj + q) * 16 + 4 * (lane >> 4), v);
-    }
-    __syncthreads();
-    const float down = g.step.c * power_of_two(s.sb - 2 * s.sa), own = g.step.b * power_of_two(s.sb - s.sa);
+    using P = Poly<RP, kPolyThreads<RP> / 64>;
+    __shared__ __attribute__((aligned(1024))) unsigned char a[P::kBytes];
+    const int matrix = blockIdx.x, lane = threadIdx.x & 63;
+    P poly;
+    poly.run(g, matrix, g.scales[int64_t(matrix) * kStackScales], a);
     unsigned char* b = reinterpret_cast<unsigned char*>(g.b) + int64_t(matrix) * RP * RP * 4;
-    f32x4 aa[kMine];
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) aa[q] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-        const f16x8 ph = rows_operand(a, kRow, fi * 16, ks, 0), pl = rows_operand(a, kRow, fi * 16, ks, 1);
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-            aa[q] = product(rows_operand(a, kRow, (fj + q) * 16, ks, 0), rows_operand(a, kRow, (fj + q) * 16, ks, 1),
-                            ph, pl, aa[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-        // element (m, n..n+3) in the order in which stack_strip's lanes take it
-        const int m = lane & 15, n = (fj + q) * 16 + 4 * (lane >> 4);
+    for (int q = 0; q < P::kMine; ++q) {
+        const int m = lane & 15, n = (poly.fj + q) * 16 + 4 * (lane >> 4);  // elements (m, n..n+3)
         f16x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const Pair p = split(own * acc[q][e] + down * aa[q][e]);
+            const Pair p = split(poly.b[q][e]);
             hi[e] = p.hi, lo[e] = p.lo;
         }
-        unsigned char* at = b + (((fi * kSteps + (n >> 5)) * 2) * 64 + ((n & 31) >> 3) * 16 + m) * 16 + (n & 4) * 2;
+        unsigned char* at = b +
+                            (((poly.fi * P::kSteps + (n >> 5)) * 2) * 64 + ((n & 31) >> 3) * 16 + m) * 16 + (n & 4) * 2;
         *reinterpret_cast<f16x4*>(at) = hi;
         *reinterpret_cast<f16x4*>(at + 1024) = lo;
     }
@@ -450,22 +527,29 @@ hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, cons
 namespace {
 
 template <int RP>
-hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, const StackPlan& plan, hipStream_t s) {
+hipError_t run_strips(StripArgs g, float* const (&gram)[2], int64_t count, const StackScale* scales,
+                      const StackPlan& plan, hipStream_t s) {
     const dim3 grid = dim3(unsigned(g.parts * count)), block = dim3(StripGeo<RP>::kThreads);
+    const bool whole = g.parts <= 2;
     {
         LaunchTimer timer("stack_gram", s);
-        stack_strip_kernel<RP, true><<<grid, block, 0, s>>>(g);
+        g.gram_next = gram[0];
+        stack_strip_kernel<RP, kGram><<<grid, block, 0, s>>>(g);
     }
     hipError_t e = hipGetLastError();
     for (int t = 0; t < plan.n && e == hipSuccess; ++t) {
         g.scales = scales + t, g.step = plan.steps[t], g.last = t + 1 == plan.n;
-        {
+        g.gram = gram[t & 1], g.gram_next = gram[(t + 1) & 1];
+        if (!whole) {
             LaunchTimer timer("stack_poly", s);
             stack_poly_kernel<RP><<<dim3(unsigned(count)), dim3(kPolyThreads<RP>), 0, s>>>(g);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        if ((e = hipGetLastError()) != hipSuccess) return e;
         LaunchTimer timer("stack_strip", s);
-        stack_strip_kernel<RP, false><<<grid, block, 0, s>>>(g);
+        if (whole)
+            stack_strip_kernel<RP, kWholeStep><<<grid, block, 0, s>>>(g);
+        else
+            stack_strip_kernel<RP, kStep><<<grid, block, 0, s>>>(g);
         e = hipGetLastError();
     }
     return e;
@@ -474,10 +558,11 @@ hipError_t run_strips(StripArgs g, int64_t count, const StackScale* scales, cons
 }  // namespace
 
 hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int64_t count, void* out, void* x,
-                               void* gram, void* b, const StackScale* scales, const StackPlan& plan,
-                               float scale, hipStream_t s) {
+                               void* gram0, void* gram1, void* b, const StackScale* scales,
+                               const StackPlan& plan, float scale, hipStream_t s) {
     StripArgs g{};
-    g.x = static_cast<_Float16*>(x), g.gram = static_cast<float*>(gram), g.b = static_cast<_Float16*>(b);
+    g.x = static_cast<_Float16*>(x), g.b = static_cast<_Float16*>(b);
+    float* const gram[2] = {static_cast<float*>(gram0), static_cast<float*>(gram1)};
     g.out = out, g.out_stride = st.out_stride, g.out_row = st.out_row;
     g.cp = int32_t(sh.cp), g.rows = int32_t(st.rows), g.cols = int32_t(st.cols);
     g.tall = sh.tall, g.out_bf16 = st.out_dtype == MUON_DTYPE_BF16, g.scale = scale;
@@ -488,9 +573,9 @@ hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int
     const int64_t parts = std::min({strips, want, sh.cp / sh.rp, int64_t(32)});
     g.per = int32_t((strips + parts - 1) / parts);
     g.parts = int32_t((strips + g.per - 1) / g.per);
-    if (sh.rp == 32) return run_strips<32>(g, count, scales, plan, s);
-    return sh.rp == 64 ? run_strips<64>(g, count, scales, plan, s)
-                       : run_strips<128>(g, count, scales, plan, s);
+    if (sh.rp == 32) return run_strips<32>(g, gram, count, scales, plan, s);
+    return sh.rp == 64 ? run_strips<64>(g, gram, count, scales, plan, s)
+                       : run_strips<128>(g, gram, count, scales, plan, s);
 }
 
 }  // namespace muon

@@ -55,11 +55,11 @@ StackTiling stack_tiling(int stage, const StackShape& s, int64_t count) {
 // Two iterates, A and B, 4 bytes an element, the partial sums of squares, the exponents, and the
 // sums of tiles that several workgroups share.
 size_t stack_matrix_bytes(const StackShape& s, int64_t count) {
-    size_t shared = 0;
+    size_t shared = size_t(s.rp * s.cp) * 4;  // r <= 128: Gram matrices
     if (s.r > 128)
         for (int stage : {kStageA, kStageB, kStageX}) {
             const StackTiling t = stack_tiling(stage, s, count);
-            shared = std::max(shared, size_t(t.slots()) * t.slot_bytes());
+            shared = std::max(stage == kStageA ? 0 : shared, size_t(t.slots()) * t.slot_bytes());
         }
     return size_t(2 * s.rp * s.cp + 2 * s.rp * s.rp) * 4 + size_t(stack_part_slots(s.r, s.c)) * sizeof(double) +
            kStackScales * sizeof(StackScale) + shared;
