@@ -449,10 +449,10 @@ typedef struct muon_fp8 {
 /* A matrix into 8 bits: out, out_t or both (either may be NULL) receive x
  * (rows x cols of dtype, row_stride elements between rows) and its transpose, each
  * in its own blocks.  For each block
- *   s = fl(max(largest magnitude, 2^-100) / L)     L = 448 or 57344
- *   code = fl(x * fl(1 / s)) rounded to nearest even
+ *   m = max(largest magnitude, 2^-100),  s = fl(m / L)     L = 448 or 57344
+ *   code = fl(x L / m) rounded to nearest even, fl one float32 rounding
  * A block that holds a NaN gets the scale NaN, one that holds an infinity an
- * infinite one.  x, codes and scales must not overlap: neither each other nor,
+ * infinite one; its codes say nothing.  x, codes and scales must not overlap: neither each other nor,
  * where there are gaps between rows, each other's span from the first element to
  * the last.  Elements in the gaps stay as they are. */
 int muon_fp8_cast(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,

@@ -1,19 +1,23 @@
 // Casts into 8-bit floats with a scale for each 1 x 128 or 128 x 128 block, of a
 // matrix and of its transpose in one pass.
 //
-//   s = fl(max(largest magnitude of the block, 2^-100) / L),  code = rne8(fl(x fl(1 / s)))
+//   m = max(largest magnitude of the block, 2^-100),  s = fl(m / L),  code = rne8(fl(x L / m))
 //
-// with L the format's largest number.  |x| fl(1 / s) exceeds L by less than 4
-// float32 roundings, far below the middle between L and the next step, so no code
-// leaves the format's range and nothing has to be clamped.  Magnitudes are
-// compared as bit patterns, in which a NaN is above infinity: a block that
-// holds one gets the scale NaN.
+// with L the format's largest number.  L / m is held in two float32 (high and rest), so that
+// x L / m is off by one float32 rounding only: with fl(x fl(1 / s)), three roundings, more than twice as
+// many elements near the middle between two codes get the farther one.  |x| L / m exceeds
+// L by less than a float32 rounding, far below the middle between L and the next step, so no
+// code leaves the format's range and nothing has to be clamped.  Magnitudes are compared as bit
+// patterns, in which a NaN is above infinity: a block that holds one gets the scale NaN.
 //
 // A workgroup takes a 128 x 128 tile, a thread an 8 x 8 block of it, held in
 // registers: 16 neighbouring lanes read one row's 128 elements.  Row blocks
 // reduce over these 16 lanes (DPP), column blocks over the 16 threads of a column
-// group (lanes, then LDS).  The transposed codes go through LDS so that each
-// row of the transpose leaves as 128 contiguous bytes.  It is an HBM stream.
+// group (lanes, then LDS).  Each block's divisions are made by one lane (of a row's 16, the
+// row's; of the workgroup, the column's) and handed round.  The transposed codes go through LDS
+// so that each row of the transpose leaves as 128 contiguous bytes.  It is an HBM stream.
+#include <type_traits>
+
 #include "fp8_internal.h"
 #include "k_common.h"
 
@@ -79,10 +83,23 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
     return x;
 }
 
+// What a block's values are multiplied by: high + rest = L / m.
+struct Factor {
+    float high, rest;
+    __device__ __forceinline__ float of(float x) const { return __builtin_fmaf(x, high, x * rest); }
+};
 template <bool E5M2>
-__device__ __forceinline__ float scale_of(uint32_t largest) {
-    const uint32_t floor_bits = 27u << 23;  // 2^-100
-    return __uint_as_float(max(largest, floor_bits)) / (E5M2 ? 57344.f : 448.f);
+__device__ __forceinline__ Factor factor_of(uint32_t largest, float* scale) {
+    const float m = __uint_as_float(max(largest, 27u << 23));  // 2^-100
+    const float top = E5M2 ? 57344.f : 448.f;
+    *scale = m / top;
+    const float high = top / m;
+    return {high, __builtin_fmaf(-high, m, top) / m};
+}
+// Lane n's value in all 16 lanes of its DPP row.
+template <int N>
+__device__ __forceinline__ float row_value(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xF, 0xF, true));
 }
 
 template <bool E5M2>
@@ -110,9 +127,19 @@ __device__ __forceinline__ void store8(uint8_t* p, int left, uint2 w) {
     }
 }
 
+// f(0), ..., f(7) with the number as a constant.
+template <typename F>
+__device__ __forceinline__ void for_eight(F&& f) {
+    f(std::integral_constant<int, 0>{}), f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{}), f(std::integral_constant<int, 3>{});
+    f(std::integral_constant<int, 4>{}), f(std::integral_constant<int, 5>{});
+    f(std::integral_constant<int, 6>{}), f(std::integral_constant<int, 7>{});
+}
+
 template <typename T, bool SQUARE, bool E5M2>
 __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
     __shared__ uint32_t col_max[4][kFp8Block];
+    __shared__ Factor factors[kFp8Block];
     __shared__ uint2 turned[kFp8Block * 16];
     const int tr = blockIdx.x / a.col_tiles, tc = blockIdx.x % a.col_tiles;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;  // 8-column and 8-row group
@@ -130,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
             for (int j = 0; j < 8; ++j) v[p][j] = 0.f;
     }
 
-    float s_all = 0.f, r_all = 0.f;
+    Factor all = {0.f, 0.f};
     if constexpr (SQUARE) {
         uint32_t top = 0;
 #pragma unroll
@@ -140,45 +167,45 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
         top = row_max(top);
         if (cg == 0) col_max[0][rg] = top;
         __syncthreads();
-        top = row_max(col_max[0][cg]);
-        s_all = scale_of<E5M2>(top);
-        r_all = 1.f / s_all;
+        float scale;
+        all = factor_of<E5M2>(row_max(col_max[0][cg]), &scale);
         if (threadIdx.x == 0) {
             if (a.out.codes != nullptr)
-                a.out.scales[tr * a.out.scale_row + tc * a.out.scale_col] = s_all;
+                a.out.scales[tr * a.out.scale_row + tc * a.out.scale_col] = scale;
             if (a.out_t.codes != nullptr)
-                a.out_t.scales[tc * a.out_t.scale_row + tr * a.out_t.scale_col] = s_all;
+                a.out_t.scales[tc * a.out_t.scale_row + tr * a.out_t.scale_col] = scale;
         }
     }
 
     if (a.out.codes != nullptr) {
-        uint8_t* q = a.out.codes + int64_t(r0) * a.out.row_stride + c0;
+        float scale = 0.f;
+        Factor mine = {0.f, 0.f};  // of row cg % 8 of this thread's 8
+        if constexpr (!SQUARE) {
+            uint32_t my_top = 0;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            float s = s_all, r = r_all;
-            if constexpr (!SQUARE) {
+            for (int p = 0; p < 8; ++p) {
                 uint32_t top = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[p][j]));
-                s = scale_of<E5M2>(row_max(top));
-                r = 1.f / s;
+                top = row_max(top);
+                if ((cg & 7) == p) my_top = top;
             }
-            const uint2 w = {encode4<E5M2>(v[p][0] * r, v[p][1] * r, v[p][2] * r, v[p][3] * r),
-                             encode4<E5M2>(v[p][4] * r, v[p][5] * r, v[p][6] * r, v[p][7] * r)};
-            if (p < rows_left) {
-                store8(q + p * a.out.row_stride, cols_left, w);
-                if (!SQUARE && cg == 0)
-                    a.out.scales[(r0 + p) * a.out.scale_row + tc * a.out.scale_col] = s;
-            }
+            mine = factor_of<E5M2>(my_top, &scale);
+            if (cg < rows_left && cg < 8)
+                a.out.scales[(r0 + cg) * a.out.scale_row + tc * a.out.scale_col] = scale;
         }
+        uint8_t* q = a.out.codes + int64_t(r0) * a.out.row_stride + c0;
+        for_eight([&](auto index) {
+            constexpr int p = decltype(index)::value;
+            const Factor f = SQUARE ? all : Factor{row_value<p>(mine.high), row_value<p>(mine.rest)};
+            const uint2 w = {encode4<E5M2>(f.of(v[p][0]), f.of(v[p][1]), f.of(v[p][2]), f.of(v[p][3])),
+                             encode4<E5M2>(f.of(v[p][4]), f.of(v[p][5]), f.of(v[p][6]), f.of(v[p][7]))};
+            if (p < rows_left) store8(q + p * a.out.row_stride, cols_left, w);
+        });
     }
 
     if (a.out_t.codes == nullptr) return;
-    float rc[8];
-    if constexpr (SQUARE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) rc[j] = r_all;
-    } else {
+    if constexpr (!SQUARE) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint32_t top = 0;
@@ -189,24 +216,23 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
             if ((threadIdx.x & 63) < 16) col_max[threadIdx.x >> 6][cg * 8 + j] = top;
         }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = cg * 8 + j;
-            const float s = scale_of<E5M2>(
-                max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c])));
-            rc[j] = 1.f / s;
-            if (rg == 0 && j < cols_left)
-                a.out_t.scales[(c0 + j) * a.out_t.scale_row + tr * a.out_t.scale_col] = s;
+        if (threadIdx.x < kFp8Block) {
+            const int c = threadIdx.x, col = tc * kFp8Block + c;
+            float scale;
+            factors[c] = factor_of<E5M2>(
+                max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c])), &scale);
+            if (col < a.cols) a.out_t.scales[col * a.out_t.scale_row + tr * a.out_t.scale_col] = scale;
         }
+        __syncthreads();
     }
     // 8-byte chunk (column c, rows of group g) lies at c * 16 + (g ^ (c / 8)): lanes that write
     // together meet 16 different chunks
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float r = rc[j];
+        const Factor f = SQUARE ? all : factors[cg * 8 + j];
         turned[(cg * 8 + j) * 16 + (rg ^ cg)] = {
-            encode4<E5M2>(v[0][j] * r, v[1][j] * r, v[2][j] * r, v[3][j] * r),
-            encode4<E5M2>(v[4][j] * r, v[5][j] * r, v[6][j] * r, v[7][j] * r)};
+            encode4<E5M2>(f.of(v[0][j]), f.of(v[1][j]), f.of(v[2][j]), f.of(v[3][j])),
+            encode4<E5M2>(f.of(v[4][j]), f.of(v[5][j]), f.of(v[6][j]), f.of(v[7][j]))};
     }
     __syncthreads();
     const int left = a.rows - tr * kFp8Block - cg * 8;

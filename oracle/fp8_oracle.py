@@ -42,6 +42,17 @@ def blocks(n):
     return -(-n // BLOCK)
 
 
+def times_ratio(x, m, top):
+    """fl(x top / m) as the cast makes it: top / m in two float32 parts, one fused
+    multiplication and addition.  Extended precision (64 digits) holds every product of two float32
+    and the sums here exactly."""
+    x, m, top = np.asarray(x, np.float32), np.float32(m), np.float32(top)
+    wide = np.longdouble
+    high = top / m
+    rest = np.float32(wide(top) - wide(high) * wide(m)) / m
+    return (wide(1) * x * wide(high) + (x * rest).astype(wide)).astype(np.float32)
+
+
 def cast(x, fmt, square):
     """(codes, scales) of a float32 matrix, in float32 arithmetic, each operation rounded."""
     x = np.asarray(x, np.float32)
@@ -53,10 +64,10 @@ def cast(x, fmt, square):
     for i in range(scales.shape[0]):
         for j in range(scales.shape[1]):
             part = x[i * high:(i + 1) * high, j * BLOCK:(j + 1) * BLOCK]
-            s = np.float32(max(np.max(np.abs(part)), FLOOR)) / top
-            scales[i, j] = s
+            m = np.float32(max(np.max(np.abs(part)), FLOOR))
+            scales[i, j] = m / top
             codes[i * high:(i + 1) * high, j * BLOCK:(j + 1) * BLOCK] = encode(
-                part * (np.float32(1) / s), fmt)
+                times_ratio(part, m, top), fmt)
     return codes, scales
 
 
