@@ -767,16 +767,15 @@ def muon_adamw(params, grads, exp_avg, exp_avg_sq, ranges, groups, clip=None, mo
             len(arr), groups.data_ptr(), groups.shape[0], clip_ptr)
 
 
-def _fp8_formats():
-    """Formats of the 8-bit types, worked out once."""
-    global _FP8
-    if _FP8 is None:
+#: Formats of the 8-bit types; filled at the first call that needs it (torch is loaded then).
+_FP8: dict = {}
+
+
+def _fp8_formats() -> dict:
+    if not _FP8:
         import torch
-        _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+        _FP8.update({torch.float8_e4m3fn: 0, torch.float8_e5m2: 1})
     return _FP8
-
-
-_FP8 = None
 
 
 def fp8_scales(rows: int, cols: int, block: str, device):
@@ -792,7 +791,13 @@ def fp8_scales(rows: int, cols: int, block: str, device):
 
 
 def _matrix(t, name, dtypes):
-    """Refuses what is not a GPU matrix with neighbouring elements in a row."""
+    """Shape and row stride of a GPU matrix with neighbouring elements in a row; refuses others."""
+    try:
+        (rows, cols), (row, col) = t.shape, t.stride()
+        if t.is_cuda and t.dtype in dtypes and (col == 1 or cols <= 1):
+            return rows, cols, row
+    except (AttributeError, ValueError):
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -802,8 +807,7 @@ def _matrix(t, name, dtypes):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, it has {t.dim()}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"the elements of a row of {name} must be neighbours")
+    raise ValueError(f"the elements of a row of {name} must be neighbours")
 
 
 def _fp8(codes, scales, name, scales_name) -> Fp8C:
@@ -811,23 +815,31 @@ def _fp8(codes, scales, name, scales_name) -> Fp8C:
     matrix of one row is the same either way."""
     import torch
     formats = _fp8_formats()
-    _matrix(codes, name, formats)
-    rows, cols = codes.shape
-    if (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or not scales.is_cuda
-            or scales.dim() != 2):
+    rows, cols, row = _matrix(codes, name, formats)
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is torch.float32 and scales.is_cuda
+            and scales.dim() == 2):
         raise TypeError(f"{scales_name} must be a float32 GPU matrix")
-    if scales.device != codes.device:
+    if scales.get_device() != codes.get_device():
         raise ValueError(f"{scales_name} is on {scales.device}, {name} on {codes.device}")
-    across = -(-cols // 128)
-    if tuple(scales.shape) == (rows, across):
-        high = 1
-    elif tuple(scales.shape) == (-(-rows // 128), across):
-        high = 128
+    high, across = scales.shape
+    if across == -(-cols // 128) and high == rows:
+        block_rows = 1
+    elif across == -(-cols // 128) and high == -(-rows // 128):
+        block_rows = 128
     else:
         raise ValueError(f"{scales_name} has shape {tuple(scales.shape)}, {name} {tuple(codes.shape)}: "
                          "expected one scale for each 1 x 128 or 128 x 128 block")
-    return Fp8C(codes.data_ptr(), scales.data_ptr(), rows, cols, codes.stride(0), scales.stride(0),
-                scales.stride(1), formats[codes.dtype], high)
+    down, right = scales.stride()
+    return Fp8C(codes.data_ptr(), scales.data_ptr(), rows, cols, row, down, right,
+                formats[codes.dtype], block_rows)
+
+
+def _same_device(first, first_name, **others) -> None:
+    """``_together`` for tensors that are known to be on GPUs."""
+    at = first.get_device()
+    for t in others.values():
+        if t is not None and t.get_device() != at:
+            _together(first, first_name, **others)
 
 
 def muon_fp8_cast(x, codes=None, scales=None, codes_t=None, scales_t=None):
@@ -836,23 +848,23 @@ def muon_fp8_cast(x, codes=None, scales=None, codes_t=None, scales_t=None):
     ``codes_t`` with ``scales_t``, or both.  The scales' shape says the blocks: see
     ``fp8_scales``."""
     import torch
-    _matrix(x, "x", (torch.float32, torch.bfloat16))
+    bf16 = torch.bfloat16
+    rows, cols, row = _matrix(x, "x", (torch.float32, bf16))
     if codes is None and codes_t is None:
         raise ValueError("codes or codes_t must be given")
     if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
         raise ValueError("codes and scales belong together, and so do codes_t and scales_t")
-    _together(x, "x", codes=codes, codes_t=codes_t)
     out = None if codes is None else _fp8(codes, scales, "codes", "scales")
     out_t = None if codes_t is None else _fp8(codes_t, scales_t, "codes_t", "scales_t")
+    _same_device(x, "x", codes=codes, codes_t=codes_t)
     if out is not None and out_t is not None and out.block_rows != out_t.block_rows:
         # one row or one column: its 1 x 128 and 128 x 128 blocks are the same
-        if x.shape[0] <= 1:
+        if rows <= 1:
             out.block_rows = out_t.block_rows
-        elif x.shape[1] <= 1:
+        elif cols <= 1:
             out_t.block_rows = out.block_rows
-    dt = MUON_DTYPE_BF16 if x.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    _launch(x.get_device(), load_library().muon_fp8_cast, x.data_ptr(), dt, x.shape[0], x.shape[1],
-            x.stride(0), None if out is None else ctypes.byref(out),
+    _launch(x.get_device(), load_library().muon_fp8_cast, x.data_ptr(),
+            MUON_DTYPE_BF16 if x.dtype is bf16 else MUON_DTYPE_F32, rows, cols, row, None if out is None else ctypes.byref(out),
             None if out_t is None else ctypes.byref(out_t))
 
 
@@ -884,21 +896,23 @@ def _call_workspace(need: int, device):
     return ws
 
 
-def _launch_with_workspace(workspace, need: int, device, call, *args) -> None:
-    """``call(*args, workspace, bytes, stream)`` with the given workspace, or, where one is
-    needed, the stream's default one under its lock."""
+def _launch_with_workspace(workspace, need: int, beside, call, *args) -> None:
+    """``call(*args, workspace, bytes, stream)`` on the device of ``beside`` with the given
+    workspace, or, where one is needed, the stream's default one under its lock."""
     import torch
+    index = beside.get_device()
     if workspace is not None:
         _require(workspace, "workspace", (torch.uint8,))
-        if workspace.device != device:
-            raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
-        _launch(device.index, call, *args, workspace.data_ptr(), workspace.numel())
+        if workspace.get_device() != index:
+            raise ValueError(f"workspace is on {workspace.device}, the tensors on {beside.device}")
+        _launch(index, call, *args, workspace.data_ptr(), workspace.numel())
     elif need == 0:
-        _launch(device.index, call, *args, None, 0)
+        _launch(index, call, *args, None, 0)
     else:
+        device = beside.device
         with _stream_lock(device):
             ws = _call_workspace(need, device)
-            _launch(device.index, call, *args, ws.data_ptr(), ws.numel())
+            _launch(index, call, *args, ws.data_ptr(), ws.numel())
 
 
 def muon_fp8_matmul(a, a_scales, b, b_scales, out, accumulate: bool = False, workspace=None):
@@ -908,17 +922,17 @@ def muon_fp8_matmul(a, a_scales, b, b_scales, out, accumulate: bool = False, wor
     ``workspace``: a uint8 GPU tensor of ``muon_fp8_workspace_bytes`` (default: a cached
     one per device and stream, where one is needed; give one under graph capture)."""
     import torch
+    bf16 = torch.bfloat16
     left, right = _fp8(a, a_scales, "a", "a_scales"), _fp8(b, b_scales, "b", "b_scales")
-    _matrix(out, "out", (torch.float32, torch.bfloat16))
-    _together(a, "a", b=b, out=out)
-    m, n, k = left.rows, right.rows, left.cols
-    if tuple(out.shape) != (m, n):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(m, n)}")
-    dt = MUON_DTYPE_BF16 if out.dtype == torch.bfloat16 else MUON_DTYPE_F32
-    need = 0 if workspace is not None else muon_fp8_workspace_bytes(m, n, k)
-    _launch_with_workspace(workspace, need, a.device, load_library().muon_fp8_matmul,
-                           ctypes.byref(left), ctypes.byref(right), out.data_ptr(), dt, out.stride(0),
-                           int(bool(accumulate)))
+    m, n, row = _matrix(out, "out", (torch.float32, bf16))
+    _same_device(a, "a", b=b, out=out)
+    if m != left.rows or n != right.rows:
+        raise ValueError(f"out has shape {(m, n)}, expected {(left.rows, right.rows)}")
+    need = 0 if workspace is not None else muon_fp8_workspace_bytes(m, n, left.cols)
+    _launch_with_workspace(workspace, need, a, load_library().muon_fp8_matmul, ctypes.byref(left),
+                           ctypes.byref(right), out.data_ptr(),
+                           MUON_DTYPE_BF16 if out.dtype is bf16 else MUON_DTYPE_F32, row,
+                           1 if accumulate else 0)
 
 
 #: Coefficients of ``muon_orthogonalize_stack`` where none are given: those of ``muon_step``.
@@ -981,7 +995,7 @@ def muon_orthogonalize_stack(x, out, coefficients=None, scale=None, workspace=No
     if scale is None:
         scale = max(1.0, stack.rows / max(1, stack.cols)) ** 0.5
     need = 0 if workspace is not None else muon_stack_workspace_bytes(x)
-    _launch_with_workspace(workspace, need, x.device, load_library().muon_orthogonalize_stack,
+    _launch_with_workspace(workspace, need, x, load_library().muon_orthogonalize_stack,
                            ctypes.byref(stack), flat, len(steps), scale)
 
 
