@@ -107,17 +107,21 @@ struct Wide {
     }
 };
 
-// One 16 x 16 product over a block of 128.
-template <int FA, int FB, bool EXACT>
-__device__ __forceinline__ f32x4 block_product(const Wide<FA, EXACT>& a, const Wide<FB, EXACT>& b) {
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+// N 16 x 16 products over a block of 128.
+template <int N, int FA, int FB, bool EXACT>
+__device__ __forceinline__ void block_products(const Wide<FA, EXACT>* a, const Wide<FB, EXACT>& b, f32x4* sum) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) sum[q] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (EXACT) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[t], b.v[t], sum, 0, 0, 0);
-        return sum;
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                sum[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q].v[t], b.v[t], sum[q], 0, 0, 0);
     } else {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, sum, FA, FB, 0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            sum[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[q].v, b.v, sum[q], FA, FB, 0, 0, 0, 0);
     }
 }
 
@@ -340,10 +344,11 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
         else
             put(buf);
         __syncthreads();
-        if (kb + 1 < last) fetch(kb + 1, buf ^ 1);
         Wide<FB, EXACT> fb[G::kNj];
 #pragma unroll
         for (int j = 0; j < G::kNj; ++j) fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
+        // (behind these reads, not before them: 1 to 3% on every shape)
+        if (kb + 1 < last) fetch(kb + 1, buf ^ 1);
         const float sb1 = scales[buf][TILE + wn];
 #pragma unroll
         for (int i = 0; i < G::kMi; ++i) {
@@ -354,13 +359,22 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
             // with widened codes 44 spilled registers and twice the time
             int at = TILE + wn + 4 * (lane >> 4);
             if constexpr (!SQUARE && EXACT) asm volatile("" : "+v"(at));
+            // two tiles at once: of widened codes an inner sum is a chain of four instructions (846
+            // against 819 us, 8192 x 14336 over 4096; with scales of single rows there are no
+            // registers left for it)
+            constexpr int kAtOnce = EXACT && !SQUARE ? 1 : 2;
 #pragma unroll
-            for (int j = 0; j < G::kNj; ++j) {
-                const f32x4 sum = block_product(fb[j], fa);
-                if constexpr (SQUARE)
-                    acc[i][j] += sum * (sb1 * sa);
-                else
-                    acc[i][j] += sum * (*reinterpret_cast<const f32x4*>(&scales[buf][at + 16 * j]) * sa);
+            for (int j = 0; j < G::kNj; j += kAtOnce) {
+                f32x4 sum[kAtOnce];
+                block_products<kAtOnce>(fb + j, fa, sum);
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    if constexpr (SQUARE)
+                        acc[i][j + q] += sum[q] * (sb1 * sa);
+                    else
+                        acc[i][j + q] +=
+                            sum[q] * (*reinterpret_cast<const f32x4*>(&scales[buf][at + 16 * (j + q)]) * sa);
+                }
             }
         }
     }
@@ -423,7 +437,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp8_few_kernel(const ProductAr
             Wide<FB, EXACT> wb;
             Wide<FA, EXACT> wa;
             wb.set(fb[u]), wa.set(fa[u]);
-            acc += block_product(wb, wa) * scale[u];
+            f32x4 sum;
+            block_products<1>(&wb, wa, &sum);
+            acc += sum * scale[u];
         }
     }
     sums[wave][lane] = acc;
@@ -483,7 +499,7 @@ float estimate(int64_t m, int64_t n, int64_t nk, int tile, int64_t tiles, int64_
     const float full = std::floor(load / most), rest = load - full * most;
     float t = 2.5f + per * full * (once + more * most);
     if (rest > 0.f) t += per * (tile == 256 ? more : once + more * std::max(rest, 0.4f));
-    if (splits > 1) t += 2.5f + float(splits * m) * float(n) * 1e-6f;
+    if (splits > 1) t += 5.f + float(splits * m) * float(n) * 1e-6f;
     return t;
 }
 

@@ -343,7 +343,6 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void sta
         for (int ks = k0; ks < k1; ++ks) {
             wait_loads<(G::kStages - 2) * 2 * G::kLoads>();
             __syncthreads();
-            if (G::kStages > 2 || ks + 1 < k1) fetch(ahead);
             const unsigned char* p_lds = lds + stage * 2 * G::kOp;
             const unsigned char* q_lds = p_lds + G::kOp;
             f16x8 qh[G::kNj], ql[G::kNj];
@@ -357,6 +356,7 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void sta
                     ql[j] = rows_fragment(q_lds, wn + 16 * j, 1);
                 }
             }
+            if (G::kStages > 2 || ks + 1 < k1) fetch(ahead);
 #pragma unroll
             for (int i = 0; i < G::kMi; ++i) {
                 const f16x8 ph = rows_fragment(p_lds, wm + 16 * i, 0);
