@@ -177,7 +177,10 @@ struct Geo {
     static constexpr int kMi = kWm / 16, kNj = kWn / 16;
     static constexpr int kOp = TILE * kFp8Block;          // bytes of one operand's block
     static constexpr int kLoads = kOp / (kThreads * 16);  // 16-byte loads of a thread
-    static constexpr int kMinWaves = TILE == 64 ? 4 : 2;  // waves a SIMD has registers for
+    // Direct loads go as many blocks ahead as LDS has stages (less one), loads through registers as
+    // many as there are sets of them: a 64-tile's block is too short to cover a load.
+    static constexpr int kStages = TILE == 64 ? 4 : 2, kSets = TILE == 64 ? 2 : 1;
+    static constexpr int kScales = TILE == 64 ? kThreads : 2 * TILE;  // one of a thread
 };
 
 // 16 bytes to LDS at lds + 16 * lane from base + offset, or 4 bytes at lds + 4 * lane from p,
@@ -203,7 +206,11 @@ __device__ __forceinline__ void load4_to_lds(const void* p, uint32_t lds) {
                  : "v"(p), "s"(lds)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits until at most N loads are on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -224,19 +231,18 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& ti
     ti = band * 4 + rest % high, tj = rest / high;
 }
 
-// One TILE x TILE tile of out over a range of blocks of k.  Blocks are double-buffered in
-// LDS; row r's 16-byte chunk c lies at chunk c ^ (r / 2 mod 8), so that the fragment reads
+// One TILE x TILE tile of out over a range of blocks of k.  Row r's 16-byte chunk c lies at chunk c ^ (r / 2 mod 8), so that the fragment reads
 // of 16 rows meet every bank.  DIRECT (rows of codes that start at multiples of 16
 // bytes and hold a multiple of 16): loads go from memory to LDS directly; else through
 // registers, by bytes at the end of a row.  Rows behind the last one read the last.
 // SQUARE: b's blocks are 128 x 128, and a wave's columns (64 or fewer, within 128) share one
 // scale.
 template <int TILE, bool DIRECT, int FA, int FB, bool EXACT, bool SQUARE>
-__global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8_tile_kernel(
-    const ProductArgs g) {
+__global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const ProductArgs g) {
     using G = Geo<TILE>;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[2][2 * G::kOp];
-    __shared__ __attribute__((aligned(16))) float scales[2][2 * TILE];
+    constexpr int kStages = DIRECT ? G::kStages : 2;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages][2 * G::kOp];
+    __shared__ __attribute__((aligned(16))) float scales[kStages][G::kScales];
     const int tiles = g.tiles_m * g.tiles_n;
     const int split = blockIdx.x / tiles;
     int ti, tj;
@@ -258,21 +264,21 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
     const auto a_row = [&](int p) { return min(lr + p * kRows, g.a.rows - 1 - m0); };
     const auto b_row = [&](int p) { return min(lr + p * kRows, g.b.rows - 1 - n0); };
 
-    // the scales of a block: a's by the first TILE threads of 2 TILE, b's by the others
-    static_assert(2 * TILE <= G::kThreads || TILE == 256, "a scale a thread");
-    const bool scaling = tid < 2 * TILE;
+    // the scales of a block: a's by the first TILE threads of 2 TILE, b's by the others (of a
+    // 64-tile's 256 threads two waves load them once more, so that every wave has as many loads)
     const float* ps;
     int64_t ps_step;
     {
-        const Operand& o = tid < TILE ? g.a : g.b;
-        const int r = min((tid < TILE ? m0 : n0) + (tid & (TILE - 1)), o.rows - 1);
-        ps = o.scales + int64_t(r >> o.shift) * o.scale_row + int64_t(first) * o.scale_col;
+        const int t = tid & (2 * TILE - 1);
+        const Operand& o = t < TILE ? g.a : g.b;
+        const int r = min((t < TILE ? m0 : n0) + (t & (TILE - 1)), o.rows - 1);
+        ps = o.scales + int64_t(r >> o.shift) * o.scale_row;
         ps_step = o.scale_col;
     }
 
     uint32_t a_off[G::kLoads], b_off[G::kLoads];
-    i32x4 ra[G::kLoads], rb[G::kLoads];
-    float rs = 0.f;
+    i32x4 ra[G::kSets][G::kLoads], rb[G::kSets][G::kLoads];
+    float rs[G::kSets];
     if constexpr (DIRECT) {
 #pragma unroll
         for (int p = 0; p < G::kLoads; ++p) {
@@ -281,11 +287,11 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
         }
     }
     const uint32_t lds0 = lds_address(lds), scales0 = lds_address(scales);
-    // DIRECT: starts the loads of block kb into a buffer; else: into registers
-    auto fetch = [&](int kb, int buf) {
+    // starts the loads of block kb: DIRECT into a stage, else into a set of registers
+    auto fetch = [&](int kb, int to_stage, auto set) {
         const int at = kb * kFp8Block;
         if constexpr (DIRECT) {
-            const uint32_t to = lds0 + buf * 2 * G::kOp + wave * 1024;
+            const uint32_t to = lds0 + to_stage * 2 * G::kOp + wave * 1024;
             if (at + kFp8Block <= g.k) {
 #pragma unroll
                 for (int p = 0; p < G::kLoads; ++p) {
@@ -302,26 +308,27 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
                                   to + G::kOp + p * G::kThreads * 16);
                 }
             }
-            if (scaling) load4_to_lds(ps, scales0 + buf * 2 * TILE * 4 + wave * 256);
+            load4_to_lds(ps + kb * ps_step, scales0 + to_stage * G::kScales * 4 + wave * 256);
         } else {
+            constexpr int kSet = decltype(set)::value;
 #pragma unroll
             for (int p = 0; p < G::kLoads; ++p) {
-                ra[p] = load_chunk(a_base + a_row(p) * g.a.row_stride, at + chunk * 16, g.k);
-                rb[p] = load_chunk(b_base + b_row(p) * g.b.row_stride, at + chunk * 16, g.k);
+                ra[kSet][p] = load_chunk(a_base + a_row(p) * g.a.row_stride, at + chunk * 16, g.k);
+                rb[kSet][p] = load_chunk(b_base + b_row(p) * g.b.row_stride, at + chunk * 16, g.k);
             }
-            if (scaling) rs = *ps;
+            rs[kSet] = ps[kb * ps_step];
         }
-        ps += ps_step;
     };
-    auto put = [&](int buf) {
+    auto put = [&](int to_stage, auto set) {
         if constexpr (!DIRECT) {
+            constexpr int kSet = decltype(set)::value;
 #pragma unroll
             for (int p = 0; p < G::kLoads; ++p) {
                 const int at = (lr + p * kRows) * kFp8Block + ((chunk ^ x) << 4);
-                *reinterpret_cast<i32x4*>(&lds[buf][at]) = ra[p];
-                *reinterpret_cast<i32x4*>(&lds[buf][G::kOp + at]) = rb[p];
+                *reinterpret_cast<i32x4*>(&lds[to_stage][at]) = ra[kSet][p];
+                *reinterpret_cast<i32x4*>(&lds[to_stage][G::kOp + at]) = rb[kSet][p];
             }
-            if (scaling) scales[buf][tid] = rs;
+            scales[to_stage][tid] = rs[kSet];
         }
     };
     auto fragment = [&](const unsigned char* op, int row0) {
@@ -336,19 +343,23 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
 #pragma unroll
         for (int j = 0; j < G::kNj; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
 
-    fetch(first, 0);
-    for (int kb = first; kb < last; ++kb) {
-        const int buf = (kb - first) & 1;
+    int stage = 0, ahead = kStages - 1;
+    auto step = [&](int kb, auto set) {
         if constexpr (DIRECT)
-            wait_loads();
+            wait_loads<(kStages - 2) * (2 * G::kLoads + 1)>();
         else
-            put(buf);
+            put(stage, set);
         __syncthreads();
+        const int buf = stage;
         Wide<FB, EXACT> fb[G::kNj];
 #pragma unroll
         for (int j = 0; j < G::kNj; ++j) fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
-        // (behind these reads, not before them: 1 to 3% on every shape)
-        if (kb + 1 < last) fetch(kb + 1, buf ^ 1);
+        // (behind these reads, not before them: 1 to 3% on every shape.)  With more than two stages
+        // the last block is loaded once more at the end, so that as many loads are on their way
+        if constexpr (DIRECT && kStages > 2)
+            fetch(min(kb + kStages - 1, last - 1), ahead, set);
+        else if (kb + (DIRECT ? 1 : G::kSets) < last)
+            fetch(kb + (DIRECT ? 1 : G::kSets), ahead, set);
         const float sb1 = scales[buf][TILE + wn];
 #pragma unroll
         for (int i = 0; i < G::kMi; ++i) {
@@ -377,7 +388,27 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void fp8
                 }
             }
         }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
+    };
+    using Set0 = std::integral_constant<int, 0>;
+    using Set1 = std::integral_constant<int, !DIRECT && G::kSets == 2 ? 1 : 0>;
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int p = 0; p < kStages - 1; ++p) fetch(min(first + p, last - 1), p, Set0{});
+    } else {
+        fetch(first, 0, Set0{});
+        if (G::kSets == 2 && first + 1 < last) fetch(first + 1, 0, Set1{});
     }
+    if constexpr (!DIRECT && G::kSets == 2) {
+        for (int kb = first; kb < last; kb += 2) {
+            step(kb, Set0{});
+            if (kb + 1 < last) step(kb + 1, Set1{});
+        }
+    } else {
+        for (int kb = first; kb < last; ++kb) step(kb, Set0{});
+    }
+    if constexpr (DIRECT && kStages > 2) wait_loads<0>();  // the repeated ones: LDS must be left alone
 #pragma unroll
     for (int i = 0; i < G::kMi; ++i)
 #pragma unroll
@@ -488,19 +519,18 @@ struct Shape {
 // About how many microseconds a product takes in `tiles` workgroups of one size and `splits`
 // splits of its nk blocks of k, from measurements of 21 shapes (100 x 700 over 300 to 8192 x
 // 4096 over 4096): a block takes the longer the more workgroups share a CU, up to `most` of them.
-// Off by 20% at most there; what it chooses takes at most 10% more than the best, where
-// 256-tiles throughout take 5 times the best (100 x 700), 64-tiles 1.7 times (4096^3).
+// What it chooses takes at most 15% more than the best there, where 256-tiles throughout
+// take up to 3.5 times the best (512 x 512 over 512: 16.8 and 4.8 us) and 64-tiles 1.8 times (4096^3: 124
+// and 68).
 float estimate(int64_t m, int64_t n, int64_t nk, int tile, int64_t tiles, int64_t splits) {
-    const float most = tile == 256 ? 1.f : tile == 128 ? 2.f : 4.f;
-    const float once = tile == 256 ? 0.f : tile == 128 ? 0.55f : 0.4f;
-    const float more = tile == 256 ? 2.f : tile == 128 ? 0.4f : 0.15f;
-    const float per = float((nk + splits - 1) / splits);
-    const float load = float(tiles * splits) / 256.f;  // workgroups a CU
-    const float full = std::floor(load / most), rest = load - full * most;
-    float t = 2.5f + per * full * (once + more * most);
-    if (rest > 0.f) t += per * (tile == 256 ? more : once + more * std::max(rest, 0.4f));
-    if (splits > 1) t += 5.f + float(splits * m) * float(n) * 1e-6f;
-    return t;
+    const float most = tile == 256 ? 1.f : 2.f;
+    const float first = tile == 256 ? 2.f : tile == 128 ? 0.82f : 0.36f;
+    const float full = tile == 256 ? 2.f : tile == 128 ? 1.12f : 0.5f;
+    const float load = float(tiles * splits) / 256.f, rounds = std::floor(load / most);  // a CU
+    const float rest = load - rounds * most;
+    const float block = rounds * full + (rest > 1.f ? full : rest > 0.f ? first : 0.f);
+    const float join = splits > 1 ? 5.f + float(splits * m) * float(n) * 1e-6f : 0.f;
+    return 2.5f + block * float((nk + splits - 1) / splits) + join;
 }
 
 Shape shape_of(int64_t m, int64_t n, int64_t k) {
