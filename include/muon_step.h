@@ -505,9 +505,10 @@ typedef struct muon_stack {
 } muon_stack_t;
 
 /* Bytes of device workspace (256-byte aligned) of muon_orthogonalize_stack: the
- * whole stack's intermediates.  With less, but at least
- * what one matrix needs (`count` 1), the matrices run in groups that fit, with
- * identical results.  Host-only. */
+ * whole stack's intermediates.  With less, but at least its `count`-th part
+ * (one matrix of this stack: how a matrix is divided among workgroups depends on
+ * how many there are), the matrices run in groups that fit, with identical
+ * results.  Host-only. */
 int muon_stack_workspace_bytes(const muon_stack_t* stack, size_t* out_bytes);
 
 /*   coefficients  host, 3 * n_steps float32: (a, b, c) of every step.  Finite, and such
@@ -530,8 +531,12 @@ int muon_orthogonalize_stack(const muon_stack_t* stack, const float* coefficient
  * "front", "sumsq", "norm", "cast", "apply" and "ns_<stage>_t<tile>_<type>"
  * for the Newton-Schulz products (stage a: X X^T, b: b A + c A A, x: a X + B X;
  * tile 64/128/256; type bf16/f32); "grad_norm", "norm_solo", "tensor_norms",
- * "norm_finish", "clip_finish", "clip" and "adamw" for the operators above.  Events come from a pool the library owns;
- * when timing is off the only cost is one flag test per launch. */
+ * "norm_finish", "clip_finish", "clip" and "adamw" for the clipping and AdamW
+ * above; "fp8_cast", "fp8_matmul" and "fp8_join" for 8-bit matrices; "stack_norm",
+ * "stack_split", "stack_a", "stack_b", "stack_x", "stack_join", "stack_scaled",
+ * "stack_whole", "stack_gram", "stack_poly" and "stack_strip" for stacks.  Events
+ * come from a pool the library owns; when timing is off the only cost is one flag
+ * test per launch. */
 typedef struct muon_kernel_time {
     char name[48];
     double total_ms;   /* sum of the launches' event-to-event times */

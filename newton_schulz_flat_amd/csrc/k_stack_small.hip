@@ -96,7 +96,7 @@ struct WholeArgs {
 // RP: rows, padded (32 or 64).  16 waves: A and B in tiles of 16 x 16, a wave each (of 32 rows
 // there are 4 tiles, and four waves share A's K steps); X in blocks of 16 tiles, which are all read
 // before they are renewed in place.  The matrices are small: what counts is the number
-// of waves that wait for LDS at once (64 x 64: 4 waves 24 us, 16 waves TODO).
+// of waves that wait for LDS at once (64 x 64, five steps: 4 waves 24 us, 16 waves 19).
 constexpr int kWholeThreads = 1024;
 
 template <int RP, typename T>

@@ -377,3 +377,90 @@ def test_descriptors_from_an_iterator(gpu, monkeypatch, name, workspace):
     assert args[at + 1] == len(args[at]) == 3
     assert [d.offset for d in args[at]] == [0, 32, 64]
     assert sized in ([], [3])
+
+
+# ------------------------------------------------ 8-bit matrices and stacks
+
+def on_gpu(device, *shape, dtype=None):
+    """A tensor that says that it is on a GPU."""
+    import torch
+
+    class OnGpu(torch.Tensor):
+        is_cuda = property(lambda self: True)
+        device = property(lambda self: torch.device("cuda", self.at))
+
+        def get_device(self):
+            return self.at
+    t = torch.zeros(*shape, dtype=dtype or torch.float32).as_subclass(OnGpu)
+    t.at = device
+    return t
+
+
+MATRIX_TAKES = {"muon_fp8_cast": ["codes", "scales", "codes_t", "scales_t"],
+                "muon_fp8_matmul": ["a", "a_scales", "b_scales", "out", "workspace"],
+                "muon_orthogonalize_stack": ["out", "workspace"]}
+
+
+def matrix_call(name, own=True, **devices):
+    """A call of one of these entry points with everything on device 0 but for what is named."""
+    import torch
+    at = lambda what: devices.get(what, devices.get("all", 0))
+    e4m3 = torch.float8_e4m3fn
+    ws = dict(workspace=on_gpu(at("workspace"), 4096, dtype=torch.uint8)) if own else {}
+    if name == "muon_fp8_cast":
+        return nsf.muon_fp8_cast(on_gpu(at("x"), 8, 256), on_gpu(at("codes"), 8, 256, dtype=e4m3),
+                                 on_gpu(at("scales"), 8, 2), on_gpu(at("codes_t"), 256, 8, dtype=e4m3),
+                                 on_gpu(at("scales_t"), 256, 1))
+    if name == "muon_fp8_matmul":
+        return nsf.muon_fp8_matmul(on_gpu(at("a"), 8, 256, dtype=e4m3), on_gpu(at("a_scales"), 8, 2),
+                                   on_gpu(at("b"), 130, 256, dtype=e4m3), on_gpu(at("b_scales"), 2, 2),
+                                   on_gpu(at("out"), 8, 130), **ws)
+    return nsf.muon_orthogonalize_stack(on_gpu(at("x"), 2, 8, 16), on_gpu(at("out"), 2, 8, 16), **ws)
+
+
+@pytest.fixture
+def matrices(gpu, monkeypatch):
+    lib = Library(gpu)
+    monkeypatch.setattr(nsf, "load_library", lambda: lib)
+    monkeypatch.setattr(nsf, "muon_fp8_workspace_bytes", lambda m, n, k: 4096)
+    monkeypatch.setattr(nsf, "muon_stack_workspace_bytes", lambda x: 4096)
+    monkeypatch.setattr(nsf, "_call_workspaces", {})
+    return lib
+
+
+@pytest.mark.parametrize("index", [0, 1])
+@pytest.mark.parametrize("name", MATRIX_TAKES)
+def test_matrices_launch_on_the_device_of_their_tensors(gpu, matrices, name, index):
+    for workspace in (True, False):
+        matrices.calls.clear()
+        matrix_call(name, workspace, all=index)
+        (called, current, args), = matrices.calls
+        assert (called, current, getattr(args[-1], "value", args[-1])) == (name, index, 100 + index)
+        assert gpu["device"] == 0
+
+
+@pytest.mark.parametrize("name,odd", [(n, k) for n in MATRIX_TAKES for k in MATRIX_TAKES[n]])
+def test_matrices_refuse_tensors_of_two_devices(gpu, matrices, name, odd):
+    with pytest.raises(ValueError, match="is on cuda:"):
+        matrix_call(name, **{odd: 1})
+    assert not matrices.calls
+
+
+@pytest.mark.parametrize("name", ["muon_fp8_matmul", "muon_orthogonalize_stack"])
+def test_matrices_default_workspace(gpu, matrices, name):
+    """Refused under capture, one per device and stream otherwise; two threads on one stream
+    take turns."""
+    gpu["capturing"] = 1
+    with pytest.raises(RuntimeError, match="explicit workspace"):
+        matrix_call(name, False, all=1)
+    assert not matrices.calls
+    matrix_call(name, True, all=1)
+    matrix_call(name, False)                  # another device captures
+    assert len(matrices.calls) == 2 and len(nsf._call_workspaces) == 1
+    gpu["capturing"] = None
+    matrix_call(name, False, all=1)
+    assert len(nsf._call_workspaces) == 2
+    matrices.pause = 0.05
+    matrices.events.clear()
+    from_two_threads(lambda: matrix_call(name, False))
+    assert len(matrices.calls) == 5 and not overlap(matrices.events)

@@ -256,3 +256,211 @@ def test_another_stream():
         nsf.muon_fp8_matmul(a, sa, b, sb, out)
     torch.cuda.current_stream().wait_stream(stream)
     check_product(out, wa, wb, "f32")
+
+
+# --------------------------------------------------------------- larger shapes, against float64 on the GPU
+
+def wide_gpu(codes, scales):
+    s = scales.double()
+    if s.shape[0] != codes.shape[0]:
+        s = s.repeat_interleave(128, 0)[:codes.shape[0]]
+    return codes.double() * s.repeat_interleave(128, 1)[:, :codes.shape[1]]
+
+
+def check_on_gpu(got, a, sa, b, sb, before=None):
+    """As check_product; what the 8-bit instruction cuts off, 7 of 8 products at 2^-13 of their
+    group's largest, is below 7 x 2^-13 of the sum of magnitudes."""
+    wa, wb = wide_gpu(a, sa), wide_gpu(b, sb)
+    want, total = wa @ wb.t().contiguous(), wa.abs() @ wb.abs().t().contiguous()
+    bound = (128 + fo.blocks(a.shape[1]) + 4) * 2.0 ** -24 * total
+    if before is not None:
+        want = want + before.double()
+        bound += 2.0 ** -23 * want.abs()
+    err = (got.double() - want).abs()
+    if got.dtype == torch.bfloat16:
+        bound = bound + 7 * 2.0 ** -13 * total
+        bound = bound + 2.0 ** -8 * (want.abs() + bound)
+        assert torch.linalg.norm(err) <= 2.0 ** -8 * torch.linalg.norm(want)
+    else:
+        bound = bound + 2.0 ** -24 * want.abs()
+    assert (err <= bound + 1e-300).all(), (err / (bound + 1e-300)).max().item()
+
+
+def big_operand(rows, k, fmt, block, seed, pad):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, k, generator=g, device="cuda")
+    x *= torch.exp2(torch.randint(-6, 7, (rows, 1), generator=g, device="cuda").float())
+    held = torch.full((rows, k + pad), 0x7F, dtype=torch.uint8, device="cuda").view(TYPES[fmt])[:, :k]
+    s = nsf.fp8_scales(rows, k, block, "cuda")
+    nsf.muon_fp8_cast(x, held, s)
+    return held, s
+
+
+# tiles of 256 (whole and ragged), of 128, and of either with k's blocks shared by workgroups
+BIG = [(2048, 8192, 1152), (2000, 8100, 1168), (1000, 4000, 512), (1024, 1024, 8192), (600, 2048, 7168),
+       (4096, 1024, 8200)]
+
+
+@pytest.mark.parametrize("m,n,k", BIG)
+@pytest.mark.parametrize("blocks", ["square", "row"])
+@pytest.mark.parametrize("pad", [0, 11])
+def test_large_products(m, n, k, blocks, pad):
+    for fa, fb, out, add in (("e4m3", "e4m3", "bf16", False), ("e5m2", "e4m3", "f32", True),
+                             ("e4m3", "e5m2", "f32", False), ("e5m2", "e5m2", "bf16", False)):
+        say("large product", m, n, k, blocks, fa, fb, out, add, pad)
+        a, sa = big_operand(m, k, fa, "row", 1, pad)
+        b, sb = big_operand(n, k, fb, blocks, 2, pad)
+        c = torch.full((m, n), 0.5, dtype=DT[out], device="cuda")
+        before = c.clone() if add else None
+        nsf.muon_fp8_matmul(a, sa, b, sb, c, accumulate=add)
+        check_on_gpu(c, a, sa, b, sb, before)
+
+
+def test_products_past_2_31_elements():
+    say("past 2^31")
+    m, n, k = 50001, 50000, 144            # 2.5 G results
+    a, sa = big_operand(m, k, "e4m3", "row", 1, 0)
+    b, sb = big_operand(n, k, "e4m3", "square", 2, 0)
+    c = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    nsf.muon_fp8_matmul(a, sa, b, sb, c)
+    for at in (0, 25000, m - 70):
+        check_on_gpu(c[at:at + 70], a[at:at + 70], sa[at:at + 70], b, sb)
+
+
+def test_casts_past_2_31_elements():
+    say("cast past 2^31")
+    rows, cols = 70000, 32768              # 2.3 G elements
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    for block in ("row", "square"):
+        q = torch.empty(rows, cols, dtype=TYPES["e4m3"], device="cuda")
+        qt = torch.empty(cols, rows, dtype=TYPES["e4m3"], device="cuda")
+        s, st = nsf.fp8_scales(rows, cols, block, "cuda"), nsf.fp8_scales(cols, rows, block, "cuda")
+        nsf.muon_fp8_cast(x, q, s, qt, st)
+        for at in (0, 128 * 300, rows - rows % 128 - 128):
+            part = x[at:at + 128, cols - 300:].float().cpu().numpy()
+            part = part[:, 300 % 128:]     # whole blocks
+            want, ws = fo.cast(part, "e4m3", block == "square")
+            got = q[at:at + 128, cols - 256:]
+            assert np.array_equal(codes_of(got), want)
+            sc = s[at // 128:at // 128 + 1] if block == "square" else s[at:at + 128]
+            assert np.array_equal(host(sc[:, -2:].contiguous()), ws)
+            want, ws = fo.cast(part.T, "e4m3", block == "square")
+            assert np.array_equal(codes_of(qt[cols - 256:, at:at + 128]), want)
+            sc = st[-2:] if block == "square" else st[cols - 256:]
+            assert np.array_equal(host(sc[:, at // 128:at // 128 + 1].contiguous()), ws)
+        del q, qt
+
+
+def test_one_matrix_as_both_operands():
+    say("a a^T")
+    a, sa = big_operand(300, 700, "e4m3", "row", 1, 0)
+    out = torch.empty(300, 300, device="cuda")
+    nsf.muon_fp8_matmul(a, sa, a, sa, out)
+    check_on_gpu(out, a, sa, a, sa)
+    assert torch.equal(out, out.t())
+
+
+def test_scales_in_either_order():
+    """Scales that lie row after row give what block-major ones give."""
+    say("scale order")
+    a, sa = big_operand(300, 700, "e4m3", "row", 1, 0)
+    b, sb = big_operand(200, 700, "e4m3", "square", 2, 0)
+    one, two = (torch.empty(300, 200, device="cuda") for _ in range(2))
+    nsf.muon_fp8_matmul(a, sa, b, sb, one)
+    nsf.muon_fp8_matmul(a, sa.contiguous(), b, sb.contiguous(), two)
+    assert sa.contiguous().stride() != sa.stride() and torch.equal(one, two)
+    x = values(300, 700, "f32", 3)
+    q, qs = torch.empty_like(a), torch.empty(300, 6, device="cuda")
+    nsf.muon_fp8_cast(x, q, qs)
+    want = fo.cast(x.cpu().numpy(), "e4m3", False)
+    assert np.array_equal(codes_of(q), want[0]) and np.array_equal(host(qs), want[1])
+
+
+# --------------------------------------------------------------- a layer's training step
+
+def test_training_step_of_a_layer():
+    """The 8-bit copy of the weight, the layer's three products with the weight's gradient added
+    into the flat buffer, the norm, the clipped step and the refreshed copy: eager, then captured
+    and replayed on other inputs."""
+    say("layer")
+    m, n, k = 96, 256, 384
+    hyper = [(0.02, 0.01, 0.95, True)]
+    descs = [(0, n, k)]
+    state = {name: torch.zeros(n * k, device="cuda") for name in ("w", "grad", "mom")}
+    x, dy = (torch.zeros(m, j, dtype=torch.bfloat16, device="cuda") for j in (k, n))
+    y, dx = (torch.zeros(m, j, dtype=torch.bfloat16, device="cuda") for j in (n, k))
+    shapes = {"w": (n, k), "wt": (k, n), "x": (m, k), "xt": (k, m), "dy": (m, n), "dyt": (n, m)}
+    q = {name: torch.zeros(*z, dtype=TYPES["e5m2" if name[0] == "d" else "e4m3"], device="cuda")
+         for name, z in shapes.items()}
+    s = {name: nsf.fp8_scales(*z, "square" if name[0] == "w" else "row", "cuda")
+         for name, z in shapes.items()}
+    groups, clip = nsf.group_table(hyper, "cuda"), nsf.clip_state("cuda")
+    tensors = nsf.tensor_list([state["grad"]])
+    ws = torch.empty(max(nsf.muon_workspace_bytes(descs), 1 << 20), dtype=torch.uint8, device="cuda")
+    need = max(nsf.muon_fp8_workspace_bytes(*z) for z in ((m, n, k), (m, k, n), (n, k, m)))
+    ws8 = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def step():
+        w = state["w"].view(n, k)
+        state["grad"].zero_()
+        nsf.muon_fp8_cast(x, q["x"], s["x"], q["xt"], s["xt"])
+        nsf.muon_fp8_matmul(q["x"], s["x"], q["w"], s["w"], y, workspace=ws8)
+        nsf.muon_fp8_cast(dy, q["dy"], s["dy"], q["dyt"], s["dyt"])
+        nsf.muon_fp8_matmul(q["dy"], s["dy"], q["wt"], s["wt"], dx, workspace=ws8)
+        nsf.muon_fp8_matmul(q["dyt"], s["dyt"], q["xt"], s["xt"], state["grad"].view(n, k),
+                            accumulate=True, workspace=ws8)
+        nsf.muon_grad_norm(tensors, 1.0, clip, workspace=ws)
+        nsf.muon_step_clipped(state["w"], state["grad"], state["mom"], descs, groups, clip, workspace=ws)
+        nsf.muon_fp8_cast(w, q["w"], s["w"], q["wt"], s["wt"])
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        state["w"].normal_(0, 0.02, generator=g)
+        state["mom"].normal_(0, 1e-3, generator=g)
+        x.normal_(0, 1, generator=g)
+        dy.normal_(0, 1e-2, generator=g)
+        nsf.muon_fp8_cast(state["w"].view(n, k), q["w"], s["w"], q["wt"], s["wt"])
+
+    fill(0)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2, 3):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {name: t.clone() for name, t in (("y", y), ("dx", dx), *state.items())}
+        copies = {name: q[name].view(torch.uint8).clone() for name in ("w", "wt")}
+        fill(seed)
+        old = {name: wide_gpu(q[name], s[name]) for name in ("w", "wt")}
+        step()
+        for name, t in (("y", y), ("dx", dx), *state.items()):
+            assert torch.equal(got[name], t), name
+        # the refreshed copies are the casts of the updated weight
+        wn = state["w"].view(n, k).cpu().numpy()
+        for name, m_ in (("w", wn), ("wt", wn.T)):
+            want = fo.cast(m_, "e4m3", True)
+            assert np.array_equal(copies[name].cpu().numpy(), want[0])
+            assert np.array_equal(host(s[name].contiguous()), want[1])
+        # gradients of L = sum(dy * y), y = x w^T, against its differences: L is linear in each of x and
+        # w, so a difference quotient of any step is the gradient, up to float64 roundings
+        wide = {name: wide_gpu(q[name], s[name]) for name in ("x", "dy", "dyt", "xt")}
+        grad = got["grad"].view(n, k).double()
+        for i, j in ((0, 0), (17, 300), (n - 1, k - 1)):
+            loss = []
+            for move in (-1.0, 1.0):
+                w = old["w"].clone()
+                w[i, j] += move
+                loss.append((wide["dyt"].t() * (wide["xt"].t() @ w.t())).sum())
+            size = (wide["dyt"][i].abs() * wide["xt"][j].abs()).sum()
+            assert abs((loss[1] - loss[0]) / 2 - grad[i, j]) <= 200 * 2.0 ** -24 * size + 1e-12
+            loss = []
+            for move in (-1.0, 1.0):
+                xs = wide["x"].clone()
+                xs[i % m, j] += move
+                loss.append((wide["dy"] * (xs @ old["wt"])).sum())
+            size = (wide["dy"][i % m].abs() * old["wt"][j].abs()).sum()
+            assert abs((loss[1] - loss[0]) / 2 - got["dx"][i % m, j]) <= (
+                2.0 ** -8 * abs(got["dx"][i % m, j]) * 1.01 + (7 * 2.0 ** -13 + 200 * 2.0 ** -24) * size + 1e-12)

@@ -191,3 +191,124 @@ def test_same_update_as_the_flat_entry_point():
     for k in range(3):
         assert rel_fro(out[k].double().cpu().numpy(),
                        flat.view_as(x)[k].double().cpu().numpy()) <= 2e-5
+
+
+# --------------------------------------------------------------- larger matrices, against float64 on the GPU
+
+def reference(u, steps, digits=None):
+    """fo.newton_schulz on the GPU."""
+    def held(m):
+        if digits is None:
+            return m
+        step = torch.exp2(torch.ceil(torch.log2(m.abs().clamp(min=1e-30))) - digits)
+        return torch.round(m / step) * step
+
+    x = u.double()
+    x = x / (torch.linalg.norm(x) + 1e-7)
+    tall = x.shape[0] > x.shape[1]
+    x = held(x.t().contiguous() if tall else x)
+    for a, b, c in steps:
+        a, b, c = (float(np.float32(v)) for v in (a, b, c))
+        g = held(x @ x.t().contiguous())
+        x = held(a * x + held(b * g + c * (g @ g)) @ x)
+    return x.t() if tall else x
+
+
+# one workgroup a matrix with more than 64 KB of LDS; strips with B made beside them and apart; tiles
+# of 64, 128 and 256, a workgroup a tile and shared
+@pytest.mark.parametrize("count,rows,cols", [(2, 64, 400), (1, 1000, 30), (3, 64, 900), (1, 5000, 60),
+                                             (1, 128, 8000), (40, 100, 700), (1, 1024, 1024),
+                                             (1, 1500, 2100), (1, 2048, 2048), (8, 1024, 1000),
+                                             (1, 256, 8192), (1, 4096, 4096), (1, 4100, 2000)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_larger_matrices(count, rows, cols, out):
+    say("larger", count, rows, cols, out)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = 1e-3 * torch.randn(count, rows, cols, generator=g, device="cuda")
+    o = torch.empty(count, rows, cols, dtype=DT[out], device="cuda")
+    nsf.muon_orthogonalize_stack(x, o)
+    again = torch.empty_like(o)
+    nsf.muon_orthogonalize_stack(x, again)
+    assert torch.equal(o, again)
+    for k in {0, count - 1}:
+        want = reference(x[k], nsf.QUINTIC)
+        tol = 2e-6 + 8 * torch.linalg.norm(reference(x[k], nsf.QUINTIC, 22) - want) / torch.linalg.norm(want)
+        tol += 2.0 ** -8 if out == "bf16" else 0
+        want = want * max(1.0, rows / cols) ** 0.5
+        assert torch.linalg.norm(o[k].double() - want) <= tol * torch.linalg.norm(want)
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 400), (60, 2000), (128, 128), (1100, 900), (2048, 2048)])
+def test_larger_replayed(rows, cols):
+    say("larger replay", rows, cols)
+    x = stack(2, rows, cols, seed=1)
+    out, want = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(nsf.muon_stack_workspace_bytes(x), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nsf.muon_orthogonalize_stack(x, out, workspace=ws)
+    for seed in (2, 3, 4):
+        x.copy_(stack(2, rows, cols, seed=seed))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        nsf.muon_orthogonalize_stack(x, want)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(5, 100, 700), (3, 700, 900), (2, 2048, 1024)])
+def test_larger_groups_that_fit(count, rows, cols):
+    say("larger groups", count, rows, cols)
+    x = stack(count, rows, cols, seed=8)
+    one, two = torch.empty_like(x), torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, one)
+    ws = torch.full((nsf.muon_stack_workspace_bytes(x) // count,), 0xFF, dtype=torch.uint8, device="cuda")
+    nsf.muon_orthogonalize_stack(x, two, workspace=ws)
+    assert torch.equal(one, two)
+    with pytest.raises(nsf.MuonError, match="WORKSPACE"):
+        nsf.muon_orthogonalize_stack(x, two, workspace=ws[:-256])
+
+
+def test_offsets_past_2_31():
+    """Three matrices of 1.05 G elements: one step, checked on some columns of the last one."""
+    say("past 2^31")
+    rows, cols = 1000, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(3, rows, cols, dtype=torch.bfloat16, device="cuda")
+    for k in range(3):
+        x[k].normal_(0, 1e-3 * (k + 1), generator=g)
+    out = torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, out, coefficients=nsf.QUINTIC[:1], scale=1.0)
+    for k in (0, 2):
+        gram = torch.zeros(rows, rows, dtype=torch.float64, device="cuda")
+        for at in range(0, cols, 1 << 17):
+            part = x[k, :, at:at + (1 << 17)].double()
+            gram += part @ part.t().contiguous()
+        norm = torch.sqrt(torch.trace(gram)) + 1e-7
+        gram /= norm * norm
+        a, b, c = (float(np.float32(v)) for v in nsf.QUINTIC[0])
+        poly = b * gram + c * gram @ gram
+        for at in (0, cols // 2 + 5, cols - 100):
+            u = x[k, :, at:at + 100].double() / norm
+            want = a * u + poly @ u
+            err = torch.linalg.norm(out[k, :, at:at + 100].double() - want)
+            assert err <= (2.0 ** -8 + 1e-5) * torch.linalg.norm(want)
+
+
+def test_another_stream_and_default_workspaces():
+    say("stream")
+    x, z = stack(2, 200, 150, seed=1), stack(2, 150, 300, seed=2)
+    want = [torch.empty_like(x), torch.empty_like(z)]
+    nsf.muon_orthogonalize_stack(x, want[0])
+    nsf.muon_orthogonalize_stack(z, want[1])
+    got = [torch.empty_like(x), torch.empty_like(z)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s, u, o in zip(streams, (x, z), got):
+            with torch.cuda.stream(s):
+                nsf.muon_orthogonalize_stack(u, o)
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
