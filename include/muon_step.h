@@ -450,7 +450,7 @@ typedef struct muon_fp8 {
  * (rows x cols of dtype, row_stride elements between rows) and its transpose, each
  * in its own blocks.  For each block
  *   m = max(largest magnitude, 2^-100),  s = fl(m / L)     L = 448 or 57344
- *   code = fl(x L / m) rounded to nearest even, fl one float32 rounding
+ *   code = x L / m rounded to nearest, to even in the middle (once)
  * A block that holds a NaN gets the scale NaN, one that holds an infinity an
  * infinite one; its codes say nothing.  x, codes and scales must not overlap: neither each other nor,
  * where there are gaps between rows, each other's span from the first element to

@@ -1,14 +1,18 @@
 // Casts into 8-bit floats with a scale for each 1 x 128 or 128 x 128 block, of a
 // matrix and of its transpose in one pass.
 //
-//   m = max(largest magnitude of the block, 2^-100),  s = fl(m / L),  code = rne8(fl(x L / m))
+//   m = max(largest magnitude of the block, 2^-100),  s = fl(m / L),  code = rne8(x L / m)
 //
-// with L the format's largest number.  L / m is held in two float32 (high and rest), so that
-// x L / m is off by one float32 rounding only: with fl(x fl(1 / s)), three roundings, more than twice as
-// many elements near the middle between two codes get the farther one.  |x| L / m exceeds
-// L by less than a float32 rounding, far below the middle between L and the next step, so no
-// code leaves the format's range and nothing has to be clamped.  Magnitudes are compared as bit
-// patterns, in which a NaN is above infinity: a block that holds one gets the scale NaN.
+// with L the format's largest number.  The code is that of the quotient itself.  L / m is held in two
+// float32 (high and rest), so that y = x high + x rest is x L / m with one float32 rounding and before
+// it an error below 2^-30 (2^-47 unless m is above 2^100).  Middles between codes are float32 numbers,
+// and a quotient that is not one lies at least 2^-29 beside it (7 X and D M, integers of 27 and
+// 29 bits, differ by one at least), so y is on the quotient's side of every middle or on the middle
+// itself; where it is on it, x L and y m, both exact in float64, tell the side.  (Without that
+// look 28 of 58.7 million float32 elements get the farther of two codes, with fl(x fl(1 / s)) 42;
+// it costs 1% of the time.)
+// Magnitudes are compared as bit patterns, in which a NaN is above infinity: a block that holds
+// one gets the scale NaN.
 //
 // A workgroup takes a 128 x 128 tile, a thread an 8 x 8 block of it, held in
 // registers: 16 neighbouring lanes read one row's 128 elements.  Row blocks
@@ -89,11 +93,18 @@ struct Factor {
     __device__ __forceinline__ float of(float x) const { return __builtin_fmaf(x, high, x * rest); }
 };
 template <bool E5M2>
+constexpr float kTop = E5M2 ? 57344.f : 448.f;
+__device__ __forceinline__ float held_max(uint32_t largest) {
+    return __uint_as_float(max(largest, 27u << 23));  // 2^-100
+}
+template <bool E5M2>
 __device__ __forceinline__ Factor factor_of(uint32_t largest, float* scale) {
-    const float m = __uint_as_float(max(largest, 27u << 23));  // 2^-100
-    const float top = E5M2 ? 57344.f : 448.f;
+    const float m = held_max(largest);
+    const float top = kTop<E5M2>;
     *scale = m / top;
-    const float high = top / m;
+    float high = top / m;
+    // not above L / m: a negative rest would turn -0 into 0
+    if (__builtin_fmaf(-high, m, top) < 0.f) high = __uint_as_float(__float_as_uint(high) - 1);
     return {high, __builtin_fmaf(-high, m, top) / m};
 }
 // Lane n's value in all 16 lanes of its DPP row.
@@ -113,6 +124,40 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
         w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     }
     return uint32_t(w);
+}
+
+// Eight codes.  EXACT: a y on a middle is looked at again.  Middles of normal codes have the bit below
+// the code's last one and none behind it; of subnormal codes, which are rare, every y but 0 is looked
+// at.  m(): the block's held_max, called by whole waves.  (bfloat16 x and m have 8 bits: a quotient
+// that is no middle lies 2^-14 beside it at least, so y is never on one by rounding.)
+template <bool E5M2, bool EXACT, typename M>
+__device__ __forceinline__ uint2 encode8(const Factor& f, const float (&x)[8], M&& m) {
+    constexpr int kBehind = E5M2 ? 11 : 12;  // shift that leaves that bit and those behind it
+    constexpr uint32_t kNormal = (E5M2 ? 127 - 14 : 127 - 6) << 23;
+    float y[8];
+    uint32_t middle = ~0u, small = ~0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = f.of(x[j]);
+        if constexpr (EXACT) {
+            const uint32_t bits = __float_as_uint(y[j]);
+            middle = min(middle, (bits << kBehind) + 0x80000000u);
+            small = min(small, (bits << 1) - 2);  // (0: the largest)
+        }
+    }
+    if constexpr (EXACT) {
+        if (__builtin_amdgcn_ballot_w64(middle == 0 || small < (kNormal << 1) - 2) != 0) {
+            const double top = double(kTop<E5M2>), held = double(m());
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t bits = __float_as_uint(y[j]);
+                const double exact = fabs(double(x[j]) * top), here = fabs(double(y[j]) * held);
+                if (bits << (kBehind + 1) == 0 && y[j] != 0.f && exact != here)
+                    y[j] = __uint_as_float(exact > here ? bits + 1 : bits - 1);
+            }
+        }
+    }
+    return {encode4<E5M2>(y[0], y[1], y[2], y[3]), encode4<E5M2>(y[4], y[5], y[6], y[7])};
 }
 
 // The first `left` of eight codes.
@@ -140,7 +185,9 @@ template <typename T, bool SQUARE, bool E5M2>
 __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
     __shared__ uint32_t col_max[4][kFp8Block];
     __shared__ Factor factors[kFp8Block];
+    __shared__ float held[kFp8Block];
     __shared__ uint2 turned[kFp8Block * 16];
+    constexpr bool kExact = std::is_same_v<T, float>;
     const int tr = blockIdx.x / a.col_tiles, tc = blockIdx.x % a.col_tiles;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;  // 8-column and 8-row group
     const int r0 = tr * kFp8Block + rg * 8, c0 = tc * kFp8Block + cg * 8;
@@ -158,6 +205,7 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
     }
 
     Factor all = {0.f, 0.f};
+    float all_held = 0.f;
     if constexpr (SQUARE) {
         uint32_t top = 0;
 #pragma unroll
@@ -168,7 +216,8 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
         if (cg == 0) col_max[0][rg] = top;
         __syncthreads();
         float scale;
-        all = factor_of<E5M2>(row_max(col_max[0][cg]), &scale);
+        top = row_max(col_max[0][cg]);
+        all = factor_of<E5M2>(top, &scale), all_held = held_max(top);
         if (threadIdx.x == 0) {
             if (a.out.codes != nullptr)
                 a.out.scales[tr * a.out.scale_row + tc * a.out.scale_col] = scale;
@@ -180,6 +229,7 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
     if (a.out.codes != nullptr) {
         float scale = 0.f;
         Factor mine = {0.f, 0.f};  // of row cg % 8 of this thread's 8
+        float mine_held = 0.f;
         if constexpr (!SQUARE) {
             uint32_t my_top = 0;
 #pragma unroll
@@ -190,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
                 top = row_max(top);
                 if ((cg & 7) == p) my_top = top;
             }
-            mine = factor_of<E5M2>(my_top, &scale);
+            mine = factor_of<E5M2>(my_top, &scale), mine_held = held_max(my_top);
             if (cg < rows_left && cg < 8)
                 a.out.scales[(r0 + cg) * a.out.scale_row + tc * a.out.scale_col] = scale;
         }
@@ -198,8 +248,7 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
         for_eight([&](auto index) {
             constexpr int p = decltype(index)::value;
             const Factor f = SQUARE ? all : Factor{row_value<p>(mine.high), row_value<p>(mine.rest)};
-            const uint2 w = {encode4<E5M2>(f.of(v[p][0]), f.of(v[p][1]), f.of(v[p][2]), f.of(v[p][3])),
-                             encode4<E5M2>(f.of(v[p][4]), f.of(v[p][5]), f.of(v[p][6]), f.of(v[p][7]))};
+            const uint2 w = encode8<E5M2, kExact>(f, v[p], [&] { return SQUARE ? all_held : row_value<p>(mine_held); });
             if (p < rows_left) store8(q + p * a.out.row_stride, cols_left, w);
         });
     }
@@ -219,8 +268,8 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
         if (threadIdx.x < kFp8Block) {
             const int c = threadIdx.x, col = tc * kFp8Block + c;
             float scale;
-            factors[c] = factor_of<E5M2>(
-                max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c])), &scale);
+            const uint32_t top = max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c]));
+            factors[c] = factor_of<E5M2>(top, &scale), held[c] = held_max(top);
             if (col < a.cols) a.out_t.scales[col * a.out_t.scale_row + tr * a.out_t.scale_col] = scale;
         }
         __syncthreads();
@@ -230,9 +279,9 @@ __global__ __launch_bounds__(kThreads) void fp8_cast_kernel(const CastArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const Factor f = SQUARE ? all : factors[cg * 8 + j];
-        turned[(cg * 8 + j) * 16 + (rg ^ cg)] = {
-            encode4<E5M2>(f.of(v[0][j]), f.of(v[1][j]), f.of(v[2][j]), f.of(v[3][j])),
-            encode4<E5M2>(f.of(v[4][j]), f.of(v[5][j]), f.of(v[6][j]), f.of(v[7][j]))};
+        const float column[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+        turned[(cg * 8 + j) * 16 + (rg ^ cg)] =
+            encode8<E5M2, kExact>(f, column, [&] { return SQUARE ? all_held : held[cg * 8 + j]; });
     }
     __syncthreads();
     const int left = a.rows - tr * kFp8Block - cg * 8;

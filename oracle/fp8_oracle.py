@@ -42,19 +42,10 @@ def blocks(n):
     return -(-n // BLOCK)
 
 
-def times_ratio(x, m, top):
-    """fl(x top / m) as the cast makes it: top / m in two float32 parts, one fused
-    multiplication and addition.  Extended precision (64 digits) holds every product of two float32
-    and the sums here exactly."""
-    x, m, top = np.asarray(x, np.float32), np.float32(m), np.float32(top)
-    wide = np.longdouble
-    high = top / m
-    rest = np.float32(wide(top) - wide(high) * wide(m)) / m
-    return (wide(1) * x * wide(high) + (x * rest).astype(wide)).astype(np.float32)
-
-
 def cast(x, fmt, square):
-    """(codes, scales) of a float32 matrix, in float32 arithmetic, each operation rounded."""
+    """(codes, scales) of a float32 matrix: scales in float32, codes of x top / m itself.  (In
+    float64 x top is exact, and where the quotient is the middle of two codes, so is it; others
+    lie 2^-29 beside one at least.)"""
     x = np.asarray(x, np.float32)
     rows, cols = x.shape
     high = BLOCK if square else 1
@@ -67,7 +58,7 @@ def cast(x, fmt, square):
             m = np.float32(max(np.max(np.abs(part)), FLOOR))
             scales[i, j] = m / top
             codes[i * high:(i + 1) * high, j * BLOCK:(j + 1) * BLOCK] = encode(
-                times_ratio(part, m, top), fmt)
+                part.astype(np.float64) * np.float64(top) / np.float64(m), fmt)
     return codes, scales
 
 

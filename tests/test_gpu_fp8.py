@@ -81,6 +81,35 @@ def test_cast_ties_zeros_and_small_numbers(block):
         assert np.array_equal(codes_of(got), want[0])
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block", ["row", "square"])
+def test_cast_numbers_beside_the_middles(block, fmt):
+    """The float32 numbers closest to every middle between two codes, their neighbours, and exact
+    middles whose L / m is no float32: all lie nearer to it than a rounding of the quotient."""
+    say("cast beside middles", block, fmt)
+    rng = np.random.default_rng(3)
+    v = fo.numbers(fmt)
+    middles, top = (v[1:] + v[:-1]) / 2, v[-1]
+    rows = 128 * 24
+    m = np.exp2(rng.uniform(-99, 127.5, rows)).astype(np.float32)
+    m[::3] = np.float32(7) * rng.integers(1, 100, rows)[::3].astype(np.float32)
+    m[:4] = 3.4e38, 2.0 ** 101, 2.0 ** -100, 1.0
+    if block == "square":
+        m = m.reshape(-1, 128).max(axis=1).repeat(128)
+    x = np.zeros((rows, 256), np.float32)
+    near = (rng.choice(middles, x.shape) * m[:, None].astype(np.float64) / top).astype(np.float32)
+    x[:] = np.nextafter(near, np.float32(np.inf) * rng.choice([-1, 1], x.shape).astype(np.float32))
+    x = np.where(rng.integers(0, 3, x.shape) == 0, x, near) * rng.choice(np.float32([-1, 1, 1, 0]), x.shape)
+    x[:, ::128] = m[:, None]
+    for part in (x, np.ascontiguousarray(x.T)):
+        t = torch.from_numpy(part).cuda()
+        (q, qt), (s, st) = cast(t, fmt, block)
+        for got, sc, w in ((q, s, part), (qt, st, part.T)):
+            want = fo.cast(w, fmt, block == "square")
+            assert np.array_equal(host(sc.contiguous()).view(np.uint32), want[1].view(np.uint32))
+            assert np.array_equal(codes_of(got), want[0])
+
+
 def test_cast_nan_and_infinity_stay_in_their_block():
     say("cast nan")
     x = values(200, 300, "f32", 5)
