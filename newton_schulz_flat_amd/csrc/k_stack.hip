@@ -489,6 +489,9 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
                  : stack_scaled_kernel<float, float><<<grid, dim3(256), 0, s>>>(in);
         return hipGetLastError();
     }
+    if (sh.r <= 128)
+        return launch_stack_strips(st, sh, count, in, x[0], x[1], reinterpret_cast<unsigned char*>(b) + a_bytes, b,
+                                   plan, scale, s);
     {
         LaunchTimer timer("stack_split", s);
         const dim3 grid = dim3(unsigned((sh.rp + 63) / 64 * (sh.cp / 64) * count));
@@ -501,9 +504,6 @@ hipError_t run_group(const muon_stack_t& st, const StackShape& sh, int64_t first
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
-    if (sh.r <= 128)
-        return launch_stack_strips(st, sh, count, in.out, x[0], x[1],
-                                   reinterpret_cast<unsigned char*>(b) + a_bytes, b, scales, plan, scale, s);
     for (int t = 0; t < n; ++t) {
         ProductArgs g{};
         g.x = x[t & 1], g.x_next = x[(t + 1) & 1], g.a = a, g.b = b;

@@ -8,8 +8,11 @@
 // columns, X <- a X + B X in place, and adds X X^T of the strip to its own partial
 // Gram matrix; stack_poly adds a matrix's partial ones in order and makes B = b A + c A A of
 // them.  Two launches and one read and write of X a step, where the stages of k_stack.hip take
-// three and two reads.
+// three and two reads.  A strip of 128 rows takes 5 us of which 1.4 are matrix instructions: three
+// barriers a strip and one workgroup a CU.  (Two tiles below each other of the strip a wave, for
+// fewer LDS reads, spilled: 234 us of 5 steps for 206; Gram tiles on and above the diagonal only: 194.)
 #include <algorithm>
+#include <type_traits>
 
 #include "stack_device.h"
 
@@ -237,6 +240,7 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
 // ------------------------------------------------------------- strips of 64 columns
 
 struct StripArgs {
+    InArgs in;
     _Float16* x;    // [matrix][cp / 32][rp][64]
     const float* gram;  // [matrix][part][tile of 16 x 16][lane][4]
     float* gram_next;   // of the next iterate
@@ -315,15 +319,52 @@ struct Poly {
     }
 };
 
-// MODE kGram: X is only read (the Gram matrix of the first iterate).  kStep: B comes from
+// Eight neighbouring elements of U as they are in memory, zeros behind the first `left`.
+template <typename T>
+struct Eight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T* p, int left) {
+        typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+        if (left >= 8) {
+#pragma unroll
+            for (int k = 0; k < int(sizeof(T)) / 2; ++k) {
+                const u32x4_any t = reinterpret_cast<const u32x4_any*>(p)[k];
+                w[4 * k] = t.x, w[4 * k + 1] = t.y, w[4 * k + 2] = t.z, w[4 * k + 3] = t.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < int(2 * sizeof(T)); ++k) w[k] = 0;
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (k < left) {
+                    if constexpr (sizeof(T) == 4)
+                        w[k] = __float_as_uint(p[k]);
+                    else
+                        w[k / 2] |= uint32_t(p[k]) << (16 * (k & 1));
+                }
+        }
+    }
+    __device__ __forceinline__ float operator[](int k) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[k]);
+        else
+            return __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+    }
+};
+struct Nothing {};
+
+// MODE kGram: the Gram matrix of the first iterate.  kStep: B comes from
 // stack_poly_kernel.  kWholeStep: the workgroup makes B of the partial Gram matrices itself, which
-// saves a launch of 5 to 7 us where they are few.
+// saves a launch where they are few (2 x 128 x 512, 4 of them: 92 us, with stack_poly 100), but is work
+// done by every workgroup (64 x 128 x 1024, 4 of them: 212 and 206; 32 x 128 x 4096, 8: 362 and 302).
+// T: U's type, where the iterate is the first one; it is made of U anew in kGram and in the first step
+// (32 x 128 x 4096, bfloat16: 277 us, with a launch that stores it once 303).  void: X.
 enum StripMode { kGram, kStep, kWholeStep };
 
-template <int RP, int MODE>
+template <int RP, int MODE, typename T>
 __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(const StripArgs g) {
     using G = StripGeo<RP>;
-    constexpr bool FIRST = MODE == kGram;
+    constexpr bool FIRST = MODE == kGram, FROM_U = !std::is_void_v<T>;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[G::kStages][G::kOp];
     const int matrix = blockIdx.x / g.parts, part = blockIdx.x % g.parts;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -343,14 +384,66 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
         const int r = (mover >> 4) + p * kRows, c = (mover & 15) ^ turn(r);
         off[p] = (c >> 3) * RP * 128 + r * 128 + (c & 7) * 16;
     }
+    // eight neighbours in a row of U: in a row of the strip, or (tall) in a column, where 4 lanes take
+    // 32 neighbours, 16 columns side by side (16 lanes a column: 8 of them meet in a bank)
+    static_assert(RP * 64 == 8 * G::kThreads, "eight elements a thread");
+    const int across = g.tall ? (wave % (RP / 32) * 4 + (lane & 3)) * 8 : tid % 8 * 8;
+    const int down_to = g.tall ? wave / (RP / 32) * 16 + (lane >> 2) : tid / 8;
+    std::conditional_t<FROM_U, Eight<std::conditional_t<FROM_U, T, float>>, Nothing> u;
+    float inv = 0.f, up = 0.f;
+    const auto take = [&](int strip) {
+        if constexpr (FROM_U) {
+            const int i = g.tall ? strip * 64 + down_to : down_to, j = g.tall ? across : strip * 64 + across;
+            const T* from = static_cast<const T*>(g.in.in) + matrix * g.in.in_stride + int64_t(i) * g.in.in_row + j;
+            u.load(from, i < g.rows ? g.cols - j : 0);
+        }
+    };
+    const auto place = [&](unsigned char* m) {
+        if constexpr (FROM_U) {
+            f16x8 hi, lo;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const Pair p = split(u[k] * inv * up);
+                hi[k] = p.hi, lo[k] = p.lo;
+            }
+            if (g.tall) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    *element_at(m, 256, across + k, down_to, 0) = hi[k];
+                    *element_at(m, 256, across + k, down_to, 1) = lo[k];
+                }
+            } else {
+                *reinterpret_cast<f16x8*>(element_at(m, 256, down_to, across, 0)) = hi;
+                *reinterpret_cast<f16x8*>(element_at(m, 256, down_to, across, 1)) = lo;
+            }
+        }
+    };
     const auto fetch = [&](int strip, int stage) {
-        if (!loads) return;
+        if (FROM_U || !loads) return;
 #pragma unroll
         for (int p = 0; p < G::kLoads; ++p)
             load_to_lds(x + int64_t(strip) * G::kOp, off[p],
                         lds0 + stage * G::kOp + p * G::kMovers * 16 + wave * 1024);
     };
 
+    take(first);
+    if constexpr (FROM_U) {
+        const double norm = matrix_norm(g.in.partial + int64_t(matrix) * g.in.part_slots, g.in.parts);
+        inv = inverse_of(norm);
+        float top = first_bound(norm);
+        const bool small = top < kStackSmallBound;
+        up = power_of_two(small ? stack_exponent(top, 0) : g.in.plan.scales[0].sx);
+        if (FIRST && part == 0) {
+            // the matrix's exponents
+            StackScale* ex = g.in.scales + int64_t(matrix) * kStackScales;
+            if (!small) {
+                if (tid <= g.in.plan.n) ex[tid] = g.in.plan.scales[tid];
+            } else if (tid == 0) {
+                for (int k = 0; k < g.in.plan.n; ++k) ex[k] = stack_scale(g.in.plan.steps[k], top);
+                ex[g.in.plan.n] = {int16_t(stack_exponent(top, 0)), 0, 0, 0};
+            }
+        }
+    }
     StackScale s{};
     float down = 0.f, own = 0.f;
     f16x8 bh[G::kSteps], bl[G::kSteps];
@@ -396,7 +489,10 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
     int stage = 0;
     for (int strip = first; strip < end; ++strip) {
         unsigned char* m = lds[stage];
-        if (loads) {
+        if constexpr (FROM_U) {
+            place(m);
+            if (strip + 1 < end) take(strip + 1);
+        } else if (loads) {
             // all but the next strip's loads (and, of the results' stores, none: loads return in
             // their order, so what is left are these)
             if (strip + 1 < end)
@@ -526,15 +622,15 @@ hipError_t launch_stack_whole(const muon_stack_t& st, const StackShape& sh, cons
 
 namespace {
 
-template <int RP>
+template <int RP, typename T>
 hipError_t run_strips(StripArgs g, float* const (&gram)[2], int64_t count, const StackScale* scales,
                       const StackPlan& plan, hipStream_t s) {
     const dim3 grid = dim3(unsigned(g.parts * count)), block = dim3(StripGeo<RP>::kThreads);
-    const bool whole = g.parts <= 2;
+    const bool whole = g.parts <= (g.parts * count <= 64 ? 4 : 2);
     {
         LaunchTimer timer("stack_gram", s);
         g.gram_next = gram[0];
-        stack_strip_kernel<RP, kGram><<<grid, block, 0, s>>>(g);
+        stack_strip_kernel<RP, kGram, T><<<grid, block, 0, s>>>(g);
     }
     hipError_t e = hipGetLastError();
     for (int t = 0; t < plan.n && e == hipSuccess; ++t) {
@@ -546,24 +642,35 @@ hipError_t run_strips(StripArgs g, float* const (&gram)[2], int64_t count, const
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         LaunchTimer timer("stack_strip", s);
-        if (whole)
-            stack_strip_kernel<RP, kWholeStep><<<grid, block, 0, s>>>(g);
+        if (t == 0)
+            whole ? stack_strip_kernel<RP, kWholeStep, T><<<grid, block, 0, s>>>(g)
+                  : stack_strip_kernel<RP, kStep, T><<<grid, block, 0, s>>>(g);
         else
-            stack_strip_kernel<RP, kStep><<<grid, block, 0, s>>>(g);
+            whole ? stack_strip_kernel<RP, kWholeStep, void><<<grid, block, 0, s>>>(g)
+                  : stack_strip_kernel<RP, kStep, void><<<grid, block, 0, s>>>(g);
         e = hipGetLastError();
     }
     return e;
 }
 
+template <typename T>
+hipError_t run_strips(int64_t rp, const StripArgs& g, float* const (&gram)[2], int64_t count,
+                      const StackScale* scales, const StackPlan& plan, hipStream_t s) {
+    if (rp == 32) return run_strips<32, T>(g, gram, count, scales, plan, s);
+    return rp == 64 ? run_strips<64, T>(g, gram, count, scales, plan, s)
+                    : run_strips<128, T>(g, gram, count, scales, plan, s);
+}
+
 }  // namespace
 
-hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int64_t count, void* out, void* x,
-                               void* gram0, void* gram1, void* b, const StackScale* scales,
-                               const StackPlan& plan, float scale, hipStream_t s) {
+hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int64_t count, const InArgs& in,
+                               void* x, void* gram0, void* gram1, void* b, const StackPlan& plan, float scale,
+                               hipStream_t s) {
     StripArgs g{};
+    g.in = in;
     g.x = static_cast<_Float16*>(x), g.b = static_cast<_Float16*>(b);
     float* const gram[2] = {static_cast<float*>(gram0), static_cast<float*>(gram1)};
-    g.out = out, g.out_stride = st.out_stride, g.out_row = st.out_row;
+    g.out = in.out, g.out_stride = st.out_stride, g.out_row = st.out_row;
     g.cp = int32_t(sh.cp), g.rows = int32_t(st.rows), g.cols = int32_t(st.cols);
     g.tall = sh.tall, g.out_bf16 = st.out_dtype == MUON_DTYPE_BF16, g.scale = scale;
     // about a workgroup a CU for the whole stack (not for `count`, so that groups make the same
@@ -573,9 +680,8 @@ hipError_t launch_stack_strips(const muon_stack_t& st, const StackShape& sh, int
     const int64_t parts = std::min({strips, want, sh.cp / sh.rp, int64_t(32)});
     g.per = int32_t((strips + parts - 1) / parts);
     g.parts = int32_t((strips + g.per - 1) / g.per);
-    if (sh.rp == 32) return run_strips<32>(g, gram, count, scales, plan, s);
-    return sh.rp == 64 ? run_strips<64>(g, gram, count, scales, plan, s)
-                       : run_strips<128>(g, gram, count, scales, plan, s);
+    return st.in_dtype == MUON_DTYPE_BF16 ? run_strips<uint16_t>(sh.rp, g, gram, count, in.scales, plan, s)
+                                          : run_strips<float>(sh.rp, g, gram, count, in.scales, plan, s);
 }
 
 }  // namespace muon

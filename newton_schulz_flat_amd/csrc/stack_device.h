@@ -105,6 +105,8 @@ __device__ __forceinline__ void store_result(T* o, int64_t out_row, bool tall, i
     }
 }
 
+}  // namespace
+
 struct InArgs {
     const void* in;
     void* out;  // split with no steps: the result itself
@@ -118,7 +120,9 @@ struct InArgs {
     StackScale* scales;  // [matrix][kStackScales]
     StackPlan plan;
 };
-static_assert(sizeof(InArgs) + 64 <= 4096, "kernel arguments");
+static_assert(sizeof(InArgs) + 256 <= 4096, "kernel arguments");
+
+namespace {
 
 // ||U|| of a matrix from its partial sums: every wave adds them by itself, in the same order.
 __device__ __forceinline__ double matrix_norm(const double* partial, int parts) {
@@ -137,5 +141,11 @@ __device__ __forceinline__ float first_bound(double norm) {
 }
 
 }  // namespace
+
+// Shorter side up to 128: all steps, from the partial sums of squares on.  `count` matrices of the
+// stack; gram0, gram1: room for rp * cp floats a matrix each.
+hipError_t launch_stack_strips(const muon_stack_t& stack, const StackShape& s, int64_t count, const InArgs& in,
+                               void* x, void* gram0, void* gram1, void* b, const StackPlan& plan, float scale,
+                               hipStream_t stream);
 
 }  // namespace muon

@@ -108,11 +108,6 @@ constexpr size_t kStackWholeLds = 156 * 1024;
 bool stack_is_whole(const StackShape& s);
 hipError_t launch_stack_whole(const muon_stack_t& stack, const StackShape& s, const StackPlan& plan,
                               float scale, hipStream_t stream);
-// Shorter side up to 128: all steps from the first iterate and its exponents on.  `count` matrices
-// of the stack; gram0, gram1: room for rp * cp floats a matrix each.
-hipError_t launch_stack_strips(const muon_stack_t& stack, const StackShape& s, int64_t count, void* out,
-                               void* x, void* gram0, void* gram1, void* b, const StackScale* scales,
-                               const StackPlan& plan, float scale, hipStream_t stream);
 // Workspace bytes of one matrix of a stack of `count`.
 size_t stack_matrix_bytes(const StackShape& s, int64_t count);
 

@@ -256,7 +256,7 @@ def test_larger_replayed(rows, cols):
         assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("count,rows,cols", [(5, 100, 700), (3, 700, 900), (2, 2048, 1024)])
+@pytest.mark.parametrize("count,rows,cols", [(5, 100, 700), (40, 100, 400), (3, 700, 900), (2, 2048, 1024)])
 def test_larger_groups_that_fit(count, rows, cols):
     say("larger groups", count, rows, cols)
     x = stack(count, rows, cols, seed=8)
