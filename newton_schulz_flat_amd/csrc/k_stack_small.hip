@@ -311,7 +311,9 @@ struct Poly {
                                rows_operand(a, in_a, (fj + q) * 16, ks, 1), ph, pl, b[q]);
         }
 #pragma unroll
-        for (int q = 0; q < kMine; ++q) b[q] = acc[q] * own + b[q] * down;
+        for (int q = 0; q < kMine; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[q][e] = __builtin_fmaf(acc[q][e], own, b[q][e] * down);
     }
     __device__ __forceinline__ void put(unsigned char* m, const Place& place, int q, const f32x4& t) const {
         const float v[4] = {t.x, t.y, t.z, t.w};
@@ -357,6 +359,7 @@ struct Nothing {};
 // stack_poly_kernel.  kWholeStep: the workgroup makes B of the partial Gram matrices itself, which
 // saves a launch where they are few (2 x 128 x 512, 4 of them: 92 us, with stack_poly 100), but is work
 // done by every workgroup (64 x 128 x 1024, 4 of them: 212 and 206; 32 x 128 x 4096, 8: 362 and 302).
+// Both give the same bits: fused sums are written out, since the compiler's choice differs.
 // T: U's type, where the iterate is the first one; it is made of U anew in kGram and in the first step
 // (32 x 128 x 4096, bfloat16: 277 us, with a launch that stores it once 303).  void: X.
 enum StripMode { kGram, kStep, kWholeStep };
@@ -401,6 +404,9 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
     const auto place = [&](unsigned char* m) {
         if constexpr (FROM_U) {
             f16x8 hi, lo;
+            // (places are worked out for every strip: held, they cost spilled registers)
+            int col = across, row = down_to;
+            asm volatile("" : "+v"(col), "+v"(row));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const Pair p = split(u[k] * inv * up);
@@ -409,12 +415,12 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
             if (g.tall) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    *element_at(m, 256, across + k, down_to, 0) = hi[k];
-                    *element_at(m, 256, across + k, down_to, 1) = lo[k];
+                    *element_at(m, 256, col + k, row, 0) = hi[k];
+                    *element_at(m, 256, col + k, row, 1) = lo[k];
                 }
             } else {
-                *reinterpret_cast<f16x8*>(element_at(m, 256, down_to, across, 0)) = hi;
-                *reinterpret_cast<f16x8*>(element_at(m, 256, down_to, across, 1)) = lo;
+                *reinterpret_cast<f16x8*>(element_at(m, 256, row, col, 0)) = hi;
+                *reinterpret_cast<f16x8*>(element_at(m, 256, row, col, 1)) = lo;
             }
         }
     };
@@ -517,7 +523,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
                 const int col = (wc * 2 + j) * 16;
                 get_quad(m, in_strip, wr, wc * 2 + j, v[j]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = own * v[j][e] + down * y[j][e];
+                for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(own, v[j][e], down * y[j][e]);
                 if (g.last) {
                     if (g.out_bf16)
                         store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
