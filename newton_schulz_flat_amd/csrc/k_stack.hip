@@ -345,6 +345,11 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void sta
             __syncthreads();
             const unsigned char* p_lds = lds + stage * 2 * G::kOp;
             const unsigned char* q_lds = p_lds + G::kOp;
+            // P's first rows before Q's: LDS returns in order, and the first products wait for fewer reads
+            // (1024 x 1024 196 us to 188; larger tiles have steps that are long enough, 1% slower)
+            constexpr bool kEarly = TILE == 64;
+            f16x8 early_h, early_l;
+            if constexpr (kEarly) early_h = rows_fragment(p_lds, wm, 0), early_l = rows_fragment(p_lds, wm, 1);
             f16x8 qh[G::kNj], ql[G::kNj];
 #pragma unroll
             for (int j = 0; j < G::kNj; ++j) {
@@ -359,8 +364,8 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, Geo<TILE>::kMinWaves) void sta
             if (G::kStages > 2 || ks + 1 < k1) fetch(ahead);
 #pragma unroll
             for (int i = 0; i < G::kMi; ++i) {
-                const f16x8 ph = rows_fragment(p_lds, wm + 16 * i, 0);
-                const f16x8 pl = rows_fragment(p_lds, wm + 16 * i, 1);
+                const f16x8 ph = kEarly && i == 0 ? early_h : rows_fragment(p_lds, wm + 16 * i, 0);
+                const f16x8 pl = kEarly && i == 0 ? early_l : rows_fragment(p_lds, wm + 16 * i, 1);
 #pragma unroll
                 for (int j = 0; j < G::kNj; ++j) acc[i][j] = mfma(ql[j], ph, acc[i][j]);
 #pragma unroll
