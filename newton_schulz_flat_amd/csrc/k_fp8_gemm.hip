@@ -237,9 +237,9 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& ti
 // registers, by bytes at the end of a row.  Rows behind the last one read the last.
 // SQUARE: b's blocks are 128 x 128, and a wave's columns (64 or fewer, within 128) share one
 // scale.
-// What bounds it (8192 x 14336 over 4096 into bfloat16, 470 us, 2.05 PFLOP/s at 1.9 GHz): matrix
-// instructions are busy 44% of the cycles, the vector unit 41%, with little of one beside the other. Without
-// the scaling it takes 395 us, without the matrix instructions 313, without loads 395.
+// What bounds it (8192 x 14336 over 4096 into bfloat16, 460 us, 2.1 PFLOP/s at 1.9 GHz): matrix
+// instructions are busy 44% of the cycles, the vector unit 41%, with little of one beside the other. Of 470 us,
+// 395 were left without the scaling, 313 without the matrix instructions, 395 without loads.
 template <int TILE, bool DIRECT, int FA, int FB, bool EXACT, bool SQUARE>
 __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const ProductArgs g) {
     using G = Geo<TILE>;
@@ -347,7 +347,12 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
         for (int j = 0; j < G::kNj; ++j) acc[i][j] = {0.f, 0.f, 0.f, 0.f};
 
     int stage = 0, ahead = kStages - 1;
-    auto step = [&](int kb, auto set) {
+    // DEALT: a's and b's loads of the next block, a whole one, among the products: issued all at once
+    // they hold up the first of these (8192 x 14336 over 4096 484 us to 464, 600 x 2048 over 7168 25.3 to
+    // 24.6; of 256-tiles those with more registers at work lose 1 to 3%)
+    constexpr bool kDeals = DIRECT && kStages == 2 && (TILE == 128 || (SQUARE && !EXACT));
+    auto step = [&](int kb, auto set, auto dealt) {
+        constexpr bool kDealt = decltype(dealt)::value;
         if constexpr (DIRECT)
             wait_loads<(kStages - 2) * (2 * G::kLoads + 1)>();
         else
@@ -367,7 +372,9 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
         for (int j = 0; j < G::kNj; ++j) fb[j].set(fragment(lds[buf] + G::kOp, wn + 16 * j));
         // (behind these reads, not before them: 1 to 3% on every shape.)  With more than two stages
         // the last block is loaded once more at the end, so that as many loads are on their way
-        if constexpr (DIRECT && kStages > 2)
+        if constexpr (kDealt)
+            load4_to_lds(ps + (kb + 1) * ps_step, scales0 + ahead * G::kScales * 4 + wave * 256);
+        else if constexpr (DIRECT && kStages > 2)
             fetch(min(kb + kStages - 1, last - 1), ahead, set);
         else if (kb + (DIRECT ? 1 : G::kSets) < last)
             fetch(kb + (DIRECT ? 1 : G::kSets), ahead, set);
@@ -377,6 +384,20 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
             Wide<FA, EXACT> fa;
             fa.set(kEarly && i == 0 ? early : fragment(lds[buf], wm + 16 * i));
             const float sa = kEarly && i == 0 ? early_sa : scales[buf][wm + 16 * i + (lane & 15)];
+            if constexpr (kDealt) {
+                constexpr int kEach = 2 * G::kLoads / G::kMi;
+                static_assert(kEach * G::kMi == 2 * G::kLoads, "loads of a row of tiles");
+                const uint32_t to = lds0 + ahead * 2 * G::kOp + wave * 1024;
+                const int next = (kb + 1) * kFp8Block;
+#pragma unroll
+                for (int q = i * kEach; q < (i + 1) * kEach; ++q) {
+                    const int p = q / 2;
+                    if (q % 2 == 0)
+                        load16_to_lds(a_base + next, a_off[p], to + p * G::kThreads * 16);
+                    else
+                        load16_to_lds(b_base + next, b_off[p], to + G::kOp + p * G::kThreads * 16);
+                }
+            }
             // b's scales of single rows are read anew for every i: held, they cost the 256-tile
             // with widened codes 44 spilled registers and twice the time
             int at = TILE + wn + 4 * (lane >> 4);
@@ -413,11 +434,14 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
     }
     if constexpr (!DIRECT && G::kSets == 2) {
         for (int kb = first; kb < last; kb += 2) {
-            step(kb, Set0{});
-            if (kb + 1 < last) step(kb + 1, Set1{});
+            step(kb, Set0{}, std::false_type{});
+            if (kb + 1 < last) step(kb + 1, Set1{}, std::false_type{});
         }
     } else {
-        for (int kb = first; kb < last; ++kb) step(kb, Set0{});
+        int kb = first;
+        if constexpr (kDeals)
+            for (; kb + 1 < last && (kb + 2) * kFp8Block <= g.k; ++kb) step(kb, Set0{}, std::true_type{});
+        for (; kb < last; ++kb) step(kb, Set0{}, std::false_type{});
     }
     if constexpr (DIRECT && kStages > 2) wait_loads<0>();  // the repeated ones: LDS must be left alone
 #pragma unroll
