@@ -312,3 +312,38 @@ def test_another_stream_and_default_workspaces():
     for s in streams:
         torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# shorter side above 64 or too long for a workgroup's LDS, up to 128: strips; one and several parts
+SHORT = [(100, 700), (900, 40), (128, 128), (20, 5000)]
+
+
+@pytest.mark.parametrize("rows,cols", SHORT)
+@pytest.mark.parametrize("std", [1e-30, 1e-12, 1e15, 1e30])
+def test_short_sides_sizes_of_numbers(rows, cols, std):
+    test_sizes_of_numbers(rows, cols, std)
+
+
+@pytest.mark.parametrize("rows,cols", SHORT)
+def test_short_sides(rows, cols):
+    test_zero_matrices_and_low_rank(rows, cols)
+    for steps in (1, 2):
+        for bad in (float("nan"), float("inf")):
+            test_nan_and_infinity_stay_in_their_matrix(rows, cols, bad, steps)
+    test_groups_that_fit_the_workspace(rows, cols)
+    test_replayed(rows, cols)
+    test_coefficients_and_scale(rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", SHORT)
+def test_short_sides_within_larger_matrices(rows, cols):
+    """Views that start and step at odd elements of a bfloat16 tensor full of NaN elsewhere."""
+    say("short views", rows, cols)
+    base = torch.full((3, rows + 3, cols + 9), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x = base[:, 1:-2, 5:-4]
+    x.copy_(stack(3, rows, cols, seed=5))
+    held = torch.full((3, rows + 2, cols + 5), 7.0, dtype=torch.bfloat16, device="cuda")
+    nsf.muon_orthogonalize_stack(x, held[:, 1:-1, 3:-2])
+    check(x, held[:, 1:-1, 3:-2])
+    held[:, 1:-1, 3:-2] = 7.0
+    assert (held == 7.0).all()
