@@ -19,7 +19,9 @@
 // reduce over these 16 lanes (DPP), column blocks over the 16 threads of a column
 // group (lanes, then LDS).  Each block's divisions are made by one lane (of a row's 16, the
 // row's; of the workgroup, the column's) and handed round.  The transposed codes go through LDS
-// so that each row of the transpose leaves as 128 contiguous bytes.  It is an HBM stream.
+// so that each row of the transpose leaves as 128 contiguous bytes.  It is an HBM stream: 14336 x
+// 4096 float32 in 128 x 128 blocks, both ways, take 70 us (5.0 TB/s), one way 45 (6.5); 8192 x 4096 bfloat16
+// in rows, both ways, 28 (4.8).
 #include <type_traits>
 
 #include "fp8_internal.h"

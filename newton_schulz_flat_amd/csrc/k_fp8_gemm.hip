@@ -231,8 +231,8 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& ti
     ti = band * 4 + rest % high, tj = rest / high;
 }
 
-// One TILE x TILE tile of out over a range of blocks of k.  Row r's 16-byte chunk c lies at chunk c ^ (r / 2 mod 8), so that the fragment reads
-// of 16 rows meet every bank.  DIRECT (rows of codes that start at multiples of 16
+// One TILE x TILE tile of out over a range of blocks of k.  Row r's 16-byte chunk c lies at
+// chunk c ^ (r / 2 mod 8), so that the fragment reads of 16 rows meet every bank.  DIRECT (rows of codes that start at multiples of 16
 // bytes and hold a multiple of 16): loads go from memory to LDS directly; else through
 // registers, by bytes at the end of a row.  Rows behind the last one read the last.
 // SQUARE: b's blocks are 128 x 128, and a wave's columns (64 or fewer, within 128) share one
