@@ -95,12 +95,12 @@ __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
     const double norm = matrix_norm(a.partial + int64_t(matrix) * a.part_slots, a.parts);
     const float inv = inverse_of(norm);
     float top = first_bound(norm);
-    const float up = power_of_two(top < kStackSmallBound ? stack_exponent(top, 0) : a.plan.scales[0].sx);
+    const float up = stack_scaled(1.f, top < kStackSmallBound ? stack_exponent(top, kStackLeastX) : a.plan.scales[0].sx);
     if (t == 0 && threadIdx.x == 0) {
         StackScale* out = a.scales + int64_t(matrix) * kStackScales;
         if (top < kStackSmallBound) {
             for (int k = 0; k < a.plan.n; ++k) out[k] = stack_scale(a.plan.steps[k], top);
-            out[a.plan.n] = {int16_t(stack_exponent(top, 0)), 0, 0, 0};
+            out[a.plan.n] = {int16_t(stack_exponent(top, kStackLeastX)), 0, 0, 0};
         }
     }
     if (t == 0 && !(first_bound(norm) < kStackSmallBound) && int(threadIdx.x) <= a.plan.n)
@@ -185,8 +185,7 @@ __device__ __forceinline__ void place_of(int t, int tm, int tn, int& ti, int& tj
     }
 }
 
-// C (or O) = own * (the axpy's operand as stored) + down * (the sums), each with the exponents
-// of what it reads and of what is written; N rows of 16 x 16 tiles of each wave, from row i0 on.
+// C (or O) = own * (the axpy's operand as stored) + down * (the sums); N rows of 16 x 16 tiles of each wave, from row i0 on.
 template <int TILE, int STAGE, int N>
 __device__ __forceinline__ void finish(const ProductArgs& g, int matrix, int ti, int tj, int i0,
                                        const f32x4 (&acc)[N][Geo<TILE>::kNj]) {
@@ -195,16 +194,13 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int matrix, int ti,
     const int m0 = ti * TILE + (wave / (G::kWaves / 2)) * G::kWm, n0 = tj * TILE + (wave % (G::kWaves / 2)) * G::kWn;
     const int64_t x_at = int64_t(matrix) * g.rp * 2 * g.cp, a_at = int64_t(matrix) * g.rp * 2 * g.rp;
     const StackScale* ex = g.scales + int64_t(matrix) * kStackScales;
-    const int to = STAGE == kStageA ? ex[0].sa : STAGE == kStageB ? ex[0].sb : g.last ? 0 : ex[1].sx;
-    float down, own = 0.f;
-    if constexpr (STAGE == kStageA) {
-        down = power_of_two(to - 2 * ex[0].sx);
-    } else if constexpr (STAGE == kStageB) {
-        down = g.step.c * power_of_two(to - 2 * ex[0].sa), own = g.step.b * power_of_two(to - ex[0].sa);
-    } else {
-        down = power_of_two(to - ex[0].sx - ex[0].sb), own = g.step.a * power_of_two(to - ex[0].sx);
-        if (g.last) down *= g.scale, own *= g.scale;
-    }
+    StackFactors f = {0.f, 0.f, 1.f};
+    if constexpr (STAGE == kStageA)
+        f.down = stack_a_factor(ex[0]);
+    else if constexpr (STAGE == kStageB)
+        f = stack_b_factors(g.step, ex[0]);
+    else
+        f = stack_x_factors(g.step, ex[0], ex[1].sx, g.last, g.scale);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int m = m0 + 16 * (i0 + i) + (lane & 15);
@@ -214,16 +210,18 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int matrix, int ti,
             if (m >= g.rp || n >= (STAGE == kStageX ? g.cp : g.rp)) continue;
             float v[4];
 #pragma unroll
-            for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc[i][j][t4] * down;
+            for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc[i][j][t4] * f.down;
             if constexpr (STAGE != kStageA) {
                 const _Float16* w = (STAGE == kStageX ? g.x + x_at : g.a + a_at) + pair_at(m, n, g.rp);
                 const f16x4 hi = *reinterpret_cast<const f16x4*>(w);
                 const f16x4 lo = *reinterpret_cast<const f16x4*>(w + 32);
 #pragma unroll
-                for (int t4 = 0; t4 < 4; ++t4) v[t4] += own * (float(hi[t4]) + float(lo[t4]));
+                for (int t4 = 0; t4 < 4; ++t4) v[t4] += f.own * (float(hi[t4]) + float(lo[t4]));
             }
             if constexpr (STAGE == kStageX) {
                 if (g.last) {
+#pragma unroll
+                    for (int t4 = 0; t4 < 4; ++t4) v[t4] *= f.after;
                     if (g.out_bf16)
                         store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
                                      g.rows, g.cols, m, n, v);

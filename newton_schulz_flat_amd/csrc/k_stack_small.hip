@@ -140,8 +140,8 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
     const float inv = inverse_of(norm);
     float top = first_bound(norm);
     const bool small = top < kStackSmallBound;
-    int sx = small ? stack_exponent(top, 0) : g.plan.scales[0].sx;
-    const float up = power_of_two(sx);
+    int sx = small ? stack_exponent(top, kStackLeastX) : g.plan.scales[0].sx;
+    const float up = stack_scaled(1.f, sx);
 #pragma unroll 4
     for (int i = i0; i < g.rows; i += 16 * at_once)
 #pragma unroll 4
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
 #pragma unroll
                 for (int k = 0; k < kShare - 1; ++k) acc += sums_a[(tile * (kShare - 1) + k) * 64 + lane];
         }
-        const float down_a = power_of_two(s.sa - 2 * sx);
+        const float down_a = stack_a_factor(s);
         const auto put = [&](unsigned char* to) {
             const float v[4] = {acc.x, acc.y, acc.z, acc.w};
             put_quad(to, in_square, fi, fj, v);
@@ -186,21 +186,20 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
         __syncthreads();
         // B = b A + c A A, with this wave's tile of A still in registers
         if (share == 0) {
-            const float down_b = step.c * power_of_two(s.sb - 2 * s.sa), own_b = step.b * power_of_two(s.sb - s.sa);
+            const StackFactors fb = stack_b_factors(step, s);
             f32x4 aa = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks)
                 aa = product(rows_operand(a, in_square, fj * 16, ks, 0), rows_operand(a, in_square, fj * 16, ks, 1),
                              rows_operand(a, in_square, fi * 16, ks, 0), rows_operand(a, in_square, fi * 16, ks, 1), aa);
-            acc = acc * own_b + aa * down_b;
+            acc = acc * fb.own + aa * fb.down;
             put(b);
         }
         __syncthreads();
         // X <- a X + B X
         const bool last = t + 1 == g.plan.n;
-        const int next = small ? stack_exponent(top, 0) : g.plan.scales[t + 1].sx, to = last ? 0 : next;
-        float down_x = power_of_two(to - sx - s.sb), own_x = step.a * power_of_two(to - sx);
-        if (last) down_x *= g.scale, own_x *= g.scale;
+        const int next = small ? stack_exponent(top, kStackLeastX) : g.plan.scales[t + 1].sx;
+        const StackFactors fx = stack_x_factors(step, s, next, last, g.scale);
         const int xi = wave % kF, xm = xi * 16 + (lane & 15);
         f16x8 bh[kSteps], bl[kSteps];
 #pragma unroll
@@ -219,12 +218,14 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
                                 bl[ks], y);
                 get_quad(x, in_x, xi, xj, v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = own_x * v[e] + down_x * y[e];
+                for (int e = 0; e < 4; ++e) v[e] = fx.own * v[e] + fx.down * y[e];
             }
             if (!last) {
                 __syncthreads();
                 if (col < g.cp) put_quad(x, in_x, xi, xj, v);
             } else if (col < g.cp) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= fx.after;
                 if (w.out_bf16)
                     store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, w.tall, g.rows,
                                  g.cols, xm, n, v);
@@ -293,14 +294,14 @@ struct Poly {
 #pragma unroll
             for (int q = 0; q < kMine; ++q) acc[q] += from[p * (RP * RP / 4) + q * 64];
         const Place in_a(kRow);
-        const float down_a = power_of_two(s.sa - 2 * s.sx);
+        const float down_a = stack_a_factor(s);
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
             acc[q] *= down_a;
             put(a, in_a, q, acc[q]);
         }
         __syncthreads();
-        const float down = g.step.c * power_of_two(s.sb - 2 * s.sa), own = g.step.b * power_of_two(s.sb - s.sa);
+        const StackFactors f = stack_b_factors(g.step, s);
 #pragma unroll
         for (int q = 0; q < kMine; ++q) b[q] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -314,7 +315,7 @@ struct Poly {
 #pragma unroll
         for (int q = 0; q < kMine; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[q][e] = __builtin_fmaf(acc[q][e], own, b[q][e] * down);
+            for (int e = 0; e < 4; ++e) b[q][e] = __builtin_fmaf(acc[q][e], f.own, b[q][e] * f.down);
     }
     __device__ __forceinline__ void put(unsigned char* m, const Place& place, int q, const f32x4& t) const {
         const float v[4] = {t.x, t.y, t.z, t.w};
@@ -439,7 +440,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
         inv = inverse_of(norm);
         float top = first_bound(norm);
         const bool small = top < kStackSmallBound;
-        up = power_of_two(small ? stack_exponent(top, 0) : g.in.plan.scales[0].sx);
+        up = stack_scaled(1.f, small ? stack_exponent(top, kStackLeastX) : g.in.plan.scales[0].sx);
         if (FIRST && part == 0) {
             // the matrix's exponents
             StackScale* ex = g.in.scales + int64_t(matrix) * kStackScales;
@@ -447,19 +448,17 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
                 if (tid <= g.in.plan.n) ex[tid] = g.in.plan.scales[tid];
             } else if (tid == 0) {
                 for (int k = 0; k < g.in.plan.n; ++k) ex[k] = stack_scale(g.in.plan.steps[k], top);
-                ex[g.in.plan.n] = {int16_t(stack_exponent(top, 0)), 0, 0, 0};
+                ex[g.in.plan.n] = {int16_t(stack_exponent(top, kStackLeastX)), 0, 0, 0};
             }
         }
     }
     StackScale s{};
-    float down = 0.f, own = 0.f;
+    StackFactors f = {0.f, 0.f, 1.f};
     f16x8 bh[G::kSteps], bl[G::kSteps];
     if constexpr (!FIRST) {
         const StackScale* ex = g.scales + int64_t(matrix) * kStackScales;
         s = ex[0];
-        const int to = g.last ? 0 : ex[1].sx;
-        down = power_of_two(to - s.sx - s.sb), own = g.step.a * power_of_two(to - s.sx);
-        if (g.last) down *= g.scale, own *= g.scale;
+        f = stack_x_factors(g.step, s, ex[1].sx, g.last, g.scale);
     }
     if constexpr (MODE == kStep) {
         const f16x8* b = reinterpret_cast<const f16x8*>(g.b) + int64_t(matrix) * RP * RP / 4;
@@ -524,8 +523,10 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
                 const int col = (wc * 2 + j) * 16;
                 get_quad(m, in_strip, wr, wc * 2 + j, v[j]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(own, v[j][e], down * y[j][e]);
+                for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(f.own, v[j][e], f.down * y[j][e]);
                 if (g.last) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[j][e] *= f.after;
                     if (g.out_bf16)
                         store_result(static_cast<uint16_t*>(g.out) + matrix * g.out_stride, g.out_row, g.tall,
                                      g.rows, g.cols, row, strip * 64 + col + 4 * (lane >> 4), v[j]);

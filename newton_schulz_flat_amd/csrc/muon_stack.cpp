@@ -136,7 +136,7 @@ int plan_steps(const float* k, int n, StackPlan* plan, Status* st) {
             return fail(st, MUON_ERR_BAD_ARG,
                         "coefficients of step %d let singular values grow beyond 2^24", t);
     }
-    plan->scales[n] = {int16_t(stack_exponent(top, 0)), 0, 0, 0};
+    plan->scales[n] = {int16_t(stack_exponent(top, kStackLeastX)), 0, 0, 0};
     return MUON_OK;
 }
 

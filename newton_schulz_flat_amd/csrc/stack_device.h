@@ -27,11 +27,6 @@ __device__ __forceinline__ Pair split(float v) {
     const _Float16 hi = static_cast<_Float16>(v);
     return {hi, static_cast<_Float16>(v - static_cast<float>(hi))};
 }
-// 2^e for e <= 127; 0 below 2^-126, where what it multiplies is lost beside its sum's other term.
-__device__ __forceinline__ float power_of_two(int e) {
-    return e < -126 ? 0.f : __uint_as_float(uint32_t(127 + e) << 23);
-}
-
 // Element (i, j) of a matrix of pairs with rp rows (padded): its high half; the low one lies 32
 // further on.  Blocks of 32 columns lie one behind the other, each rp rows of 128 bytes: a K step of
 // a tile is one contiguous piece, whatever the matrix's width.  (Row after row, a K step of a tile

@@ -27,9 +27,10 @@ struct StackScale {
 };
 
 // The exponent that brings magnitudes of up to `top` to at most 2^15, half of
-// float16's range.  Below 2^-240 (an X of 2^-120) it stays where it is.
-__host__ __device__ inline int stack_exponent(float top, int square) {
-    const int least = square ? -240 : -120;
+// float16's range.  For a `top` below 2^least it is that of 2^least: an X is scaled by 2^127 at most,
+// a float32, which gives the smallest one (2^-126, of a U of the smallest subnormal number) all its digits.
+constexpr int kStackLeastX = -112, kStackLeastPoly = -120;
+__host__ __device__ inline int stack_exponent(float top, int least) {
     int e = least;
     if (top > 0.f) {
         const uint32_t bits = __builtin_bit_cast(uint32_t, top);
@@ -37,6 +38,10 @@ __host__ __device__ inline int stack_exponent(float top, int square) {
     }
     return 15 - (e > least ? e : least);
 }
+
+// v 2^e, for any e: exponents of factors leave float32's range (down to -500) where the product does not, or
+// where it is lost beside its sum's other term.
+__host__ __device__ inline float stack_scaled(float v, int e) { return __builtin_ldexpf(v, e); }
 
 // The largest |a x + b x^3 + c x^5| on [0, top]: at an end or where the derivative
 // a + 3 b y + 5 c y^2, y = x^2, is zero.
@@ -64,11 +69,34 @@ __host__ __device__ inline float stack_largest(const StackStep& k, float top) {
 // bound included, add a part in a thousand at most.  The largest entry of A is at most top^2; where
 // that leaves float32's range the exponent follows from top's.
 __host__ __device__ inline StackScale stack_scale(const StackStep& k, float& top) {
-    const int sx = stack_exponent(top, 0), sa = 2 * sx - 15;
+    const int sx = stack_exponent(top, kStackLeastX), sa = 2 * sx - 15;
     const float gram = top * top, poly = fabsf(k.b) + fabsf(k.c) * gram;
-    const StackScale s = {int16_t(sx), int16_t(sa), int16_t(sa - (15 - stack_exponent(poly, 0))), 0};
+    const StackScale s = {int16_t(sx), int16_t(sa), int16_t(sa - (15 - stack_exponent(poly, kStackLeastPoly))), 0};
     top = 1.001f * stack_largest(k, top);
     return s;
+}
+
+// What a stage's sums (down) and the matrix that is added to them (own) are multiplied by, each with
+// the exponents of what it reads and of what is written; x_factors: the result once more, by after.
+struct StackFactors {
+    float own, down, after;
+};
+__host__ __device__ inline float stack_a_factor(const StackScale& s) { return stack_scaled(1.f, s.sa - 2 * s.sx); }
+__host__ __device__ inline StackFactors stack_b_factors(const StackStep& k, const StackScale& s) {
+    return {stack_scaled(k.b, s.sb - s.sa), stack_scaled(k.c, s.sb - 2 * s.sa), 1.f};
+}
+// `next`: the next X's exponent.  Results of the last step are those of the call, times `scale`; where X
+// is small, 2^64 of its 2^-sx waits for the end, so that own and down, which are rounded, stay normal numbers.
+__host__ __device__ inline StackFactors stack_x_factors(const StackStep& k, const StackScale& s, int next, bool last,
+                                                        float scale) {
+    const bool late = last && s.sx > 32;
+    const int to = late ? 64 : last ? 0 : next;
+    StackFactors f = {stack_scaled(k.a, to - s.sx), stack_scaled(1.f, to - s.sx - s.sb), 1.f};
+    if (late)
+        f.after = stack_scaled(scale, -64);
+    else if (last)
+        f.own *= scale, f.down *= scale;
+    return f;
 }
 
 // The shape as the iteration sees it: r <= c, sides padded to whole blocks.

@@ -347,3 +347,41 @@ def test_short_sides_within_larger_matrices(rows, cols):
     check(x, held[:, 1:-1, 3:-2])
     held[:, 1:-1, 3:-2] = 7.0
     assert (held == 7.0).all()
+
+
+# --------------------------------------------------------------- numbers at the ends of float32
+
+# one workgroup a matrix, strips, tiles of 64 with shared K steps
+@pytest.mark.parametrize("rows,cols", [(24, 60), (100, 700), (700, 90), (200, 150)])
+@pytest.mark.parametrize("norm", [1.4e-45, 1e-44, 1e-42, 7e-42, 1e-41, 1e-38])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_subnormal_matrices(rows, cols, norm, out):
+    """Matrices whose norm is far below 1e-7: every step multiplies by its first coefficient
+    (b X^3 is 2^-200 of that).  Roundings, half steps of 2^-24: the norm's reciprocal, its product with U,
+    a float16 pair (2), for each of five steps a product and, but for the last, a pair, the scale, its product.
+    A pair is also off by half of the smallest float16, 2^-25, where the norm's bound, at most 1.01 times the norm,
+    lies between 2^14 and 2^15: 2^-39 of the norm for each of five pairs (where the bound is below 2^-112 and
+    the norm therefore stored below 2^14, no number but 0 is below 2, and 2^-25 is less than the first kind)."""
+    say("subnormal", rows, cols, norm, out)
+    g = torch.Generator().manual_seed(rows)
+    u = torch.randn(2, rows, cols, generator=g, dtype=torch.float64)
+    if norm < 1e-42:
+        u[:, 3:], u[:, :, 4:] = 0, 0
+    if norm < 1e-44:
+        u[:, :, 1:], u[:, 1:] = 0, 0
+    u *= norm / torch.linalg.norm(u, dim=(1, 2), keepdim=True)
+    x = u.float().cuda()
+    assert (x != 0).any()
+    u = x.double().cpu().numpy()
+    inverse = 1 / (np.sqrt((u * u).sum(axis=(1, 2), keepdims=True)) + 1e-7)
+    for steps, scale in ((nsf.QUINTIC, None), (POLISHED, -0.25), ([], 3.0)):
+        o = torch.empty(2, rows, cols, dtype=DT[out], device="cuda")
+        nsf.muon_orthogonalize_stack(x, o, coefficients=steps, scale=scale)
+        want = u * inverse * (max(1.0, rows / cols) ** 0.5 if scale is None else scale)
+        for a, _, _ in steps:
+            want = want * float(np.float32(a))
+        tol = 20 * 2.0 ** -24 + (2.0 ** -8 if out == "bf16" else 0)
+        err = np.abs(o.double().cpu().numpy() - want)
+        pairs = 5 * 1.01 * 2.0 ** -39 * np.sqrt((want * want).sum(axis=(1, 2), keepdims=True))
+        # (a bfloat16 result below 2^-126 is off by half of 2^-133)
+        assert (err <= tol * np.abs(want) + pairs + 2.0 ** -134).all(), (err / (np.abs(want) + 1e-300)).max()
