@@ -44,24 +44,23 @@ __host__ __device__ inline int stack_exponent(float top, int least) {
 __host__ __device__ inline float stack_scaled(float v, int e) { return __builtin_ldexpf(v, e); }
 
 // The largest |a x + b x^3 + c x^5| on [0, top]: at an end or where the derivative
-// a + 3 b y + 5 c y^2, y = x^2, is zero.
+// a + 3 b x^2 + 5 c x^4 is zero.  Worked out for x = top sqrt(z), z up to 1, and coefficients of at most 1, so
+// that nothing leaves float32's range that the result does not; the roots without a difference of
+// numbers that may be alike (where c is small beside b, one of them).
 __host__ __device__ inline float stack_largest(const StackStep& k, float top) {
-    const float a = k.a, b = k.b, c = k.c;
-    const auto value = [&](float x) { return fabsf(x * (a + x * x * (b + c * x * x))); };
-    float most = value(top);
-    const auto at = [&](float y) {
-        if (y > 0.f && y < top * top) most = fmaxf(most, value(sqrtf(y)));
-    };
-    if (c == 0.f) {
-        if (b != 0.f) at(-a / (3.f * b));
-    } else {
-        const float d = 9.f * b * b - 20.f * a * c;
-        if (d >= 0.f) {
-            at((-3.f * b + sqrtf(d)) / (10.f * c));
-            at((-3.f * b - sqrtf(d)) / (10.f * c));
-        }
+    float a = k.a, b = k.b * top * top, c = k.c * top * top * top * top;
+    const float most_of = fmaxf(fabsf(a), fmaxf(fabsf(b), fabsf(c)));
+    if (!(most_of > 0.f)) return 0.f;
+    a /= most_of, b /= most_of, c /= most_of;
+    const auto value = [&](float z) { return fabsf(sqrtf(z) * (a + z * (b + c * z))); };
+    float most = value(1.f);
+    const float d = 9.f * b * b - 20.f * a * c;
+    if (d >= 0.f) {
+        const float q = -0.5f * (3.f * b + copysignf(sqrtf(d), b));
+        for (float z : {q / (5.f * c), a / q})  // (c = 0: one of them infinite, or no number)
+            if (z > 0.f && z < 1.f) most = fmaxf(most, value(z));
     }
-    return most;
+    return most * most_of * top;
 }
 
 // One step: the exponents of its matrices where the largest singular value (and with it every

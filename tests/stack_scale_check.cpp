@@ -54,9 +54,32 @@ void run(const std::vector<StackStep>& steps, float x, float top, float scale) {
     }
 }
 
+// The bound of a step's results against the largest of them on a fine grid.
+void bound(const StackStep& k, float top) {
+    double most = 0;
+    for (int i = 1; i <= 4000; ++i) {
+        const double x = double(top) * i / 4000;
+        most = std::fmax(most, std::fabs(x * (k.a + x * x * (k.b + x * x * double(k.c)))));
+    }
+    const double got = stack_largest(k, top);
+    if (!(got >= most * (1 - 1e-5) - 1e-44) || !(got <= most * (1 + 1e-4) + 1e-44)) fail("a bound", top, 0, got, most);
+    ++g_checked;
+}
+
 }  // namespace
 
 int main() {
+    for (const StackStep& k : std::initializer_list<StackStep>{
+             {3.4445f, -4.7750f, 2.0315f}, {8.f, -22.f, 15.f}, {30.f, -29.f, 0.f}, {1.f, 0.f, 0.f}, {0.f, 1.f, 0.f},
+             {0.f, 0.f, -1.f}, {0.f, -2.f, 1.f}, {3.f, -3.f, 1e-8f}, {3.f, -3.f, -1e-8f}, {3.f, -3.f, 1e-3f},
+             {1e-7f, -3.f, 3.f}, {-1e-7f, 3.f, -3.f}, {5.f, -20.f, 16.f}, {-5.f, 20.f, -16.f}, {1.f, -1.f, 1e-20f}})
+        // the same polynomial on other intervals, and of other sizes
+        for (float top : {1.001f, 1e-3f, 1e-9f, 4e-10f, 300.f})
+            for (float size : {1.f, 1e-25f, 1e-33f, 1e4f}) {
+                const double t = top, s = size;
+                const StackStep scaled{float(k.a * s), float(k.b * s / (t * t)), float(k.c * s / (t * t * t * t))};
+                if (std::isfinite(scaled.a) && std::isfinite(scaled.b) && std::isfinite(scaled.c)) bound(scaled, top);
+            }
     const StackStep quintic{3.4445f, -4.7750f, 2.0315f};
     const std::vector<std::vector<StackStep>> lists = {
         {quintic},
@@ -69,6 +92,9 @@ int main() {
         {{1000.f, 0.f, 0.f}, {1e-40f, 0.f, 0.f}, {1.f, 0.f, 0.f}},
         // the iterate shrunk and grown again
         {{1e-5f, 0.f, 0.f}, {1e5f, 0.f, 0.f}, quintic},
+        // an end where the polynomial is nearly zero, with a small last coefficient; coefficients for a shrunk iterate
+        {{2.598f, -2.598f, 1e-8f}, {1.5f, -0.5f, 0.f}},
+        {{1e-9f, 0.f, 0.f}, {5.f, -20e18f, 16e36f}, quintic},
     };
     for (const auto& steps : lists)
         for (float scale : {1.f, -0.2f, 1e-3f, 1e6f})

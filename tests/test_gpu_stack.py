@@ -385,3 +385,16 @@ def test_subnormal_matrices(rows, cols, norm, out):
         pairs = 5 * 1.01 * 2.0 ** -39 * np.sqrt((want * want).sum(axis=(1, 2), keepdims=True))
         # (a bfloat16 result below 2^-126 is off by half of 2^-133)
         assert (err <= tol * np.abs(want) + pairs + 2.0 ** -134).all(), (err / (np.abs(want) + 1e-300)).max()
+
+
+@pytest.mark.parametrize("rows,cols", [(24, 60), (100, 700), (200, 150)])
+def test_coefficients_of_unlike_sizes(rows, cols):
+    """Polynomials that are nearly zero at the end of their interval, with a last coefficient far
+    below the others, and coefficients for an iterate that was shrunk before."""
+    x = stack(2, rows, cols, seed=12)
+    for steps in ([(2.598, -2.598, 1e-8), (1.5, -0.5, 0.0)], [(2.598, -2.598, -1e-8)] + POLISHED,
+                  [(1e-9, 0.0, 0.0), (5.0, -20e18, 16e36)] + POLISHED):
+        say("unlike", rows, cols, steps)
+        out = torch.empty_like(x)
+        nsf.muon_orthogonalize_stack(x, out, coefficients=steps)
+        check(x, out, steps)
