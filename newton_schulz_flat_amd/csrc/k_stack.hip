@@ -95,7 +95,8 @@ __global__ __launch_bounds__(256) void stack_split_kernel(const InArgs a) {
     const double norm = matrix_norm(a.partial + int64_t(matrix) * a.part_slots, a.parts);
     const float inv = inverse_of(norm);
     float top = first_bound(norm);
-    const float up = stack_scaled(1.f, top < kStackSmallBound ? stack_exponent(top, kStackLeastX) : a.plan.scales[0].sx);
+    const int sx = top < kStackSmallBound ? stack_exponent(top, kStackLeastX) : a.plan.scales[0].sx;
+    const float up = stack_scaled(1.f, sx - kInverseUp);
     if (t == 0 && threadIdx.x == 0) {
         StackScale* out = a.scales + int64_t(matrix) * kStackScales;
         if (top < kStackSmallBound) {
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(256) void stack_scaled_kernel(const InArgs a) {
     for (uint64_t e = uint64_t(part) * 256 + threadIdx.x; e < numel; e += uint64_t(a.parts) * 256) {
         const uint32_t i = uint32_t(e) / uint32_t(a.cols), j = uint32_t(e) - i * uint32_t(a.cols);
         store_one(o + int64_t(i) * a.out_row + j,
-                  load_one(u + int64_t(i) * a.in_row + j) * inv * a.scale);
+                  stack_scaled(load_one(u + int64_t(i) * a.in_row + j) * inv, -kInverseUp) * a.scale);
     }
 }
 

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kWholeThreads) void stack_whole_kernel(const WholeA
     float top = first_bound(norm);
     const bool small = top < kStackSmallBound;
     int sx = small ? stack_exponent(top, kStackLeastX) : g.plan.scales[0].sx;
-    const float up = stack_scaled(1.f, sx);
+    const float up = stack_scaled(1.f, sx - kInverseUp);
 #pragma unroll 4
     for (int i = i0; i < g.rows; i += 16 * at_once)
 #pragma unroll 4
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(StripGeo<RP>::kThreads) void stack_strip_kernel(con
         inv = inverse_of(norm);
         float top = first_bound(norm);
         const bool small = top < kStackSmallBound;
-        up = stack_scaled(1.f, small ? stack_exponent(top, kStackLeastX) : g.in.plan.scales[0].sx);
+        up = stack_scaled(1.f, (small ? stack_exponent(top, kStackLeastX) : g.in.plan.scales[0].sx) - kInverseUp);
         if (FIRST && part == 0) {
             // the matrix's exponents
             StackScale* ex = g.in.scales + int64_t(matrix) * kStackScales;

@@ -126,9 +126,12 @@ __device__ __forceinline__ double matrix_norm(const double* partial, int parts) 
     for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     return sqrt(sum);
 }
-// 1 / (||U|| + 1e-7); an infinite norm makes the whole matrix NaN, like a NaN does.
+// 2^64 / (||U|| + 1e-7): without the 2^64, norms above 2^126 (of finite matrices) would make it a
+// subnormal number and cost its digits.  U times it is 2^64 at most.  An infinite norm makes the whole
+// matrix NaN, like a NaN does.
+constexpr int kInverseUp = 64;
 __device__ __forceinline__ float inverse_of(double norm) {
-    return norm > 1.7e308 ? __uint_as_float(0x7fc00000u) : float(1. / (norm + 1e-7));
+    return norm > 1.7e308 ? __uint_as_float(0x7fc00000u) : float(0x1p64 / (norm + 1e-7));
 }
 // The bound on the largest singular value of U / (||U|| + 1e-7) (a NaN: any will do).
 __device__ __forceinline__ float first_bound(double norm) {

@@ -398,3 +398,27 @@ def test_coefficients_of_unlike_sizes(rows, cols):
         out = torch.empty_like(x)
         nsf.muon_orthogonalize_stack(x, out, coefficients=steps)
         check(x, out, steps)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(2, 64, 400), (2, 128, 2000), (1, 3000, 100), (1, 1024, 1000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_finite_matrices(count, rows, cols, dtype):
+    """Entries near float32's largest number: a norm whose reciprocal is no normal float32.
+    Without steps an element takes four roundings: the reciprocal, two products, the scale."""
+    say("largest", count, rows, cols, dtype)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = 3.3e38 * (0.5 + 0.5 * torch.rand(count, rows, cols, generator=g, device="cuda"))
+    x = (x * (torch.randint(0, 2, x.shape, generator=g, device="cuda") * 2 - 1)).to(DT[dtype])
+    assert torch.isfinite(x).all()
+    scale = max(1.0, rows / cols) ** 0.5
+    o = torch.empty(count, rows, cols, device="cuda")
+    for steps in ((), nsf.QUINTIC):
+        nsf.muon_orthogonalize_stack(x, o, coefficients=steps)
+        for k in range(count):
+            want = reference(x[k], steps) * scale
+            err = (o[k].double() - want).abs()
+            if not steps:
+                assert (err <= 4 * 2.0 ** -24 * want.abs()).all()
+            else:
+                tol = 2e-6 + 8 * torch.linalg.norm(reference(x[k], steps, 22) * scale - want) / torch.linalg.norm(want)
+                assert torch.linalg.norm(err) <= tol * torch.linalg.norm(want)
