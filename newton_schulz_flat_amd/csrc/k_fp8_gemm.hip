@@ -129,6 +129,28 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) {
     return {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 }
 
+// A sum is multiplied by the product p of its two scales.  p leaves float32's normal numbers where both
+// scales are very small or very large, which the result, the sum times both, need not do; such elements
+// take the scales by parts.  Two multiplications a sum would do for most of them, but not all, and the
+// vector unit is half of what bounds a tile: instead a tile looks at its scales as they pass (8192 x 14336
+// over 4096 into bfloat16 within 1%, into float32 801 us to 819) and is made again where it has to be.
+__device__ __forceinline__ bool is_normal(float p) { return __builtin_amdgcn_classf(p, 0x108); }
+// A scale's mantissa (0.5 to 1; a zero, an infinity or a NaN itself) and exponent.
+struct Parts {
+    float mantissa;
+    int exponent;
+    __device__ __forceinline__ explicit Parts(float s)
+        : mantissa(__builtin_amdgcn_frexp_mantf(s)), exponent(__builtin_amdgcn_frexp_expf(s)) {}
+};
+// acc + sum * a's scale * b's: the same bits as sum * p + acc where p is a normal number, else rounded
+// once more.  (A sum of zero stays away from an infinite product of finite scales.)
+__device__ __forceinline__ float add_by_parts(float acc, float sum, float sa, float sb) {
+    const float p = sb * sa;
+    if (is_normal(p)) return __builtin_fmaf(sum, p, acc);
+    const Parts a(sa), b(sb);
+    return acc + __builtin_ldexpf(sum * (a.mantissa * b.mantissa), a.exponent + b.exponent);
+}
+
 // Four neighbouring results of row i, from column j on; of one split of k where there are several.
 __device__ __forceinline__ void store_result(const ProductArgs& g, int split, int i, int j, f32x4 v) {
     if (i >= g.a.rows || j >= g.b.rows) return;
@@ -231,6 +253,76 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& ti
     ti = band * 4 + rest % high, tj = rest / high;
 }
 
+// Scales from 2^-63 to 2^63, of which no product of two leaves the normal numbers.
+__device__ __forceinline__ bool is_plain(float scale) {
+    return (__float_as_uint(scale) << 1) - (64u << 24) < (126u << 24);
+}
+// The least (but zeros) and the largest finite one of the scales of a row.
+struct Sizes {
+    uint32_t least = (255u << 23) - 1, most = 0;  // bits; least: less one, so that zeros are the largest
+    __device__ __forceinline__ void meet(float scale) {
+        const uint32_t bits = __float_as_uint(scale) & 0x7fffffffu;
+        least = min(least, bits - 1), most = max(most, bits < 255u << 23 ? bits : 0u);
+    }
+};
+// No product of a scale of a and one of b leaves the normal numbers, by the sizes of a tile's scales: the
+// first half of every `rows` threads has those of a's rows.  The same in all threads.
+template <int WAVES>
+__device__ __forceinline__ bool products_are_normal(const Sizes& s, uint2* met, int rows) {
+    uint32_t least = s.least, most = s.most;
+    for (int d = 32; d > 0; d >>= 1) {
+        least = min(least, uint32_t(__shfl_xor(int(least), d)));
+        most = max(most, uint32_t(__shfl_xor(int(most), d)));
+    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if ((threadIdx.x & 63) == 0) met[wave] = {least, most};
+    __syncthreads();
+    uint2 a = {(255u << 23) - 1, 0}, b = a;
+    for (int w = 0; w < WAVES; ++w) {
+        uint2& o = (w * 64 & (rows - 1)) < rows / 2 ? a : b;
+        o.x = min(o.x, met[w].x), o.y = max(o.y, met[w].y);
+    }
+    __syncthreads();
+    const float low = __uint_as_float(a.x + 1) * __uint_as_float(b.x + 1);
+    const float high = __uint_as_float(a.y) * __uint_as_float(b.y);
+    return __builtin_amdgcn_ballot_w64(!(low >= 0x1p-126f && high <= 3.4028235e38f)) == 0;
+}
+
+// A wave's MI x NJ tiles of 16 x 16 with their scales by parts, from row m0 of a and n0 of b on, one after the
+// other and straight from memory: what a tile is made of again where products of its scales leave the normal
+// numbers.  Rolled, and a tile at a time: what it holds, the main loop cannot.  It is 10 to 20 times slower
+// (8192 x 14336 over 4096 with all scales near 2^-70: 11 ms), for products that are otherwise lost.
+template <int MI, int NJ, int FA, int FB, bool EXACT>
+__device__ __forceinline__ void tiles_by_parts(const ProductArgs& g, int split, int m0, int n0, int first, int last) {
+    const int lane = threadIdx.x & 63, q = lane >> 4;
+#pragma unroll 1
+    for (int tile = 0; tile < MI * NJ; ++tile) {
+        const int m = m0 + tile / NJ * 16, n = n0 + tile % NJ * 16;
+        const int ar = min(m + (lane & 15), g.a.rows - 1), br = min(n + (lane & 15), g.b.rows - 1);
+        const uint8_t* pa = g.a.codes + int64_t(ar) * g.a.row_stride;
+        const uint8_t* pb = g.b.codes + int64_t(br) * g.b.row_stride;
+        const float* sa = g.a.scales + int64_t(ar >> g.a.shift) * g.a.scale_row;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int kb = first; kb < last; ++kb) {
+            const int at = kb * kFp8Block + q * 16;
+            Wide<FA, EXACT> wa;
+            Wide<FB, EXACT> wb;
+            wa.set(join(load_chunk(pa, at, g.k), load_chunk(pa, at + 64, g.k)));
+            wb.set(join(load_chunk(pb, at, g.k), load_chunk(pb, at + 64, g.k)));
+            f32x4 sum;
+            block_products<1>(&wb, wa, &sum);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int r = min(n + 4 * q + t, g.b.rows - 1) >> g.b.shift;
+                acc[t] = add_by_parts(acc[t], sum[t], sa[kb * g.a.scale_col],
+                                      g.b.scales[int64_t(r) * g.b.scale_row + kb * g.b.scale_col]);
+            }
+        }
+        store_result(g, split, m + (lane & 15), n + 4 * q, acc);
+    }
+}
+
 // One TILE x TILE tile of out over a range of blocks of k.  Row r's 16-byte chunk c lies at
 // chunk c ^ (r / 2 mod 8), so that the fragment reads of 16 rows meet every bank.  DIRECT (rows of codes that start at multiples of 16
 // bytes and hold a multiple of 16): loads go from memory to LDS directly; else through
@@ -246,6 +338,8 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
     constexpr int kStages = DIRECT ? G::kStages : 2;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kStages][2 * G::kOp];
     __shared__ __attribute__((aligned(16))) float scales[kStages][G::kScales];
+    __shared__ int not_plain[G::kWaves];
+    __shared__ uint2 met[G::kWaves];
     const int tiles = g.tiles_m * g.tiles_n;
     const int split = blockIdx.x / tiles;
     int ti, tj;
@@ -322,6 +416,7 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
             rs[kSet] = ps[kb * ps_step];
         }
     };
+    uint64_t others = 0;  // lanes that met scales that are not plain
     auto put = [&](int to_stage, auto set) {
         if constexpr (!DIRECT) {
             constexpr int kSet = decltype(set)::value;
@@ -332,6 +427,7 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
                 *reinterpret_cast<i32x4*>(&lds[to_stage][G::kOp + at]) = rb[kSet][p];
             }
             scales[to_stage][tid] = rs[kSet];
+            others |= __builtin_amdgcn_ballot_w64(!is_plain(rs[kSet]));
         }
     };
     auto fragment = [&](const unsigned char* op, int row0) {
@@ -420,6 +516,7 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
                 }
             }
         }
+        if constexpr (DIRECT) others |= __builtin_amdgcn_ballot_w64(!is_plain(scales[buf][tid & (2 * TILE - 1)]));
         stage = stage + 1 == kStages ? 0 : stage + 1;
         ahead = ahead + 1 == kStages ? 0 : ahead + 1;
     };
@@ -444,6 +541,40 @@ __global__ __launch_bounds__(Geo<TILE>::kThreads, 2) void fp8_tile_kernel(const 
         for (; kb < last; ++kb) step(kb, Set0{}, std::false_type{});
     }
     if constexpr (DIRECT && kStages > 2) wait_loads<0>();  // the repeated ones: LDS must be left alone
+    if (lane == 0) not_plain[wave] = others != 0;
+    __syncthreads();
+    if (__builtin_amdgcn_ballot_w64(lane < G::kWaves && not_plain[lane & (G::kWaves - 1)]) != 0) {
+        // (a gradient's rows may be that small, without any product of their scales being so)
+        Sizes all;
+#pragma unroll 4
+        for (int kb = first; kb < last; ++kb) all.meet(ps[kb * ps_step]);
+        bool normal = products_are_normal<G::kWaves>(all, met, 2 * TILE);
+        if (!normal) {
+            // blocks of zeros have scales near 2^-109, but their sums are zero too, and zero times a
+            // small product is right: without them
+            const int t = tid & (2 * TILE - 1);
+            const Operand& o = t < TILE ? g.a : g.b;
+            const int r = min((t < TILE ? m0 : n0) + (t & (TILE - 1)), o.rows - 1);
+            const uint8_t* row = o.codes + int64_t(r) * o.row_stride;
+            Sizes nonzero;
+#pragma unroll 1
+            for (int kb = first; kb < last; ++kb) {
+                const float scale = ps[kb * ps_step];
+                if (fabsf(scale) < 0x1p-63f) {
+                    i32x4 any = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int c = 0; c < kFp8Block; c += 16) any |= load_chunk(row, kb * kFp8Block + c, g.k);
+                    if (((any.x | any.y | any.z | any.w) & 0x7f7f7f7f) == 0) continue;
+                }
+                nonzero.meet(scale);
+            }
+            normal = products_are_normal<G::kWaves>(nonzero, met, 2 * TILE);
+        }
+        if (!normal) {
+            tiles_by_parts<G::kMi, G::kNj, FA, FB, EXACT>(g, split, m0 + wm, n0 + wn, first, last);
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < G::kMi; ++i)
 #pragma unroll
@@ -485,7 +616,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp8_few_kernel(const ProductAr
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int kb0 = first + wave; kb0 < last; kb0 += kFewWaves * kFewAhead) {
         i32x8 fb[kFewAhead], fa[kFewAhead];
-        f32x4 scale[kFewAhead];
+        float sa_at[kFewAhead], sb_at[kFewAhead][SQUARE ? 1 : 4];
 #pragma unroll
         for (int u = 0; u < kFewAhead; ++u) {
             const int kb = kb0 + u * kFewWaves;
@@ -493,9 +624,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp8_few_kernel(const ProductAr
             const int at = kb * kFp8Block + q * 16;
             fb[u] = join(load_chunk(pb, at, g.k), load_chunk(pb, at + 64, g.k));
             fa[u] = join(load_chunk(pa, at, g.k), load_chunk(pa, at + 64, g.k));
-            const float s = sa[kb * g.a.scale_col];
+            sa_at[u] = sa[kb * g.a.scale_col];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) scale[u][t] = s * sb[SQUARE ? 0 : t][kb * g.b.scale_col];
+            for (int t = 0; t < (SQUARE ? 1 : 4); ++t) sb_at[u][t] = sb[t][kb * g.b.scale_col];
         }
 #pragma unroll
         for (int u = 0; u < kFewAhead; ++u) {
@@ -505,7 +636,19 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp8_few_kernel(const ProductAr
             wb.set(fb[u]), wa.set(fa[u]);
             f32x4 sum;
             block_products<1>(&wb, wa, &sum);
-            acc += sum * scale[u];
+            f32x4 scale;
+            bool plain = true;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                scale[t] = sa_at[u] * sb_at[u][SQUARE ? 0 : t];
+                plain &= is_normal(scale[t]);
+            }
+            if (__builtin_amdgcn_ballot_w64(!plain) == 0)
+                acc += sum * scale;
+            else
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    acc[t] = add_by_parts(acc[t], sum[t], sa_at[u], sb_at[u][SQUARE ? 0 : t]);
         }
     }
     sums[wave][lane] = acc;

@@ -493,3 +493,91 @@ def test_training_step_of_a_layer():
             size = (wide["dy"][i % m].abs() * old["wt"][j].abs()).sum()
             assert abs((loss[1] - loss[0]) / 2 - got["dx"][i % m, j]) <= (
                 2.0 ** -8 * abs(got["dx"][i % m, j]) * 1.01 + (7 * 2.0 ** -13 + 200 * 2.0 ** -24) * size + 1e-12)
+
+
+# --------------------------------------------------------------- scales of every size
+
+# few rows, in one split and in several; tiles of 64 (direct and unaligned, in splits), 128 and 256
+ANY_SCALE = [(3, 140, 600), (1, 1024, 14336), (100, 300, 1999), (300, 300, 512), (33, 2048, 7168),
+             (1000, 4000, 512), (1000, 4000, 527), (2000, 8100, 1168)]
+
+
+def check_any_scale(got, a, sa, b, sb):
+    """As check_on_gpu, and what subnormal numbers add: half of 2^-149 for a block's product and for its
+    addition, half of 2^-133 for a result in bfloat16."""
+    wa, wb = wide_gpu(a, sa), wide_gpu(b, sb)
+    want, total = wa @ wb.t().contiguous(), wa.abs() @ wb.abs().t().contiguous()
+    bound = (128 + fo.blocks(a.shape[1]) + 4) * 2.0 ** -24 * total + fo.blocks(a.shape[1]) * 2.0 ** -149
+    if got.dtype == torch.bfloat16:
+        bound = bound + 7 * 2.0 ** -13 * total
+        bound = bound + 2.0 ** -8 * (want.abs() + bound) + 2.0 ** -134
+    else:
+        bound = bound + 2.0 ** -24 * want.abs()
+    err = (got.double() - want).abs()
+    assert (err <= bound).all(), ((err / bound).max().item(), torch.isnan(got).sum().item())
+
+
+@pytest.mark.parametrize("m,n,k", ANY_SCALE)
+@pytest.mark.parametrize("blocks", ["square", "row"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_products_of_scales_of_every_size(m, n, k, blocks, out):
+    """Both operands small or large, and rows and blocks of a that are, beside ordinary ones,
+    whose results keep their bits."""
+    fa, fb = ("e4m3", "e4m3") if out == "bf16" else ("e5m2", "e4m3")
+    a, sa = big_operand(m, k, fa, "row", 1, 0)
+    b, sb = big_operand(n, k, fb, blocks, 2, 0)
+    plain = torch.zeros(m, n, dtype=DT[out], device="cuda")
+    nsf.muon_fp8_matmul(a, sa, b, sb, plain)
+    for ea, eb in ((-62, -62), (-58, -70), (-110, -10), (-10, -110), (-100, 30), (50, 45), (-126, 100)):
+        say("scales", m, n, k, blocks, out, ea, eb)
+        c = torch.full((m, n), 7.0, dtype=DT[out], device="cuda")
+        ta, tb = sa * 2.0 ** ea, sb * 2.0 ** eb
+        nsf.muon_fp8_matmul(a, ta, b, tb, c)
+        check_any_scale(c, a, ta, b, tb)
+    say("scales, one row", m, n, k, blocks, out)
+    c = torch.full((m, n), 7.0, dtype=DT[out], device="cuda")
+    ta, tb = sa.clone(), sb.clone()
+    ta[m // 2] *= 2.0 ** -110
+    tb[:, -1] *= 2.0 ** -24
+    nsf.muon_fp8_matmul(a, sa, b, tb, plain)
+    nsf.muon_fp8_matmul(a, ta, b, tb, c)
+    check_any_scale(c, a, ta, b, tb)
+    rest = [i for i in range(m) if i != m // 2]
+    assert torch.equal(c[rest], plain[rest])
+
+
+@pytest.mark.parametrize("m,n,k", ANY_SCALE)
+@pytest.mark.parametrize("blocks", ["square", "row"])
+def test_large_scales_of_blocks_that_do_not_meet(m, n, k, blocks):
+    """Two scales whose product is infinite, of a block whose codes never meet: zero, not NaN."""
+    say("large scales", m, n, k, blocks)
+    a, sa = big_operand(m, k, "e4m3", "row", 1, 0)
+    b, sb = big_operand(n, k, "e4m3", blocks, 2, 0)
+    a.view(torch.uint8)[:, 128:192] = 0
+    b.view(torch.uint8)[:, 192:256] = 0
+    ta, tb = sa.clone(), sb.clone()
+    ta[:, 1], tb[:, 1] = 2.0 ** 65, 2.0 ** 66
+    for out in ("f32", "bf16"):
+        want, c = (torch.full((m, n), 7.0, dtype=DT[out], device="cuda") for _ in range(2))
+        nsf.muon_fp8_matmul(a, sa, b, sb, want)
+        nsf.muon_fp8_matmul(a, ta, b, tb, c)
+        assert torch.equal(c, want)
+
+
+@pytest.mark.parametrize("m,n,k", ANY_SCALE)
+@pytest.mark.parametrize("blocks", ["square", "row"])
+def test_rows_of_zeros(m, n, k, blocks):
+    """Padding of a and small blocks of b: products of their scales are subnormal, sums zero."""
+    say("zero rows", m, n, k, blocks)
+    for out in ("f32", "bf16"):
+        x = torch.randn(m, k, device="cuda")
+        x[m // 2:] = 0
+        a = torch.empty(m, k, dtype=TYPES["e4m3"], device="cuda")
+        sa = nsf.fp8_scales(m, k, "row", "cuda")
+        nsf.muon_fp8_cast(x, a, sa)
+        b, sb = big_operand(n, k, "e4m3", blocks, 2, 0)
+        sb *= 2.0 ** -30
+        c = torch.full((m, n), 7.0, dtype=DT[out], device="cuda")
+        nsf.muon_fp8_matmul(a, sa, b, sb, c)
+        check_any_scale(c, a, sa, b, sb)
+        assert (c[m // 2:] == 0).all()
