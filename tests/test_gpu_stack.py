@@ -422,3 +422,29 @@ def test_largest_finite_matrices(count, rows, cols, dtype):
             else:
                 tol = 2e-6 + 8 * torch.linalg.norm(reference(x[k], steps, 22) * scale - want) / torch.linalg.norm(want)
                 assert torch.linalg.norm(err) <= tol * torch.linalg.norm(want)
+
+
+# Every way in which a stage is divided among workgroups: tiles of 64, 128 and 256, a workgroup a tile, and K
+# steps shared by more or by fewer workgroups than there are tiles (test_stack_scale.py holds the list
+# to that); ragged sides, tall and wide
+EVERY_TILING = [(1, 131, 132), (84, 237, 201), (39, 989, 648), (1, 2832, 2940), (1, 2026, 2321), (1, 5034, 3274),
+                (1, 3274, 5034), (2, 129, 2756), (3, 3231, 3201), (1, 3396, 2414)]
+
+
+@pytest.mark.parametrize("count,rows,cols", EVERY_TILING)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_every_tiling(count, rows, cols, out):
+    say("tiling", count, rows, cols, out)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = 1e-3 * torch.randn(count, rows, cols, generator=g, device="cuda")
+    o, again = (torch.full((count, rows, cols), 7.0, dtype=DT[out], device="cuda") for _ in range(2))
+    ws = torch.full((nsf.muon_stack_workspace_bytes(x),), 0xFF, dtype=torch.uint8, device="cuda")
+    nsf.muon_orthogonalize_stack(x, o, workspace=ws)
+    nsf.muon_orthogonalize_stack(x, again, workspace=ws)
+    assert torch.equal(o, again)
+    for k in {0, count - 1}:
+        want = reference(x[k], nsf.QUINTIC)
+        tol = 2e-6 + 8 * torch.linalg.norm(reference(x[k], nsf.QUINTIC, 22) - want) / torch.linalg.norm(want)
+        tol += 2.0 ** -8 if out == "bf16" else 0
+        want = want * max(1.0, rows / cols) ** 0.5
+        assert torch.linalg.norm(o[k].double() - want) <= tol * torch.linalg.norm(want)
