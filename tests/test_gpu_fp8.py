@@ -581,3 +581,80 @@ def test_rows_of_zeros(m, n, k, blocks):
         nsf.muon_fp8_matmul(a, sa, b, sb, c)
         check_any_scale(c, a, sa, b, sb)
         assert (c[m // 2:] == 0).all()
+
+
+# up to 16 rows with k in several splits
+FEW_SPLIT = [(1, 1024, 14336), (16, 2047, 7169), (5, 100, 20000)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW_SPLIT)
+@pytest.mark.parametrize("blocks", ["square", "row"])
+def test_few_rows_in_splits(m, n, k, blocks):
+    assert nsf.muon_fp8_workspace_bytes(m, n, k) > 0
+    for fa, fb, out, add in (("e4m3", "e4m3", "bf16", False), ("e5m2", "e4m3", "f32", True),
+                             ("e4m3", "e5m2", "f32", False), ("e5m2", "e5m2", "bf16", False)):
+        say("few rows in splits", m, n, k, blocks, fa, fb, out, add)
+        a, sa = big_operand(m, k, fa, "row", 1, 0)
+        b, sb = big_operand(n, k, fb, blocks, 2, 0)
+        held = torch.full((m, n + 3), 0.5, dtype=DT[out], device="cuda")
+        c = held[:, :n]
+        before = c.clone() if add else None
+        ws = torch.full((nsf.muon_fp8_workspace_bytes(m, n, k),), 0xFF, dtype=torch.uint8, device="cuda")
+        nsf.muon_fp8_matmul(a, sa, b, sb, c, accumulate=add, workspace=ws)
+        check_on_gpu(c, a, sa, b, sb, before)
+        assert (held[:, n:] == 0.5).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 140, 600), (1, 1024, 14336), (100, 300, 1999), (300, 300, 512),
+                                   (512, 384, 8192), (1000, 4000, 512), (2000, 8100, 1168)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+def test_nan_and_infinities_of_either_kind(m, n, k, out, fa, fb):
+    """A NaN code, an infinite one (5 exponent bits have them) and scales that are NaN or infinite
+    reach the results of their row of a or of b and no others."""
+    a, sa = big_operand(m, k, fa, "row", 5, 0)
+    b, sb = big_operand(n, k, fb, "row", 6, 0)
+    clean = torch.zeros(m, n, dtype=DT[out], device="cuda")
+    nsf.muon_fp8_matmul(a, sa, b, sb, clean)
+    i, j = m - 1, 100
+
+    def run(what, change_a=None, change_b=None, scale_a=None, scale_b=None):
+        say("nan and infinities", m, n, k, out, fa, fb, what)
+        ta, tsa, tb, tsb = a.clone(), sa.clone(), b.clone(), sb.clone()
+        if change_a is not None:
+            ta.view(torch.uint8)[i, k // 2] = change_a
+        if change_b is not None:
+            tb.view(torch.uint8)[j, k - 1] = change_b
+        if scale_a is not None:
+            tsa[i, 1] = scale_a
+        if scale_b is not None:
+            tsb[j, 2] = scale_b
+        c = torch.full((m, n), 7.0, dtype=DT[out], device="cuda")
+        nsf.muon_fp8_matmul(ta, tsa, tb, tsb, c)
+        of_a, of_b = change_a is not None or scale_a is not None, change_b is not None or scale_b is not None
+        rest = torch.ones(m, n, dtype=torch.bool, device="cuda")
+        if of_a:
+            rest[i] = False
+        if of_b:
+            rest[:, j] = False
+        assert torch.equal(c[rest], clean[rest])
+        assert not torch.isfinite(c[~rest]).any()
+        return c, ta, tb
+
+    for nan in (0x7F, 0xFF):
+        c, _, _ = run("codes %x" % nan, nan, nan)
+        assert torch.isnan(c[i]).all() and torch.isnan(c[:, j]).all()
+    c, _, _ = run("scales", scale_a=float("nan"), scale_b=float("nan"))
+    assert torch.isnan(c[i]).all() and torch.isnan(c[:, j]).all()
+    run("infinite scales", scale_a=float("inf"))
+    run("infinite scales", scale_b=float("-inf"))
+    for code, sign in ((0x7C, 1.0), (0xFC, -1.0)):
+        if fa == "e5m2":
+            # infinity times a code: of its sign, and no number where that is zero
+            c, _, _ = run("a %x" % code, change_a=code)
+            assert torch.equal(torch.nan_to_num(c[i].float(), nan=0.0),
+                               torch.nan_to_num(sign * float("inf") * b[:, k // 2].float(), nan=0.0))
+        if fb == "e5m2":
+            c, _, _ = run("b %x" % code, change_b=code)
+            assert torch.equal(torch.nan_to_num(c[:, j].float(), nan=0.0),
+                               torch.nan_to_num(sign * float("inf") * a[:, k - 1].float(), nan=0.0))
