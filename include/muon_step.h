@@ -432,10 +432,11 @@ enum { MUON_FP8_E4M3 = 0, MUON_FP8_E5M2 = 1 };
  * scale_col].
  *   rows, cols   0..2^24, rows * cols <= 2^34
  *   block_rows   1 or 128
- *   row_stride   bytes between rows, >= cols; any alignment (products run
+ *   row_stride   bytes between rows, cols..2^26; any alignment (products run
  *                fastest where codes, row_stride and cols are multiples of 16)
- *   scale_row, scale_col  elements between the scales of adjacent blocks, none
- *                overlapping another; products read fastest with scale_row = 1 */
+ *   scale_row, scale_col  elements between the scales of adjacent blocks, 1..2^32,
+ *                none overlapping another; products read fastest with scale_row = 1
+ * (A stride counts where there is more than one row, or block, to step to.) */
 typedef struct muon_fp8 {
     void* codes;
     float* scales;
@@ -447,8 +448,8 @@ typedef struct muon_fp8 {
 } muon_fp8_t;
 
 /* A matrix into 8 bits: out, out_t or both (either may be NULL) receive x
- * (rows x cols of dtype, row_stride elements between rows) and its transpose, each
- * in its own blocks.  For each block
+ * (rows x cols of dtype, row_stride elements between rows, cols..2^26) and its
+ * transpose, each in its own blocks.  For each block
  *   m = max(largest magnitude, 2^-100),  s = fl(m / L)     L = 448 or 57344
  *   code = x L / m rounded to nearest, to even in the middle (once)
  * A block that holds a NaN gets the scale NaN, one that holds an infinity an
@@ -463,7 +464,7 @@ int muon_fp8_cast(const void* x, int dtype, int64_t rows, int64_t cols, int64_t 
 int muon_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* out_bytes);
 
 /* out = a b^T, or out += a b^T: a is m x k, b is n x k, out m x n of out_dtype
- * with out_row_stride elements between rows.  Sums over a block of 128 along k
+ * with out_row_stride elements between rows (n..2^26), m n <= 2^36.  Sums over a block of 128 along k
  * are float32, as is the sum of these times their two scales, whatever the sizes
  * of the two (where their product alone is no normal float32, and codes are not
  * zero, a product takes 10 to 20 times as long); the result is
@@ -501,8 +502,8 @@ typedef struct muon_stack {
     const void* in;
     void* out;
     int64_t count, rows, cols; /* count 0..2^20, sides 1..2^20, rows * cols <= 2^31 */
-    int64_t in_stride, in_row; /* elements; in_row >= cols, in_stride any that is not negative */
-    int64_t out_stride, out_row;
+    int64_t in_stride, in_row; /* elements; in_row cols..2^31, in_stride 0..2^40 */
+    int64_t out_stride, out_row; /* likewise */
     int32_t in_dtype, out_dtype;
 } muon_stack_t;
 
@@ -514,8 +515,8 @@ typedef struct muon_stack {
 int muon_stack_workspace_bytes(const muon_stack_t* stack, size_t* out_bytes);
 
 /*   coefficients  host, 3 * n_steps float32: (a, b, c) of every step.  Finite, and such
- *                 that the bound on the largest singular value, which starts at 1
- *                 and is worked out from them, stays below 2^24.
+ *                 that the bound s on the largest singular value, which starts at 1
+ *                 and is worked out from them, and |a| + |b| s^2 + |c| s^4 stay below 2^24.
  *   n_steps       0..64;  scale  finite
  * in and out must not overlap (spans from first to last element); the matrices of
  * in may overlap each other, those of out may not. */

@@ -969,7 +969,7 @@ def _stack(x, out) -> StackC:
 
 def muon_stack_workspace_bytes(x) -> int:
     """Workspace bytes with which ``muon_orthogonalize_stack`` takes all of ``x`` at once;
-    a ``len(x)``-th part of them is the least."""
+    of a stack, a ``len(x)``-th part of them is the least."""
     stack = _stack(x, None)
     need = ctypes.c_size_t(0)
     check(load_library().muon_stack_workspace_bytes(ctypes.byref(stack), ctypes.byref(need)))

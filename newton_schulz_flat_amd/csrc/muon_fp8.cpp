@@ -16,9 +16,9 @@ int check_sides(int64_t rows, int64_t cols, const char* name, Status* st) {
     return MUON_OK;
 }
 
-// A matrix's last row ends within 2^48 elements of its start.
+// (With rows of up to 2^24 a matrix's last one ends within 2^50 elements of its start.)
 int check_row_stride(int64_t rows, int64_t cols, int64_t stride, const char* name, Status* st) {
-    if (rows > 1 && (stride < cols || stride > (int64_t(1) << 24) * 4))
+    if (rows > 1 && (stride < cols || stride > (int64_t(1) << 26)))
         return fail(st, MUON_ERR_BAD_SHAPE, "%s: row stride %lld is outside [cols = %lld, 2^26]", name,
                     (long long)stride, (long long)cols);
     return MUON_OK;
