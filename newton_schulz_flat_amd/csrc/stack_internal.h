@@ -69,7 +69,7 @@ __host__ __device__ inline float stack_largest(const StackStep& k, float top) {
 // that leaves float32's range the exponent follows from top's.
 __host__ __device__ inline StackScale stack_scale(const StackStep& k, float& top) {
     const int sx = stack_exponent(top, kStackLeastX), sa = 2 * sx - 15;
-    const float gram = top * top, poly = fabsf(k.b) + fabsf(k.c) * gram;
+    const float poly = fabsf(k.b) + fabsf(k.c) * top * top;
     const StackScale s = {int16_t(sx), int16_t(sa), int16_t(sa - (15 - stack_exponent(poly, kStackLeastPoly))), 0};
     top = 1.001f * stack_largest(k, top);
     return s;

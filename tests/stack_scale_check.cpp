@@ -92,6 +92,7 @@ int main() {
         {{1000.f, 0.f, 0.f}, {1e-40f, 0.f, 0.f}, {1.f, 0.f, 0.f}},
         // the iterate shrunk and grown again
         {{1e-5f, 0.f, 0.f}, {1e5f, 0.f, 0.f}, quintic},
+        {{1e-9f, 0.f, 0.f}, {5.f, 0.f, 1e38f}, quintic},
         // an end where the polynomial is nearly zero, with a small last coefficient; coefficients for a shrunk iterate
         {{2.598f, -2.598f, 1e-8f}, {1.5f, -0.5f, 0.f}},
         {{1e-9f, 0.f, 0.f}, {5.f, -20e18f, 16e36f}, quintic},

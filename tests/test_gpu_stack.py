@@ -448,3 +448,21 @@ def test_every_tiling(count, rows, cols, out):
         tol += 2.0 ** -8 if out == "bf16" else 0
         want = want * max(1.0, rows / cols) ** 0.5
         assert torch.linalg.norm(o[k].double() - want) <= tol * torch.linalg.norm(want)
+
+
+@pytest.mark.parametrize("rows,cols", [(24, 60), (100, 700), (200, 150)])
+def test_large_coefficients_for_small_matrices(rows, cols):
+    """c x^5 is nothing beside a x for an iterate of 1e-27, though c alone is large: what the
+    first coefficients leave, within the roundings counted in test_subnormal_matrices."""
+    say("large coefficients", rows, cols)
+    x = stack(2, rows, cols, seed=13, std=1e-27)
+    steps = [(1e-9, 0.0, 0.0), (5.0, 0.0, 1e38), (3.0, -1.0, 0.5)]
+    out = torch.empty_like(x)
+    nsf.muon_orthogonalize_stack(x, out, coefficients=steps, scale=1.0)
+    u = x.double().cpu().numpy()
+    want = u / (np.sqrt((u * u).sum(axis=(1, 2), keepdims=True)) + 1e-7)
+    for a, _, _ in steps:
+        want = want * float(np.float32(a))
+    size = np.sqrt((want * want).sum(axis=(1, 2), keepdims=True))
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= 20 * 2.0 ** -24 * np.abs(want) + 3 * 1.01 * 2.0 ** -39 * size).all()
