@@ -290,7 +290,8 @@ __device__ __forceinline__ bool products_are_normal(const Sizes& s, uint2* met, 
 
 // A wave's MI x NJ tiles of 16 x 16 with their scales by parts, from row m0 of a and n0 of b on, one after the
 // other and straight from memory: what a tile is made of again where products of its scales leave the normal
-// numbers.  Rolled, and a tile at a time: what it holds, the main loop cannot.  It is 10 to 20 times slower
+// numbers.  Rolled, and a tile at a time: what it holds, the main loop cannot (256-tiles with widened codes keep 8
+// bytes in scratch across their loop as it is, unaligned 128-tiles 16).  It is 10 to 20 times slower
 // (8192 x 14336 over 4096 with all scales near 2^-70: 11 ms), for products that are otherwise lost.
 template <int MI, int NJ, int FA, int FB, bool EXACT>
 __device__ __forceinline__ void tiles_by_parts(const ProductArgs& g, int split, int m0, int n0, int first, int last) {
@@ -329,7 +330,7 @@ __device__ __forceinline__ void tiles_by_parts(const ProductArgs& g, int split, 
 // registers, by bytes at the end of a row.  Rows behind the last one read the last.
 // SQUARE: b's blocks are 128 x 128, and a wave's columns (64 or fewer, within 128) share one
 // scale.
-// What bounds it (8192 x 14336 over 4096 into bfloat16, 460 us, 2.1 PFLOP/s at 1.9 GHz): matrix
+// What bounds it (8192 x 14336 over 4096 into bfloat16, 450 to 500 us by machine, 1.9 to 2.1 PFLOP/s): matrix
 // instructions are busy 44% of the cycles, the vector unit 41%, with little of one beside the other. Of 470 us,
 // 395 were left without the scaling, 313 without the matrix instructions, 395 without loads.
 template <int TILE, bool DIRECT, int FA, int FB, bool EXACT, bool SQUARE>

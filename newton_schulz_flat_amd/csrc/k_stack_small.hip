@@ -2,7 +2,7 @@
 //
 // stack_whole: matrices that fit a CU's LDS (shorter side up to 64).  One workgroup and one
 // launch a matrix: norm, split, all iterations and the result, X and A and B in LDS.  Bound by the
-// latency of 15 products that follow each other: 16 matrices of 48 x 64 take 18.5 us, 512 of 64 x 64 42.
+// latency of 15 products that follow each other: 16 matrices of 48 x 64 take 18.1 us, 512 of 64 x 64 42.
 //
 // stack_strip and stack_poly: shorter side up to 128.  B (r x r) is small, so one pass over X
 // makes the next iterate and its Gram matrix at once: a workgroup takes strips of 64
