@@ -658,3 +658,48 @@ def test_nan_and_infinities_of_either_kind(m, n, k, out, fa, fb):
             c, _, _ = run("b %x" % code, change_b=code)
             assert torch.equal(torch.nan_to_num(c[:, j].float(), nan=0.0),
                                torch.nan_to_num(sign * float("inf") * a[:, k - 1].float(), nan=0.0))
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 140, 600), (100, 300, 1999), (512, 384, 8192), (2000, 8100, 1168)])
+def test_scales_of_every_size_accumulated_and_replayed(m, n, k):
+    """One captured call, replayed with ordinary, small and subnormal scales and NaN among them,
+    each added into out."""
+    say("scales replayed", m, n, k)
+    a, sa = big_operand(m, k, "e5m2", "row", 1, 0)
+    b, sb = big_operand(n, k, "e4m3", "row", 2, 0)
+    ta, tb, out = sa.clone(), sb.clone(), torch.zeros(m, n, device="cuda")
+    ws = torch.empty(max(256, nsf.muon_fp8_workspace_bytes(m, n, k)), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nsf.muon_fp8_matmul(a, ta, b, tb, out, accumulate=True, workspace=ws)
+    before = torch.randn(m, n, device="cuda")
+    for ea, eb in ((0, 0), (-62, -55), (-128, 10), (-128, -3), (0, 0)):
+        ta.copy_(sa * 2.0 ** ea)
+        tb.copy_(sb * 2.0 ** eb)
+        start = before * 2.0 ** (ea + eb)
+        out.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        wa, wb = wide_gpu(a, ta), wide_gpu(b, tb)
+        want = wa @ wb.t().contiguous() + start.double()
+        total = wa.abs() @ wb.abs().t().contiguous()
+        bound = (128 + fo.blocks(k) + 4) * 2.0 ** -24 * total + fo.blocks(k) * 2.0 ** -149 + 2.0 ** -23 * want.abs()
+        assert ((got.double() - want).abs() <= bound).all()
+        out.copy_(start)
+        nsf.muon_fp8_matmul(a, ta, b, tb, out, accumulate=True, workspace=ws)
+        assert torch.equal(out, got)
+    # a NaN beside small scales: in its row, the others as without it
+    ta.copy_(sa * 2.0 ** -62)
+    tb.copy_(sb * 2.0 ** -62)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    ta[m // 2, 1] = float("nan")
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.isnan(out[m // 2]).all()
+    rest = torch.arange(m, device="cuda") != m // 2
+    assert torch.equal(out[rest], got[rest])
